@@ -277,6 +277,156 @@ int moe_ffn_nvfp4(const moe_dims* dims, const uint16_t* x, const float* topk_wei
                   const uint8_t* w2, const uint8_t* w2_s, const float* w2_gs, uint16_t* y,
                   const moe_debug* dbg, void* ws, size_t ws_bytes, void* stream);
 
+/* moe_ffn for activations that are quantized already (by moe_add_norm or
+ * moe_quant_act): x_q [T, H] E4M3 codes and x_s [T, H/128] E8M0 scales in place of
+ * x, everything else as moe_ffn, and bit for bit its result where the codes are
+ * moe_quant_act's. No quantizer is launched; with a shared expert the codes are
+ * expanded to bf16 once. dbg->x_q and dbg->x_s are not written.
+ * Errors: as moe_ffn; MOE_EINVAL also with MOE_FLAG_A16 or MOE_FLAG_NVFP4 (bf16
+ * activations). */
+int moe_ffn_quantized(const moe_dims* dims, const uint8_t* x_q, const uint8_t* x_s, const float* topk_weights,
+                      const int32_t* expert_offsets, const int32_t* sorted_pairs, const int32_t* pair_rows,
+                      const void* plan_ws, const uint8_t* w13, const uint8_t* w13_s, const uint8_t* w2,
+                      const uint8_t* w2_s, const moe_shared* shared, uint16_t* y, const moe_debug* dbg, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * In front of the FFN: the residual add with its norm and quantizer, the dense
+ * product (the router's logits, projections), the router's gate, and for tuning a
+ * router its balance loss; with the gradients of all of them. The conventions at the
+ * top hold; every pointer below must be 16-byte aligned (MOE_EINVAL otherwise), rows
+ * are contiguous, and T or M is at most 2^21 (MOE_EUNSUPPORTED). Sums, norms and
+ * scores are formed in fp32 or better, outputs are rounded once. */
+enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 };
+
+/* Residual add + RMS norm with bf16 and 8-bit outputs:
+ *   h = x + residual,  y = h * weight / sqrt(mean over H of h^2 + eps)
+ *   T, H       T >= 0; H a multiple of 128, at most 16384
+ *   eps        >= 0, finite
+ *   x          [T, H] bf16
+ *   residual   [T, H] bf16, NULL: h = x
+ *   weight     [H] bf16 or fp32 (weight_type)
+ *   h          [T, H] bf16 out, NULL: not written; may be `residual` or x itself
+ *   y          [T, H] bf16 out, NULL: not written; may be x
+ *   x_q, x_s   [T, H] E4M3 codes and [T, H/128] E8M0 scales of y (moe_ffn_quantized's
+ *              operand; the rule of moe_quant_act, applied to y before its rounding to
+ *              bf16), both NULL: not written
+ * A row with infinities or NaN, or with squares that overflow fp32, gives
+ * non-finite or zero outputs in that row alone.
+ * Errors: MOE_EINVAL (also x_q without x_s, or no output), MOE_EUNSUPPORTED, MOE_EHIP. */
+int moe_add_norm(int32_t T, int32_t H, float eps, const uint16_t* x, const uint16_t* residual, const void* weight,
+                 int32_t weight_type, uint16_t* h, uint16_t* y, uint8_t* x_q, uint8_t* x_s, void* stream);
+
+/* Gradient of moe_add_norm from the stored h:
+ *   dx = the gradient of h from y, plus dh; it is x's and the residual's gradient
+ *   dweight = sum over rows of dy * h / sqrt(mean h^2 + eps)
+ *   dy        [T, H] bf16 gradient of y
+ *   h         [T, H] bf16 (x itself where there was no residual)
+ *   dh        [T, H] bf16 gradient that h gets from elsewhere, NULL: none; may be dx
+ *   dx        [T, H] bf16 out; may be dy
+ *   dweight   [H] fp32 out
+ *   ws        at least moe_add_norm_grad_workspace_bytes bytes
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP. */
+size_t moe_add_norm_grad_workspace_bytes(int32_t T, int32_t H);
+int moe_add_norm_grad(int32_t T, int32_t H, float eps, const uint16_t* dy, const uint16_t* h, const void* weight,
+                      int32_t weight_type, const uint16_t* dh, uint16_t* dx, float* dweight, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* Dense product y = act(x w^T + bias) + residual.
+ *   M rows (>= 0), N outputs (1..65536), K inputs (a multiple of 128, at most 65536,
+ *   N * K below 2^31)
+ *   act   one of MOE_ACT_*: relu; silu z / (1 + e^-z); gelu z Phi(z) (the exact one);
+ *         sigmoid
+ *   type  of y and residual (moe_linear) or of dy (moe_linear_grad): MOE_TYPE_* */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_SIGMOID = 4 };
+typedef struct moe_linear_dims {
+  int32_t M, N, K;
+  int32_t act, type;
+} moe_linear_dims;
+
+/*   x [M, K] bf16, w [N, K] bf16, bias [N] fp32 (NULL: none)
+ *   residual [M, N] of `type` (NULL: none; may be y), y [M, N] out
+ *   z [M, N] fp32 out: the values before the activation, which the gradient of an
+ *     activation reads (NULL: not written)
+ *   ws  at least moe_linear_workspace_bytes bytes (0 for many shapes: ws may be NULL)
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP. */
+size_t moe_linear_workspace_bytes(const moe_linear_dims* dims);
+int moe_linear(const moe_linear_dims* dims, const uint16_t* x, const uint16_t* w, const float* bias,
+               const void* residual, void* y, float* z, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_linear: dz = dy * act'(z); dx = dz w, dw = dz^T x, dbias = sum over
+ * rows of dz (the residual's gradient is dy). The products take dz rounded to bf16,
+ * dbias sums it in fp32.
+ *   dy [M, N] of `type`, x and w as in moe_linear, z [M, N] fp32 from moe_linear
+ *   (not read with MOE_ACT_NONE)
+ *   dx [M, K] bf16 out, dw [N, K] bf16 out, dbias [N] fp32 out; any may be NULL
+ *   (not computed); with M == 0, dw and dbias are zero
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP. */
+size_t moe_linear_grad_workspace_bytes(const moe_linear_dims* dims);
+int moe_linear_grad(const moe_linear_dims* dims, const void* dy, const uint16_t* x, const uint16_t* w, const float* z,
+                    uint16_t* dx, uint16_t* dw, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* The router's gate.
+ *   T tokens (>= 0), E experts (1..4096), K picks (1..min(64, E))
+ *   score        MOE_SCORE_*: softmax over the row, sigmoid, or sqrt(softplus)
+ *   renorm       1: the picks' scores are divided by (their sum + 1e-20)
+ *   logits_type  MOE_TYPE_*
+ *   scale        factor of every weight (finite)
+ * A logit of -inf or NaN masks its expert for that token: score 0, never picked. +inf
+ * counts as the largest fp32 value. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1, MOE_SCORE_SQRTSOFTPLUS = 2 };
+typedef struct moe_gate_dims {
+  int32_t T, E, K;
+  int32_t score, renorm, logits_type;
+  float scale;
+} moe_gate_dims;
+
+/* Picks the K experts of the largest score + bias, in descending order, equal ones
+ * by ascending index; the weights come from the scores without the bias.
+ *   logits        [T, E]
+ *   bias          [E] fp32 added to the scores for the choice alone, NULL: none (an
+ *                 expert whose score + bias is -inf or NaN is masked)
+ *   n_valid       [1] int32 on the device, NULL: T. Rows from *n_valid on are padding.
+ *   topk_ids      [T, K] int32 out (moe_plan's input)
+ *   topk_weights  [T, K] fp32 out (moe_ffn's)
+ * Picks that do not exist (a padding row, fewer than K experts left unmasked) get id
+ * -1, which moe_plan drops, and weight 0.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP. */
+int moe_gate(const moe_gate_dims* dims, const void* logits, const float* bias, const int32_t* n_valid,
+             int32_t* topk_ids, float* topk_weights, void* stream);
+
+/* Gradient of the weights with respect to the logits, the picks held fixed.
+ *   topk_ids   [T, K] from moe_gate; ids outside [0, E) count for nothing, an id that
+ *              appears twice counts as two picks
+ *   d_weights  [T, K] fp32 gradient of topk_weights (not read where the id counts for
+ *              nothing)
+ *   add        [T, E] fp32 added to the result (the balance loss's gradient), NULL:
+ *              none; may be d_logits
+ *   d_logits   [T, E] fp32 out, every element written
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP. */
+int moe_gate_grad(const moe_gate_dims* dims, const void* logits, const int32_t* topk_ids, const float* d_weights,
+                  const float* add, float* d_logits, void* stream);
+
+/* The balance loss of a router, per sequence, with its counts and its gradient:
+ *   tokens [off_b, off_{b+1}) are sequence b of n_b tokens; c_be = picks of expert e in
+ *   it; p = softmax(l), or score / sum of the row's scores; P_be = mean of p over the
+ *   sequence; f_be = E c_be / (K n_b)
+ *   loss = alpha / B * sum over b, e of f_be P_be          (an empty sequence adds 0)
+ * The counts are constants of the gradient. scale and renorm are not used.
+ *   logits       [T, E]; a row without any unmasked expert has p = 0
+ *   topk_ids     [T, K]; ids outside [0, E) are not counted
+ *   seq_offsets  [B + 1] int32 on the device, ascending within [0, T]; NULL with B == 1:
+ *                all tokens are one sequence. (With offsets that are not ascending the
+ *                results are unspecified, but nothing outside the buffers is touched.)
+ *   loss [1] fp32 out, counts [B, E] int32 out
+ *   d_logits [T, E] fp32 out: the gradient of the loss; rows in no sequence are zero
+ *   ws  at least moe_balance_loss_workspace_bytes bytes
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED (B * E of 2^31 or more), MOE_EWORKSPACE, MOE_EHIP. */
+size_t moe_balance_loss_workspace_bytes(const moe_gate_dims* dims, int32_t B);
+int moe_balance_loss(const moe_gate_dims* dims, int32_t B, float alpha, const void* logits, const int32_t* topk_ids,
+                     const int32_t* seq_offsets, float* loss, int32_t* counts, float* d_logits, void* ws,
+                     size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* moe_status_string(int code);
 

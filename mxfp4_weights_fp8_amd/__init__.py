@@ -10,6 +10,17 @@ call fails, an exception is raised.
     quant_act(x)                          -> (x_q, x_s)    (moe_quant_act)
     ffn(x, topk_weights, plan, weights)   -> y             (moe_ffn)
     ffn(..., static=True)                 -> y             (moe_ffn_static: no workspace)
+    ffn_quantized(x_q, x_s, ...)          -> y             (moe_ffn_quantized: x quantized already)
+
+In front of the FFN, each with its gradient as an explicit call:
+
+    add_norm(x, weight, residual)         -> h, y, x_q, x_s            (moe_add_norm)
+    add_norm_grad(dy, h, weight)          -> dx, dweight               (moe_add_norm_grad)
+    linear(x, w, bias, act, residual)     -> y                         (moe_linear)
+    linear_grad(dy, x, w)                 -> dx, dw, dbias             (moe_linear_grad)
+    gate(logits, K)                       -> topk_ids, topk_weights    (moe_gate)
+    gate_grad(logits, topk_ids, d_weights) -> d_logits                 (moe_gate_grad)
+    balance_loss(logits, topk_ids, alpha) -> loss, counts, d_logits    (moe_balance_loss)
 """
 
 from __future__ import annotations
@@ -17,7 +28,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -63,6 +74,21 @@ class Debug(ctypes.Structure):
                 ("events", ctypes.POINTER(ctypes.c_void_p))]
 
 
+class LinearDims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("type", ctypes.c_int32)]
+
+
+class GateDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("logits_type", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+#: MOE_TYPE_*, MOE_ACT_* and MOE_SCORE_* by what the functions below take
+TYPES = {torch.bfloat16: 0, torch.float32: 1}
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}
+SCORES = {"softmax": 0, "sigmoid": 1, "sqrtsoftplus": 2}
+
 _lib = None
 
 #: every symbol the header declares, with its ctypes signature
@@ -79,6 +105,24 @@ _SIGNATURES = {
                        ctypes.c_void_p, ctypes.POINTER(Debug), ctypes.c_void_p]),
     "moe_ffn_nvfp4": (ctypes.c_int, [ctypes.POINTER(Dims)] + [ctypes.c_void_p] * 13 + [ctypes.POINTER(Debug),
                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_ffn_quantized": (ctypes.c_int, [ctypes.POINTER(Dims)] + [ctypes.c_void_p] * 11 + [ctypes.POINTER(Shared),
+                          ctypes.c_void_p, ctypes.POINTER(Debug), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_add_norm": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_float] + [ctypes.c_void_p] * 3 +
+                     [ctypes.c_int32] + [ctypes.c_void_p] * 5),
+    "moe_add_norm_grad_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "moe_add_norm_grad": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_float] + [ctypes.c_void_p] * 3 +
+                          [ctypes.c_int32] + [ctypes.c_void_p] * 4 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(LinearDims)]),
+    "moe_linear": (ctypes.c_int, [ctypes.POINTER(LinearDims)] + [ctypes.c_void_p] * 7 +
+                   [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_linear_grad_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(LinearDims)]),
+    "moe_linear_grad": (ctypes.c_int, [ctypes.POINTER(LinearDims)] + [ctypes.c_void_p] * 8 +
+                        [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_gate": (ctypes.c_int, [ctypes.POINTER(GateDims)] + [ctypes.c_void_p] * 6),
+    "moe_gate_grad": (ctypes.c_int, [ctypes.POINTER(GateDims)] + [ctypes.c_void_p] * 6),
+    "moe_balance_loss_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(GateDims), ctypes.c_int32]),
+    "moe_balance_loss": (ctypes.c_int, [ctypes.POINTER(GateDims), ctypes.c_int32, ctypes.c_float] +
+                         [ctypes.c_void_p] * 7 + [ctypes.c_size_t, ctypes.c_void_p]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 
@@ -335,3 +379,277 @@ def ffn(x: torch.Tensor, topk_weights: torch.Tensor, p: Plan, weights: dict, sha
     if debug:
         return y, dbg_t
     return y
+
+
+def ffn_quantized(x_q: torch.Tensor, x_s: torch.Tensor, topk_weights: torch.Tensor, p: Plan, weights: dict,
+                  shared: Optional[dict] = None, ws: Optional[torch.Tensor] = None,
+                  y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_ffn_quantized on the current stream: ffn for activations that are quantized
+    already, x_q [T, H] E4M3 codes and x_s [T, H/128] E8M0 scales (uint8, from add_norm
+    or quant_act). weights, shared, ws and y as in ffn."""
+    d = p.dims
+    T, H, I, E, K, Is = d.T, d.H, d.I, d.E, d.K, d.Is
+    dev = x_q.device
+    _require(x_q, torch.uint8, (T, H), "x_q")
+    _require(x_s, torch.uint8, (T, H // 128), "x_s")
+    _require(topk_weights, torch.float32, (T, K), "topk_weights")
+    if weights.get("layout") != "packed":
+        raise ValueError("moe_ffn reads expert weights in the kernel-native layout: convert them with pack_weights")
+    for name, shape in (("w13", (E, 2 * I, H // 2)), ("w13_s", (E, 2 * I, H // 32)), ("w2", (E, H, I // 2)),
+                        ("w2_s", (E, H, I // 32))):
+        _require(weights[name], torch.uint8, shape, name)
+    sh = None
+    if shared is not None and Is > 0:
+        for name, shape in (("w13s", (2 * Is, H)), ("w13s_s", (2 * Is // 128, H // 128)), ("w2s", (H, Is)),
+                            ("w2s_s", (H // 128, Is // 128))):
+            _require(shared[name], torch.uint8, shape, name)
+        sh = Shared(shared["w13s"].data_ptr(), shared["w13s_s"].data_ptr(), shared["w2s"].data_ptr(),
+                    shared["w2s_s"].data_ptr())
+    if y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    _require(y, torch.bfloat16, (T, H), "y")
+    if ws is None:
+        ws = torch.empty(ffn_workspace_bytes(d), dtype=torch.uint8, device=dev)
+    _enqueue("moe_ffn_quantized", dev, ctypes.byref(d), x_q.data_ptr(), x_s.data_ptr(), topk_weights.data_ptr(),
+             p.expert_offsets.data_ptr(), p.sorted_pairs.data_ptr(), p.pair_rows.data_ptr(), p.ws.data_ptr(),
+             weights["w13"].data_ptr(), weights["w13_s"].data_ptr(), weights["w2"].data_ptr(),
+             weights["w2_s"].data_ptr(), ctypes.byref(sh) if sh is not None else None, y.data_ptr(), None,
+             ws.data_ptr(), ws.numel())
+    return y
+
+
+# ------------------------------------------------------------------ in front of the FFN
+
+def _enqueue(name: str, dev: torch.device, *args):
+    """Call an entry point with the current stream of `dev` as its last argument, with
+    that device current, so that tensors may live on another than the current one."""
+    fn = getattr(_lib or lib(), name)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc != MOE_OK:
+        raise MoEError(rc, name)
+
+
+def _tensor(t, dtype, shape, dev, name):
+    """Checks an argument (None passes) and gives its device address."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} contiguous={t.is_contiguous()} device={t.device}")
+    return t.data_ptr()
+
+
+def _first(t, dims, name):
+    """Checks that the argument that sets sizes and device is a cuda tensor of `dims` dimensions."""
+    if t.dim() != dims or not t.is_cuda:
+        raise ValueError(f"{name}: expected a cuda tensor of {dims} dimensions, got {tuple(t.shape)} on {t.device}")
+    return t.device
+
+
+def _one_of(table, key, name):
+    if key not in table:
+        raise ValueError(f"{name}: {key!r} is none of {sorted(map(str, table))}")
+    return table[key]
+
+
+def _workspace(nbytes, dev, ws):
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: expected contiguous uint8 on {dev}, got {ws.dtype} on {ws.device}")
+    return ws
+
+
+class Normed(NamedTuple):
+    h: torch.Tensor                  # [T, H] bf16 residual stream (x itself without a residual)
+    y: Optional[torch.Tensor]        # [T, H] bf16
+    x_q: Optional[torch.Tensor]      # [T, H] uint8 E4M3 codes of y
+    x_s: Optional[torch.Tensor]      # [T, H/128] uint8 E8M0 scales
+
+
+def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             bf16: bool = True, fp8: bool = True, out: Optional[Normed] = None) -> Normed:
+    """moe_add_norm on the current stream: h = x + residual, y = RMS norm of h times
+    weight, and y's E4M3 codes and E8M0 scales for ffn_quantized. x, residual: bf16
+    [T, H]; weight: bf16 or float32 [H]. bf16 / fp8 choose which forms of y are written
+    (None in the other's place). out: tensors to write (None members are allocated);
+    out.h may be the residual, out.y may be x."""
+    dev = _first(x, 2, "x")
+    shape = x.shape
+    T, H = shape
+    xp = _tensor(x, torch.bfloat16, shape, dev, "x")
+    rp = _tensor(residual, torch.bfloat16, shape, dev, "residual")
+    wt = _one_of(TYPES, weight.dtype, "weight type")
+    wp = _tensor(weight, weight.dtype, (H,), dev, "weight")
+    h, y, q, s = out if out is not None else (None, None, None, None)
+    if residual is None:
+        h, hp = x, None
+    else:
+        h = torch.empty_like(x) if h is None else h
+        hp = _tensor(h, torch.bfloat16, shape, dev, "out.h")
+    if bf16:
+        y = torch.empty_like(x) if y is None else y
+    else:
+        y = None
+    if fp8:
+        q = torch.empty(shape, dtype=torch.uint8, device=dev) if q is None else q
+        s = torch.empty((T, H // 128), dtype=torch.uint8, device=dev) if s is None else s
+    else:
+        q = s = None
+    _enqueue("moe_add_norm", dev, T, H, eps, xp, rp, wp, wt, hp, _tensor(y, torch.bfloat16, shape, dev, "out.y"),
+             _tensor(q, torch.uint8, shape, dev, "out.x_q"), _tensor(s, torch.uint8, (T, H // 128), dev, "out.x_s"))
+    return Normed(h, y, q, s)
+
+
+def add_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                  dh: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                  ws: Optional[torch.Tensor] = None):
+    """moe_add_norm_grad on the current stream. dy: bf16 [T, H] gradient of y; h: bf16
+    [T, H] as add_norm returned it; dh: optional bf16 [T, H] gradient that h has from
+    elsewhere. Returns (dx bf16 [T, H], the gradient of x and of the residual alike;
+    dweight float32 [H]). dx: optional tensor to write (may be dy or dh)."""
+    dev = _first(h, 2, "h")
+    shape = h.shape
+    T, H = shape
+    wt = _one_of(TYPES, weight.dtype, "weight type")
+    if dx is None:
+        dx = torch.empty_like(h)
+    dw = torch.empty(H, dtype=torch.float32, device=dev)
+    ws = _workspace(lib().moe_add_norm_grad_workspace_bytes(T, H), dev, ws)
+    _enqueue("moe_add_norm_grad", dev, T, H, eps, _tensor(dy, torch.bfloat16, shape, dev, "dy"),
+             _tensor(h, torch.bfloat16, shape, dev, "h"), _tensor(weight, weight.dtype, (H,), dev, "weight"), wt,
+             _tensor(dh, torch.bfloat16, shape, dev, "dh"), _tensor(dx, torch.bfloat16, shape, dev, "dx"),
+             dw.data_ptr(), *_ws_args(ws))
+    return dx, dw
+
+
+def _ws_args(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
+           residual: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+           y: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+           ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_linear on the current stream: act(x w^T + bias) + residual. x: bf16 [M, K];
+    w: bf16 [N, K]; bias: float32 [N]; act: a key of ACTS; residual: [M, N] of the
+    output's type; dtype: torch.bfloat16 or torch.float32 (a router's logits). y:
+    optional tensor to write (may be the residual); z: optional float32 [M, N] that
+    receives the values before the activation, for linear_grad."""
+    dev = _first(x, 2, "x")
+    M, K = x.shape
+    _first(w, 2, "w")
+    N = w.shape[0]
+    d = LinearDims(M, N, K, _one_of(ACTS, act, "act"), _one_of(TYPES, dtype, "dtype"))
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype, device=dev)
+    ws = _workspace(lib().moe_linear_workspace_bytes(d), dev, ws)
+    _enqueue("moe_linear", dev, d, _tensor(x, torch.bfloat16, (M, K), dev, "x"),
+             _tensor(w, torch.bfloat16, (N, K), dev, "w"), _tensor(bias, torch.float32, (N,), dev, "bias"),
+             _tensor(residual, dtype, (M, N), dev, "residual"), _tensor(y, dtype, (M, N), dev, "y"),
+             _tensor(z, torch.float32, (M, N), dev, "z"), *_ws_args(ws))
+    return y
+
+
+def linear_grad(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str = "none",
+                z: Optional[torch.Tensor] = None, need=(True, True, True), ws: Optional[torch.Tensor] = None):
+    """moe_linear_grad on the current stream. dy: bf16 or float32 [M, N]; x, w as in
+    linear; z: float32 [M, N] from linear (for an activation). need: which of the
+    results are computed. Returns (dx bf16 [M, K], dw bf16 [N, K], dbias float32 [N]),
+    None where not needed."""
+    dev = _first(x, 2, "x")
+    M, K = x.shape
+    _first(w, 2, "w")
+    N = w.shape[0]
+    d = LinearDims(M, N, K, _one_of(ACTS, act, "act"), _one_of(TYPES, dy.dtype, "dy type"))
+    dx = torch.empty_like(x) if need[0] else None
+    dw = torch.empty_like(w) if need[1] else None
+    db = torch.empty(N, dtype=torch.float32, device=dev) if need[2] else None
+    ws = _workspace(lib().moe_linear_grad_workspace_bytes(d), dev, ws)
+    _enqueue("moe_linear_grad", dev, d, _tensor(dy, dy.dtype, (M, N), dev, "dy"),
+             _tensor(x, torch.bfloat16, (M, K), dev, "x"), _tensor(w, torch.bfloat16, (N, K), dev, "w"),
+             _tensor(z, torch.float32, (M, N), dev, "z"), dx.data_ptr() if need[0] else None,
+             dw.data_ptr() if need[1] else None, db.data_ptr() if need[2] else None, *_ws_args(ws))
+    return dx, dw, db
+
+
+def _gate_dims(logits, K, score, renorm, scale):
+    T, E = logits.shape
+    return GateDims(T, E, K, _one_of(SCORES, score, "score"), 1 if renorm else 0,
+                    _one_of(TYPES, logits.dtype, "logits type"), scale)
+
+
+def gate(logits: torch.Tensor, K: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+         renorm: bool = True, scale: float = 1.0, n_valid: Optional[torch.Tensor] = None,
+         topk_ids: Optional[torch.Tensor] = None, topk_weights: Optional[torch.Tensor] = None):
+    """moe_gate on the current stream. logits: float32 or bf16 [T, E]; score: a key of
+    SCORES; bias: optional float32 [E], added to the scores for the choice alone;
+    n_valid: optional int32 [1] on the device, rows from there on are padding. Returns
+    (topk_ids int32 [T, K], topk_weights float32 [T, K]), ready for plan and ffn; picks
+    that do not exist have id -1 and weight 0."""
+    dev = _first(logits, 2, "logits")
+    T, E = logits.shape
+    d = _gate_dims(logits, K, score, renorm, scale)
+    shape = (T, K)
+    if topk_ids is None:
+        topk_ids = torch.empty(shape, dtype=torch.int32, device=dev)
+    if topk_weights is None:
+        topk_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    _enqueue("moe_gate", dev, d, _tensor(logits, logits.dtype, (T, E), dev, "logits"),
+             _tensor(bias, torch.float32, (E,), dev, "bias"), _tensor(n_valid, torch.int32, (1,), dev, "n_valid"),
+             _tensor(topk_ids, torch.int32, shape, dev, "topk_ids"),
+             _tensor(topk_weights, torch.float32, shape, dev, "topk_weights"))
+    return topk_ids, topk_weights
+
+
+def gate_grad(logits: torch.Tensor, topk_ids: torch.Tensor, d_weights: torch.Tensor, score: str = "softmax",
+              renorm: bool = True, scale: float = 1.0, add: Optional[torch.Tensor] = None,
+              d_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_gate_grad on the current stream: float32 [T, E] gradient of the logits from
+    d_weights float32 [T, K], the gradient of gate's weights, the picks held fixed. add:
+    optional float32 [T, E] added to it (balance_loss's); d_logits: optional tensor to
+    write (may be add)."""
+    dev = _first(logits, 2, "logits")
+    _first(topk_ids, 2, "topk_ids")
+    T, E = logits.shape
+    K = topk_ids.shape[1]
+    d = _gate_dims(logits, K, score, renorm, scale)
+    if d_logits is None:
+        d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+    _enqueue("moe_gate_grad", dev, d, _tensor(logits, logits.dtype, (T, E), dev, "logits"),
+             _tensor(topk_ids, torch.int32, (T, K), dev, "topk_ids"),
+             _tensor(d_weights, torch.float32, (T, K), dev, "d_weights"),
+             _tensor(add, torch.float32, (T, E), dev, "add"),
+             _tensor(d_logits, torch.float32, (T, E), dev, "d_logits"))
+    return d_logits
+
+
+def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, alpha: float, score: str = "softmax",
+                 seq_offsets: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """moe_balance_loss on the current stream. logits: float32 or bf16 [T, E]; topk_ids:
+    int32 [T, K]; seq_offsets: optional int32 [B + 1], sequence b is the tokens from
+    seq_offsets[b] up to seq_offsets[b + 1] (default: one sequence of all tokens).
+    Returns (loss float32 [1], counts int32 [B, E], d_logits float32 [T, E], the
+    gradient of the loss)."""
+    dev = _first(logits, 2, "logits")
+    _first(topk_ids, 2, "topk_ids")
+    T, E = logits.shape
+    K = topk_ids.shape[1]
+    if seq_offsets is not None:
+        _first(seq_offsets, 1, "seq_offsets")
+    B = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    d = _gate_dims(logits, K, score, False, 1.0)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    counts = torch.empty((max(B, 0), E), dtype=torch.int32, device=dev)
+    d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+    ws = _workspace(lib().moe_balance_loss_workspace_bytes(d, B), dev, ws)
+    _enqueue("moe_balance_loss", dev, d, B, alpha, _tensor(logits, logits.dtype, (T, E), dev, "logits"),
+             _tensor(topk_ids, torch.int32, (T, K), dev, "topk_ids"),
+             _tensor(seq_offsets, torch.int32, (B + 1,), dev, "seq_offsets"), loss.data_ptr(), counts.data_ptr(),
+             d_logits.data_ptr(), *_ws_args(ws))
+    return loss, counts, d_logits

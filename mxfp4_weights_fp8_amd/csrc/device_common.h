@@ -66,6 +66,12 @@ __device__ __forceinline__ uint16_t bf16_rne(float f) {
   return (uint16_t)(b >> 16);
 }
 
+// Two floats to bf16 by the hardware conversion (round to nearest even, NaN stays
+// NaN, overflow to infinity), packed low to high.
+__device__ __forceinline__ uint32_t bf16_pack2(float a, float b) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16);
+}
+
 __device__ __forceinline__ float bf16_to_float(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 
 __device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t word, int e) {

@@ -207,4 +207,36 @@ hipError_t launch_combine(const uint16_t* o, const uint8_t* os, const float* top
                           const uint16_t* so, const uint8_t* sos,
                           uint16_t* y, int T, int H, int K, hipStream_t s);
 
+// ---------------------------------------------------------------- around the FFN
+constexpr int kMaxRows = 1 << 21;    // T and M of the operators below (grids and 32-bit offsets inside a tile)
+constexpr int kMaxCols = 1 << 16;    // N and K of the dense product
+// Codes and scales of quantized activations to their values in bf16 [T, H] (x_hat
+// may be null) and n_zero int32 words set to zero: what launch_quant_act leaves
+// beside the codes.
+hipError_t launch_dequant_act(const uint8_t* x_q, const uint8_t* x_s, uint16_t* x_hat, int T, int H, int32_t* zero,
+                              int n_zero, hipStream_t s);
+// Residual add + RMS norm; res, h, y and the pair x_q, x_s are optional.
+hipError_t launch_add_norm(const uint16_t* x, const uint16_t* res, const void* w, bool w_f32, uint16_t* h,
+                           uint16_t* y, uint8_t* x_q, uint8_t* x_s, int T, int H, float eps, hipStream_t s);
+int norm_grad_parts(int T);   // rows of the fp32 workspace [parts, H] of its gradient
+hipError_t launch_add_norm_grad(const uint16_t* dy, const uint16_t* h, const void* w, bool w_f32, const uint16_t* dh,
+                                uint16_t* dx, float* dw, float* parts, int T, int H, float eps, hipStream_t s);
+// out[c] = sum over p of parts[p][c], c < n, in a fixed order.
+hipError_t launch_sum_parts(const float* parts, int n_parts, int n, float* out, hipStream_t s);
+// Dense product and its gradient (linear.h has what the two share).
+size_t linear_parts_bytes(int M, int N, int K);
+hipError_t launch_linear(const moe_linear_dims& d, const uint16_t* x, const uint16_t* w, const float* bias,
+                         const void* res, void* y, float* z, float* parts, hipStream_t s);
+size_t linear_grad_ws_bytes(int M, int N, int K);
+hipError_t launch_linear_grad(const moe_linear_dims& d, const void* dy, const uint16_t* x, const uint16_t* w,
+                              const float* z, uint16_t* dx, uint16_t* dw, float* db, void* ws, hipStream_t s);
+// The router's gate, its gradient and the balance loss.
+hipError_t launch_gate(const moe_gate_dims& d, const void* logits, const float* bias, const int32_t* n_valid,
+                       int32_t* ids, float* w, hipStream_t s);
+hipError_t launch_gate_grad(const moe_gate_dims& d, const void* logits, const int32_t* ids, const float* dw,
+                            const float* add, float* dl, hipStream_t s);
+int balance_parts(const moe_gate_dims& d);   // doubles of its workspace
+hipError_t launch_balance(const moe_gate_dims& d, int B, float alpha, const void* logits, const int32_t* ids,
+                          const int32_t* off, float* loss, int32_t* counts, float* dl, double* parts, hipStream_t s);
+
 }  // namespace moe

@@ -157,18 +157,21 @@ int ffn_args(const moe_dims* dims, const uint16_t* x, const float* topk_weights,
 // The launch sequence of the FFN on a checked argument set and a workspace of at
 // least ffn_ws_layout(d) bytes.
 // w13_gs / w2_gs: NVFP4's per-expert tensor scales (null for MXFP4 weights).
+// given_q / given_s: activations quantized by the caller, in place of x.
 int ffn_enqueue(const moe_dims& d, const uint16_t* x, const float* topk_weights, const int32_t* expert_offsets,
                 const int32_t* sorted_pairs, const int32_t* pair_rows, const void* plan_ws, const uint8_t* w13,
                 const uint8_t* w13_s, const uint8_t* w2, const uint8_t* w2_s, const moe_shared* shared, uint16_t* y,
                 const moe_debug* dbg, void* ws, hipStream_t s, const float* w13_gs = nullptr,
-                const float* w2_gs = nullptr) {
+                const float* w2_gs = nullptr, const uint8_t* given_q = nullptr, const uint8_t* given_s = nullptr) {
   const bool use_shared = shared != nullptr && d.Is > 0;
   FfnWs fw;
   ffn_ws_layout(d, ws, &fw);
   PlanWs pw;
   plan_ws_layout(d, const_cast<void*>(plan_ws), &pw);
-  uint8_t* x_q = dbg && dbg->x_q ? dbg->x_q : fw.x_q;
-  uint8_t* x_s = dbg && dbg->x_s ? dbg->x_s : fw.x_s;
+  uint8_t* own_q = dbg && dbg->x_q ? dbg->x_q : fw.x_q;   // where the quantizer writes
+  uint8_t* own_s = dbg && dbg->x_s ? dbg->x_s : fw.x_s;
+  const uint8_t* x_q = given_q ? given_q : own_q;
+  const uint8_t* x_s = given_q ? given_s : own_s;
   uint8_t* h_q = dbg && dbg->h_q ? dbg->h_q : fw.h_q;
   uint8_t* h_s = dbg && dbg->h_s ? dbg->h_s : fw.h_s;
 
@@ -201,8 +204,11 @@ int ffn_enqueue(const moe_dims& d, const uint16_t* x, const float* topk_weights,
   // launch runs W13, W2 and the combine, with the shared expert ahead of it
   const bool chain = (d.flags & MOE_FLAG_DECODE_CHAIN) && P <= kFoldPairs;
   record(dbg, MOE_EV_START, s);
-  hipError_t err = launch_quant_act(x, x_q, x_s, d.T, d.H, s, use_shared ? fw.x_hat : nullptr,
-                                    chain ? fw.sync : nullptr, chain ? (int)chain_sync_words(d) : 0);
+  uint16_t* x_hat = use_shared ? fw.x_hat : nullptr;
+  int32_t* zero = chain ? fw.sync : nullptr;
+  const int n_zero = chain ? (int)chain_sync_words(d) : 0;
+  hipError_t err = given_q ? launch_dequant_act(x_q, x_s, x_hat, d.T, d.H, zero, n_zero, s)
+                           : launch_quant_act(x, own_q, own_s, d.T, d.H, s, x_hat, zero, n_zero);
   if (err != hipSuccess) return MOE_EHIP;
   record(dbg, MOE_EV_QUANT_DONE, s);
   if (chain) {
@@ -379,6 +385,21 @@ int moe_ffn_static(const moe_dims* dims, const uint16_t* x, const float* topk_we
   // nothing is cleared
   return ffn_enqueue(*dims, x, topk_weights, expert_offsets, sorted_pairs, pair_rows, plan_ws, w13, w13_s, w2, w2_s,
                      shared, y, dbg, ws, (hipStream_t)stream);
+}
+
+int moe_ffn_quantized(const moe_dims* dims, const uint8_t* x_q, const uint8_t* x_s, const float* topk_weights,
+                      const int32_t* expert_offsets, const int32_t* sorted_pairs, const int32_t* pair_rows,
+                      const void* plan_ws, const uint8_t* w13, const uint8_t* w13_s, const uint8_t* w2,
+                      const uint8_t* w2_s, const moe_shared* shared, uint16_t* y, const moe_debug* dbg, void* ws,
+                      size_t ws_bytes, void* stream) {
+  int rc = ffn_args(dims, reinterpret_cast<const uint16_t*>(x_q), topk_weights, expert_offsets, sorted_pairs, pair_rows,
+                    plan_ws, w13, w13_s, w2, w2_s, shared, y);
+  if (rc == MOE_OK && bf16_rows(*dims)) return MOE_EINVAL;   // bf16 activations: not quantized
+  if (rc != MOE_OK || dims->T == 0) return rc;
+  if (!x_s || !ws) return MOE_EINVAL;
+  if (ws_bytes < ffn_ws_layout(*dims, nullptr, nullptr)) return MOE_EWORKSPACE;
+  return ffn_enqueue(*dims, nullptr, topk_weights, expert_offsets, sorted_pairs, pair_rows, plan_ws, w13, w13_s, w2,
+                     w2_s, shared, y, dbg, ws, (hipStream_t)stream, nullptr, nullptr, x_q, x_s);
 }
 
 int moe_ffn_nvfp4(const moe_dims* dims, const uint16_t* x, const float* topk_weights, const int32_t* expert_offsets,

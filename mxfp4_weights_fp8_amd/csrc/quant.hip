@@ -54,7 +54,32 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_act(const uint16_t* __r
   }
 }
 
+// The two by-products of k_quant_act for activations that arrive quantized: the
+// values E4M3(code) * scale as bf16, and counters set to zero.
+__global__ __launch_bounds__(kQuantThreads) void k_dequant_act(const uint8_t* __restrict__ x_q,
+                                                               const uint8_t* __restrict__ x_s,
+                                                               uint16_t* __restrict__ x_hat,
+                                                               int32_t* __restrict__ zero, int n_zero, int64_t n8) {
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < n_zero; i += kQuantThreads) zero[i] = 0;
+  const int64_t g = (int64_t)blockIdx.x * kQuantThreads + threadIdx.x;   // 8 codes per thread
+  if (g >= n8) return;
+  const int e = (int)x_s[g / 16] - 127;
+  const uint2 q = *reinterpret_cast<const uint2*>(x_q + g * 8);
+  const uint2 a = e4m3x4_to_bf16(q.x, e), b = e4m3x4_to_bf16(q.y, e);
+  *reinterpret_cast<uint4*>(x_hat + g * 8) = make_uint4(a.x, a.y, b.x, b.y);
+}
+
 }  // namespace
+
+hipError_t launch_dequant_act(const uint8_t* x_q, const uint8_t* x_s, uint16_t* x_hat, int T, int H, int32_t* zero,
+                              int n_zero, hipStream_t s) {
+  const int64_t n8 = x_hat ? (int64_t)T * H / 8 : 0;
+  if (n8 == 0 && n_zero == 0) return hipSuccess;
+  const int64_t ctas = n8 ? ceil_div(n8, kQuantThreads) : 1;
+  hipLaunchKernelGGL(k_dequant_act, dim3((unsigned)ctas), dim3(kQuantThreads), 0, s, x_q, x_s, x_hat, zero, n_zero, n8);
+  return hipGetLastError();
+}
 
 hipError_t launch_quant_act(const uint16_t* x, uint8_t* x_q, uint8_t* x_s, int T, int H, hipStream_t s,
                             uint16_t* x_hat, int32_t* zero, int n_zero) {

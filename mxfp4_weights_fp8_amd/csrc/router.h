@@ -1,0 +1,163 @@
+// What the router's kernels share: scores of the logits, row loads, reductions over
+// the lanes of a row, and the choice of a layout for the number of experts.
+//
+// Layout: LPR lanes per row (16: four rows per wave; or 64), each holding NV groups
+// of four neighbouring experts: expert 4 (j LPR + lane) + i, so a row is read in 16
+// byte (bf16: 8 byte) loads. A logit of -inf or NaN masks its expert (score 0, never
+// picked), +inf counts as the largest float.
+#pragma once
+
+#include <float.h>
+#include <math.h>
+
+#include "device_common.h"
+#include "host_internal.h"
+
+namespace moe {
+
+constexpr int kGateThreads = 256;
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kFarBelow = -20.f;   // softplus(l) = e^l here, to fp32
+constexpr float kNone = -INFINITY;   // a masked expert's logit, or a key that is taken
+
+// e^x, x <= 88: 2^(x log2 e) with the product's rounding error put back (about 1.5
+// ulp; results below 2^-126 are 0).
+__device__ __forceinline__ float exp_f(float x) {
+  x = fmaxf(x, -150.f);   // e^x is 0 there already, and the error term stays finite
+  const float t = x * kLog2e;
+  const float err = __builtin_fmaf(x, kLog2e, -t) + x * 1.925963033e-8f;   // log2 e = kLog2e + 1.92596e-8
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, err * 0.693147181f, e);
+}
+
+// A score as a function of its own logit (softmax: also of the row's largest logit
+// `top` and the sum of e^(l - top)).
+template <int SCORE>
+__device__ __forceinline__ float score_f32(float l, float top, float sum) {
+  if (l == kNone) return 0.f;
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) return expf(l - top) / sum;
+  if constexpr (SCORE == MOE_SCORE_SIGMOID) return 1.f / (1.f + expf(-l));
+  if (l < kFarBelow) return expf(0.5f * l);
+  return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
+}
+
+__device__ __forceinline__ float clean(float l) {   // NaN -> masked, +inf -> largest float
+  l = l == l ? l : kNone;
+  return fminf(l, FLT_MAX);
+}
+
+// Four logits of experts e0 .. e0 + 3 of a row; experts from E on are masked.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load_logits4(const void* row, int e0, int E, float (&v)[4]) {
+  if constexpr (VEC) {   // E % 4 == 0
+    if (e0 < E) {
+      if constexpr (BF16) {
+        const uint2 r = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(row) + e0);
+        v[0] = __uint_as_float(r.x << 16);
+        v[1] = __uint_as_float(r.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(r.y << 16);
+        v[3] = __uint_as_float(r.y & 0xFFFF0000u);
+      } else {
+        const v4f r = *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(row) + e0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = r[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = clean(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = kNone;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = e0 + i;
+      if constexpr (BF16)
+        v[i] = e < E ? clean(bf16_to_float(reinterpret_cast<const uint16_t*>(row)[e])) : kNone;
+      else
+        v[i] = e < E ? clean(reinterpret_cast<const float*>(row)[e]) : kNone;
+    }
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* row, int e) {
+  return clean(BF16 ? bf16_to_float(reinterpret_cast<const uint16_t*>(row)[e])
+                    : reinterpret_cast<const float*>(row)[e]);
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int m = 1; m < LPR; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ double row_max(double v) {
+#pragma unroll
+  for (int m = 1; m < LPR; m <<= 1) v = fmax(v, __shfl_xor(v, m));
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ int row_min(int v) {
+#pragma unroll
+  for (int m = 1; m < LPR; m <<= 1) v = min(v, __shfl_xor(v, m));
+  return v;
+}
+template <int LPR, typename F>
+__device__ __forceinline__ F row_sum(F v) {
+#pragma unroll
+  for (int m = 1; m < LPR; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// d score / d logit, for the scores that depend on their own logit alone.
+template <int SCORE>
+__device__ __forceinline__ float score_slope(float l, float s) {
+  if constexpr (SCORE == MOE_SCORE_SIGMOID) return s * (1.f / (1.f + expf(l)));
+  // sqrt(softplus): sigmoid(l) / (2 s); far below zero s^2 = e^l, so this is s / 2
+  return l < kFarBelow ? 0.5f * s : 1.f / (1.f + expf(-l)) / (2.f * s);
+}
+
+// Calls f with (LPR, NV) as integral constants: 16 lanes per row for at most 512
+// experts (NV 1..8), else 64 lanes (NV up to 16: 4096 experts). `wide`: 64 lanes
+// whatever E.
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+template <typename F>
+void by_experts(int E, bool wide, F f) {
+  if (E <= 512 && !wide) {
+    if (E <= 64) f(Int<16>{}, Int<1>{});
+    else if (E <= 128) f(Int<16>{}, Int<2>{});
+    else if (E <= 256) f(Int<16>{}, Int<4>{});
+    else if (E <= 384) f(Int<16>{}, Int<6>{});
+    else f(Int<16>{}, Int<8>{});
+  } else {
+    if (E <= 512) f(Int<64>{}, Int<2>{});
+    else if (E <= 1024) f(Int<64>{}, Int<4>{});
+    else if (E <= 2048) f(Int<64>{}, Int<8>{});
+    else f(Int<64>{}, Int<16>{});
+  }
+}
+template <typename F>
+void by_score(int score, F f) {
+  if (score == MOE_SCORE_SOFTMAX) f(Int<MOE_SCORE_SOFTMAX>{});
+  else if (score == MOE_SCORE_SIGMOID) f(Int<MOE_SCORE_SIGMOID>{});
+  else f(Int<MOE_SCORE_SQRTSOFTPLUS>{});
+}
+template <typename F>
+void by_layout(bool bf16, bool vec, F f) {
+  if (bf16) {
+    if (vec) f(Int<1>{}, Int<1>{});
+    else f(Int<1>{}, Int<0>{});
+  } else {
+    if (vec) f(Int<0>{}, Int<1>{});
+    else f(Int<0>{}, Int<0>{});
+  }
+}
+
+// 64 lanes per row also where a lane would have more than one pick otherwise
+inline bool wide_rows(const moe_gate_dims& d) { return d.K > 16; }
+
+}  // namespace moe
