@@ -131,8 +131,12 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
   constexpr int kCols = 32 * FW;
   constexpr int kStageA = kCols * 128, kStageB = kTileRows * 128;
   constexpr int kCopies = FW + FT;
-  __shared__ __attribute__((aligned(1024))) uint8_t sA[kBufs][kStageA];
-  __shared__ __attribute__((aligned(1024))) uint8_t sB[kBufs][kStageB];
+  constexpr int kOutRow = kCols + 4;   // floats per row of the staged result: 16 rows apart in distinct banks
+  constexpr int kStages = kBufs * (kStageA + kStageB);
+  static_assert(kTileRows * kOutRow * 4 <= kStages, "the result tile fits the stages' LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kStages];
+  uint8_t* const sA = smem;                       // [buf][row][128 B]
+  uint8_t* const sB = smem + kBufs * kStageA;
 
   // Workgroups are dealt to the XCDs in turn; give each XCD a contiguous run of the
   // tile order (split, group of kGroup row tiles, column tile, row tile), so that the
@@ -167,10 +171,10 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
     const bool valid = st < k1;
     const int sw = (i & 1) ? sw1 : sw0;   // FW and FT are even, so i's parity is the row block's
     if (i < FW)
-      dma16(rsrc_sized(rw, valid), lds_addr(&sA[buf][(8 * FW * wave + 8 * i) * 128]), dA + 8 * i * row_bytes + sw + st * 128,
+      dma16(rsrc_sized(rw, valid), lds_addr(sA + buf * kStageA + (8 * FW * wave + 8 * i) * 128), dA + 8 * i * row_bytes + sw + st * 128,
             0);
     else
-      dma16(rsrc_sized(rx, valid), lds_addr(&sB[buf][(8 * FT * wave + 8 * (i - FW)) * 128]),
+      dma16(rsrc_sized(rx, valid), lds_addr(sB + buf * kStageB + (8 * FT * wave + 8 * (i - FW)) * 128),
             dB + 8 * (i - FW) * row_bytes + sw + st * 128, 0);
   };
 
@@ -182,8 +186,8 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
 
   const int off0 = c * 128 + ((q ^ (c >> 1)) << 4);
   const int off1 = c * 128 + (((4 + q) ^ (c >> 1)) << 4);
-  const uint8_t* pA = &sA[0][0] + wn * FW * 2048;
-  const uint8_t* pB = &sB[0][0] + wm * FT * 2048;
+  const uint8_t* pA = sA + wn * FW * 2048;
+  const uint8_t* pB = sB + wm * FT * 2048;
   struct Ops {
     v4i w[FW][2];
     v4i x[FT][2];
@@ -236,25 +240,34 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
     step(opsA, opsB, k);
     step(opsB, opsA, k + 1);
   }
-  wait_vmcnt<0>();   // no copy may be in flight when the workgroup's LDS is given away
+  wait_vmcnt<0>();   // no copy may land in the result tile
+  __syncthreads();
 
+  // The tile goes through LDS, so that a wave's epilogue walks whole rows: 64 lanes
+  // hold 256 neighbouring columns' sums of one row, or 128 of two.
+  float* const out = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int j = 0; j < FT; ++j) {
-    const int64_t m = m0 + 64 * wm + 16 * j + c;
+  for (int j = 0; j < FT; ++j)
 #pragma unroll
-    for (int i = 0; i < FW; ++i) {
-      const int n = n0 + 16 * FW * wn + 16 * i + 4 * q;
-      if (a.splits == 1) {
-        finish4(a, m, n, acc[i][j]);
-      } else if (m < a.M && n < a.N) {
-        float* dst = a.parts + ((int64_t)split * a.M + m) * a.N + n;
-        if (a.N % 4 == 0) {
-          *reinterpret_cast<v4f*>(dst) = acc[i][j];
-        } else {
+    for (int i = 0; i < FW; ++i)
+      *reinterpret_cast<v4f*>(out + (64 * wm + 16 * j + c) * kOutRow + 16 * FW * wn + 16 * i + 4 * q) = acc[i][j];
+  __syncthreads();
+  constexpr int kGroups = kCols / 4;
+#pragma unroll 1
+  for (int g = tid; g < kTileRows * kGroups; g += kTileThreads) {
+    const int r = g / kGroups, n = n0 + 4 * (g % kGroups);
+    const int64_t m = m0 + r;
+    const v4f v = *reinterpret_cast<const v4f*>(out + r * kOutRow + 4 * (g % kGroups));
+    if (a.splits == 1) {
+      finish4(a, m, n, v);
+    } else if (m < a.M && n < a.N) {
+      float* dst = a.parts + ((int64_t)split * a.M + m) * a.N + n;
+      if (a.N % 4 == 0) {
+        *reinterpret_cast<v4f*>(dst) = v;
+      } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < a.N) dst[r] = acc[i][j][r];
-        }
+        for (int k = 0; k < 4; ++k)
+          if (n + k < a.N) dst[k] = v[k];
       }
     }
   }
