@@ -4,65 +4,54 @@
 //   w_j = scale * s_j / (sum of the picked s + 1e-20)  (or scale * s_j)
 //
 // Order of the picks. Every score rises with its logit, so without a bias the
-// logits themselves are compared, which is exact. With one, the keys s + b are
-// formed in fp32 from fast functions together with a bound on their error; where
-// two neighbours among the K + 1 best lie within the bound, the row is selected
-// again from keys in fp64. Equal keys go to the lowest index.
+// logits themselves are compared, which is exact. With one, keys s + b are formed in
+// fp32 with the hardware's fast functions, each off by at most half of `slack`. All
+// experts whose key is within `slack` of the K-th best one are taken as candidates
+// (a true pick cannot be further away), and where two neighbours in their order are
+// within it too, the candidates are ranked again by fp64 keys: one fp64 score per
+// lane. Where there are more candidates than lanes (many equal keys) the whole row
+// is selected in fp64. Equal keys go to the lowest index.
 //
-// A selection round is a maximum over the lane's values, a butterfly over the row's
-// lanes, and the same for the lowest index that holds the maximum.
+// Selection. The keys, as integers of the same order, lie in LDS in the lane's groups
+// of four, each group's maximum in a register. A round is the maximum over the
+// lane's groups, a DPP reduction over the row's lanes, the lowest index that holds
+// it (group by group, then in the one group read back), and one group rewritten:
+// about 50 instructions instead of the 120 of scanning 24 keys in registers.
 #include "router.h"
 
 namespace moe {
 namespace {
 
-// log(1 + e), 0 <= e <= 1, relative error about 1e-7 for small e (series) and e
-// near 1 (logarithm), at most 7e-6 in between
-__device__ __forceinline__ float log1p_fast(float e) {
+constexpr int kNoKey = -0x7FFFFFFF - 1;   // a masked expert, or a key that is taken
+constexpr int kNoIndex = 0x7FFFFFFF;
+
+// Floats as integers of the same order (-0 counts as 0).
+__device__ __forceinline__ int to_key(float f) {
+  const int b = __float_as_int(f + 0.f);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float from_key(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)); }
+
+// Scores from the hardware's exp2, log2, rcp and sqrt (1 ulp each): the product
+// l log2(e) is off by 2^-24 of itself, at most 127 * 2^-24 where e^l is not out of
+// range, so e^l is off by at most 6e-6 of itself, and 1 + e^l, its reciprocal, its
+// logarithm (from a series where e^l is below 0.01: at most 7e-6 of log(1 + e^l))
+// and its root by no more. Results below 2^-126 are 0 (1e-19 after the root).
+constexpr float kSlack = 1.5e-5f;   // twice that, relative to score + |bias|
+template <int SCORE>
+__device__ __forceinline__ float score_fast(float l) {
+  if constexpr (SCORE == MOE_SCORE_SIGMOID)
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l * -kLog2e));
+  const float e = __builtin_amdgcn_exp2f(fabsf(l) * -kLog2e);
   const float series = e * (1.f - e * (0.5f - e * 0.333333333f));
   const float full = __builtin_amdgcn_logf(1.f + e) * 0.693147181f;
-  return e < 0.01f ? series : full;
-}
-
-// A score as a function of its own logit (softmax: e^l relative to the row).
-template <int SCORE>
-__device__ __forceinline__ float score_fast(float l, float top, float inv_sum) {
-  if (l == kNone) return 0.f;
-  if constexpr (SCORE == MOE_SCORE_SOFTMAX) return exp_f(l - top) * inv_sum;
-  if constexpr (SCORE == MOE_SCORE_SIGMOID) return __builtin_amdgcn_rcpf(1.f + exp_f(fminf(-l, 88.f)));
-  return __builtin_amdgcn_sqrtf(fmaxf(l, 0.f) + log1p_fast(exp_f(-fabsf(l))));
+  return __builtin_amdgcn_sqrtf(fmaxf(l, 0.f) + (e < 0.01f ? series : full));
 }
 template <int SCORE>
 __device__ __forceinline__ double score_f64(double l, double top, double inv_sum) {
   if constexpr (SCORE == MOE_SCORE_SOFTMAX) return exp(l - top) * inv_sum;
   if constexpr (SCORE == MOE_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-l));
   return sqrt(fmax(l, 0.0) + log1p(exp(-fabs(l))));
-}
-
-constexpr int kNoIndex = 0x7FFFFFFF;
-
-// The largest key of the row, its lowest index (kNoIndex if every key is -inf),
-// and that key removed.
-template <int LPR, int NV, typename F>
-__device__ __forceinline__ F take_best(F (&key)[NV][4], int lane, int& index) {
-  F best = key[0][0];
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) best = key[j][i] > best ? key[j][i] : best;
-  best = row_max<LPR>(best);
-  int at = kNoIndex;
-#pragma unroll
-  for (int j = NV - 1; j >= 0; --j)
-#pragma unroll
-    for (int i = 3; i >= 0; --i) at = key[j][i] == best ? 4 * (j * LPR + lane) + i : at;
-  at = row_min<LPR>(at);
-  index = best == (F)kNone ? kNoIndex : at;
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) key[j][i] = 4 * (j * LPR + lane) + i == at ? (F)kNone : key[j][i];
-  return best;
 }
 
 struct GateArgs {
@@ -76,12 +65,21 @@ struct GateArgs {
   float scale;
 };
 
+// fp64 key of expert e, minus infinity where it is masked
+template <int SCORE, bool BF16>
+__device__ __forceinline__ double key_f64(const GateArgs& a, const char* row, int e, double top, double inv_sum) {
+  const float l = load_logit<BF16>(row, e);
+  if (l == kNone) return -INFINITY;
+  const double k = score_f64<SCORE>(l, top, inv_sum) + (double)a.bias[e];
+  return k == k ? k : -INFINITY;
+}
+
 template <int LPR, int NV, int SCORE, bool BF16, bool VEC>
 __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
+  __shared__ v4i groups[NV][kGateThreads];   // a lane reads and writes its own column only
   const int lane = threadIdx.x & (LPR - 1);
   const int64_t t = (int64_t)blockIdx.x * (kGateThreads / LPR) + threadIdx.x / LPR;
-  // every lane of a row's group leaves together; the others keep their butterflies
-  // inside their own group
+  // every lane of a row leaves together; reductions stay inside a row
   if (t >= a.T) return;
   int32_t* ids = a.ids + t * a.K;
   float* w = a.w + t * a.K;
@@ -97,8 +95,9 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) load_logits4<BF16, VEC>(row, 4 * (j * LPR + lane), a.E, l[j]);
 
+  // softmax: l becomes e^(l - top), or -1 where masked
   float top = kNone, sum = 1.f;
-  if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+  auto softmax = [&]() {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -108,79 +107,167 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum += l[j][i] == kNone ? 0.f : exp_f(l[j][i] - top);
+      for (int i = 0; i < 4; ++i) {
+        const float e = exp_f(l[j][i] - top);
+        sum += l[j][i] == kNone ? 0.f : e;
+        if (a.bias) l[j][i] = l[j][i] == kNone ? -1.f : e;
+      }
     sum = row_sum<LPR>(sum);
-  }
+  };
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) softmax();
 
-  int mine = kNoIndex;   // lane j keeps pick j (K <= LPR)
-  auto keep = [&](int j, int index) { mine = j == lane ? index : mine; };
-  if (!a.bias) {
-    for (int j = 0; j < a.K; ++j) {
-      int index;
-      take_best<LPR, NV>(l, lane, index);
-      keep(j, index);
-    }
-  } else {
+  int best_of[NV];   // largest key of each group
+  float slack = 0.f;
+  if (a.bias) {
     const float inv_sum = 1.f / sum;
-    float key[NV][4];
-    float scale_of_keys = 0.f;
+    float size = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const int e0 = 4 * (j * LPR + lane);
+      v4f bias{0.f, 0.f, 0.f, 0.f};
+      if constexpr (VEC) {
+        if (e0 < a.E) bias = *reinterpret_cast<const v4f*>(a.bias + e0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (e0 + i < a.E) bias[i] = a.bias[e0 + i];
+      }
+      v4i k;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int e = 4 * (j * LPR + lane) + i;
-        const float s = score_fast<SCORE>(l[j][i], top, inv_sum);
-        const float b = e < a.E ? a.bias[e] : 0.f;
-        key[j][i] = l[j][i] == kNone ? kNone : s + b;
-        if (!(key[j][i] == key[j][i])) key[j][i] = kNone;
-        scale_of_keys = key[j][i] == kNone ? scale_of_keys : fmaxf(scale_of_keys, s + fabsf(b));
+        const float b = bias[i];
+        const bool masked = SCORE == MOE_SCORE_SOFTMAX ? l[j][i] < 0.f : l[j][i] == kNone;
+        float s;
+        if constexpr (SCORE == MOE_SCORE_SOFTMAX) s = l[j][i] * inv_sum;
+        else s = score_fast<SCORE>(l[j][i]);
+        const float key = s + b;
+        k[i] = masked || !(key > kNone) ? kNoKey : to_key(key);
+        size = fmaxf(size, k[i] == kNoKey ? 0.f : s + fabsf(b));
       }
-    // each key is off by at most 1e-5 of its score (fast functions) and half an ulp
-    // of the sum; two of them are compared
-    const float slack = 3e-5f * row_max<LPR>(scale_of_keys) + 1e-18f;
-    bool close = false;
-    float before = INFINITY;
-    for (int j = 0; j <= a.K && j < a.E; ++j) {
-      int index;
-      const float best = take_best<LPR, NV>(key, lane, index);
-      close |= best != kNone && !(before - best > slack);
-      before = best;
-      if (j < a.K) keep(j, index);
+      groups[j][threadIdx.x] = k;
+      best_of[j] = max(max(k[0], k[1]), max(k[2], k[3]));
     }
-    if (close) {   // the same in all lanes of the row
-      double dkey[NV][4], dsum = 1.0;
+    slack = kSlack * row_max<LPR>(size) + 1e-18f;
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      v4i k;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k[i] = l[j][i] == kNone ? kNoKey : to_key(l[j][i]);
+      groups[j][threadIdx.x] = k;
+      best_of[j] = max(max(k[0], k[1]), max(k[2], k[3]));
+    }
+  }
+
+  // the row's largest key
+  auto row_best = [&]() {
+    int m = best_of[0];
+#pragma unroll
+    for (int j = 1; j < NV; ++j) m = max(m, best_of[j]);
+    return row_max<LPR>(m);
+  };
+  // the lowest index that holds `best`, which is removed
+  auto take = [&](int best) {
+    int mine = NV;
+#pragma unroll
+    for (int j = NV - 1; j >= 0; --j) mine = best_of[j] == best ? j : mine;
+    const int g = min(mine, NV - 1);
+    v4i k = groups[g][threadIdx.x];
+    int i = 3;
+    i = k[2] == best ? 2 : i;
+    i = k[1] == best ? 1 : i;
+    i = k[0] == best ? 0 : i;
+    const int at = mine < NV ? 4 * (mine * LPR + lane) + i : kNoIndex;
+    const int first = row_min<LPR>(at);
+    if (at == first) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) k[n] = n == i ? kNoKey : k[n];
+      groups[g][threadIdx.x] = k;
+    }
+    const int rest = max(max(k[0], k[1]), max(k[2], k[3]));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) best_of[j] = at == first && j == mine ? rest : best_of[j];
+    return first;
+  };
+
+  int mine = kNoIndex, pos = lane;   // the lane's pick (K <= LPR) and its place
+  if (!a.bias) {
+    for (int j = 0; j < a.K; ++j) {
+      const int best = row_best();
+      const int index = best == kNoKey ? kNoIndex : take(best);
+      mine = j == lane ? index : mine;
+    }
+  } else {
+    bool more = true, close = false;
+    float before = INFINITY, least = kNone;   // the key before, and what a candidate needs from K on
+    for (int j = 0; j < LPR && __any(more); ++j) {
+      const int best = row_best();
+      const float f = best == kNoKey ? kNone : from_key(best);
+      more = more && best != kNoKey && !(f < least);
+      if (!more) continue;   // the same in all lanes of the row
+      close = close || !(before - f > slack);
+      before = f;
+      const int index = take(best);
+      mine = j == lane ? index : mine;
+      if (j == a.K - 1) least = f - slack;
+    }
+    const int left = row_best();
+    const bool crowd = more && left != kNoKey && !(from_key(left) < least);
+    if (close || crowd) {
+      double dtop = top, inv = 1.0;
       if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-        dsum = 0.0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dsum += l[j][i] == kNone ? 0.0 : exp((double)l[j][i] - (double)top);
-        dsum = 1.0 / row_sum<LPR>(dsum);
+        double ds = 0.0;
+#pragma unroll 1
+        for (int g = 0; g < NV; ++g)
+#pragma unroll 1
+          for (int e = 4 * (g * LPR + lane); e < min(4 * (g * LPR + lane) + 4, a.E); ++e)
+            ds += exp((double)load_logit<BF16>(row, e) - dtop);   // masked: exp(-inf) is 0
+        inv = 1.0 / row_sum<LPR>(ds);
       }
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = 4 * (j * LPR + lane) + i;
-          const double b = e < a.E ? (double)a.bias[e] : 0.0;
-          dkey[j][i] = l[j][i] == kNone ? (double)kNone : score_f64<SCORE>(l[j][i], top, dsum) + b;
-          if (!(dkey[j][i] == dkey[j][i])) dkey[j][i] = (double)kNone;
+      if (!crowd) {
+        const double key = mine == kNoIndex ? -INFINITY : key_f64<SCORE, BF16>(a, row, mine, dtop, inv);
+        const int row0 = (threadIdx.x & 63) & ~(LPR - 1);
+        int rank = 0;
+        for (int r = 0; r < LPR; ++r) {
+          const double k = __shfl(key, row0 + r);
+          const int i = __shfl(mine, row0 + r);
+          if (k > key || (k == key && i < mine)) ++rank;
         }
-      for (int j = 0; j < a.K; ++j) {
-        int index;
-        take_best<LPR, NV>(dkey, lane, index);
-        keep(j, index);
+        if (mine != kNoIndex) pos = rank;   // empty lanes come last already
+      } else {
+        double last = INFINITY;
+        int last_at = -1;
+        mine = kNoIndex;
+        for (int j = 0; j < a.K; ++j) {   // the best one after `last` in the order
+          double best = -INFINITY;
+          int at = kNoIndex;
+#pragma unroll 1
+          for (int g = 0; g < NV; ++g)
+#pragma unroll 1
+            for (int e = 4 * (g * LPR + lane); e < min(4 * (g * LPR + lane) + 4, a.E); ++e) {
+              const double k = key_f64<SCORE, BF16>(a, row, e, dtop, inv);
+              if ((k < last || (k == last && e > last_at)) && k > best) {
+                best = k;
+                at = e;
+              }
+            }
+          last = row_max<LPR>(best);
+          last_at = row_min<LPR>(best == last ? at : kNoIndex);
+          mine = j == lane ? last_at : mine;
+          if (last_at == kNoIndex) break;
+        }
       }
     }
   }
 
   // weight of the lane's pick, from its logit again
-  const float s = mine == kNoIndex ? 0.f : score_f32<SCORE>(load_logit<BF16>(row, mine), top, sum);
+  const bool pick = pos < a.K;
+  const float s = !pick || mine == kNoIndex ? 0.f : score_f32<SCORE>(load_logit<BF16>(row, mine), top, sum);
   float mul = a.scale;
   if (a.renorm) mul = a.scale / (row_sum<LPR>(s) + 1e-20f);
-  if (lane < a.K) {
-    ids[lane] = mine == kNoIndex ? -1 : mine;
-    w[lane] = s * mul;
+  if (pick) {
+    ids[pos] = mine == kNoIndex ? -1 : mine;
+    w[pos] = s * mul;
   }
 }
 

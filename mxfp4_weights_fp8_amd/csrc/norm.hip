@@ -230,19 +230,28 @@ void add_norm_grad_by_width(const NormGradArgs& a, int ctas, hipStream_t s) {
   else hipLaunchKernelGGL((k_add_norm_grad<8, WF32>), grid, block, 0, s, a);
 }
 
-// out[c] = sum over p of parts[p][c], c < n: one 64-column block per workgroup, its
-// four waves add every fourth part, their sums are added in wave order.
-__global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ parts, int n_parts, int n,
-                                                   float* __restrict__ out) {
-  __shared__ float red[4][64];
+// out[c] = sum over p of parts[p][c], c < n: 64 columns per workgroup; each of its 16
+// waves adds every 16th part, four at a time, then their sums are added in order.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void k_sum_parts(const float* __restrict__ parts, int n_parts, int n,
+                                                               float* __restrict__ out) {
+  __shared__ float red[kSumWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
-  float s = 0.f;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < n)
-    for (int p = wave; p < n_parts; p += 4) s += parts[(int64_t)p * n + c];
-  red[wave][lane] = s;
+    for (int p = wave; p < n_parts; p += 4 * kSumWaves) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (p + u * kSumWaves < n_parts) s[u] += parts[(int64_t)(p + u * kSumWaves) * n + c];
+    }
+  red[wave][lane] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
-  if (wave == 0 && c < n) out[c] = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
+  if (wave == 0 && c < n) {
+    float sum = red[0][lane];
+    for (int k = 1; k < kSumWaves; ++k) sum += red[k][lane];
+    out[c] = sum;
+  }
 }
 
 }  // namespace
@@ -267,7 +276,8 @@ hipError_t launch_add_norm_grad(const uint16_t* dy, const uint16_t* h, const voi
 }
 
 hipError_t launch_sum_parts(const float* parts, int n_parts, int n, float* out, hipStream_t s) {
-  hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)ceil_div(n, 64)), dim3(256), 0, s, parts, n_parts, n, out);
+  hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)ceil_div(n, 64)), dim3(64 * kSumWaves), 0, s, parts,
+                     n_parts, n, out);
   return hipGetLastError();
 }
 
