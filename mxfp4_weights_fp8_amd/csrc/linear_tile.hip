@@ -1,0 +1,322 @@
+// The tiled dense product on v_mfma_f32_16x16x32_bf16: tiles of 32 FT rows x 32 FW
+// columns, four waves in a 2 x 2 grid of FT x FW fragments of 16 x 16 each, one wave
+// per SIMD. The weights are the MFMA's first operand, so lane (c, q) = (l % 16, l / 16)
+// of a result fragment holds columns 4q .. 4q+3 of row c.
+//
+// The accumulators (256 registers at 8 x 8) live in the AGPR file through inline-asm
+// MFMAs with "+a" operands; the compiler's own choice copies them between the register
+// files inside the loop.
+//
+// LDS: stages of 64 of the contraction index (one step), three for x and two for w,
+// filled by direct-to-LDS copies. A step has two halves of 32:
+//   half A: the MFMAs of the first half, the fragment reads of the second half into
+//           the other register set, the copies of x of step s + 2;
+//   wait for this wave's copies of step s + 1 (all but those of x of step s + 2) and
+//   barrier: they have landed, and everybody has read step s to its end;
+//   half B: the MFMAs of the second half, the fragment reads of the next step's first
+//           half, the copies of w of step s + 2 into the stage of step s.
+// One barrier per 2 FT FW MFMAs; x, which more often comes from HBM, is copied a step
+// and a half ahead, w one step. Both operands' copies read at least 128 neighbouring
+// bytes of a row: with stages of 32 (64-byte pieces) the copies' issue took most of the
+// loop (32768 x 384 x 7168: 208 us).
+//
+// An operand stored [rows, C] is staged as 128-byte rows, 16-byte chunks XORed by a
+// function of the row (the 8 or 16 lanes that LDS serves together then hit every bank
+// once), and a fragment is one ds_read_b128 per lane. One stored [C, rows] is staged as
+// 64 rows of the contraction, and a fragment is two ds_read_b64_tr_b16: lane
+// (4i + g, q) reads columns 4g .. 4g+3 of contraction row 8q + i (then 8q + 4 + i), and
+// the transpose within 16 lanes leaves lane c with four contraction values of column c.
+// The 16 rows of a read lie a multiple of 128 bytes apart, so 32-byte blocks are XORed
+// by a function of the row that spreads them over the banks.
+//
+// Copies past an operand's end, or past this workgroup's share of the contraction, are
+// zeros from the buffer resource's bounds check. A transposed operand's columns past
+// its last one are the next row's values: they only reach outputs that are not stored.
+#include "linear.h"
+#include "lds_copy.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTileThreads = 256;
+constexpr int kXcds = 8;
+constexpr int kGroup = 8;   // row tiles that share a pass over the column tiles
+
+typedef short v4h __attribute__((ext_vector_type(4)));
+
+// acc += A B, acc in AGPRs. The compiler does not know that the statement is an MFMA
+// and inserts no wait states after a VALU write of an operand: s_nop provides them.
+__device__ __forceinline__ void mma_agpr(v4f& acc, const v4i& a, const v4i& b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+#endif
+}
+
+// One operand's steps: ROWS tile rows (columns of the result for w).
+template <int ROWS, bool TRANS>
+struct Operand {
+  static constexpr int kBytes = ROWS * 128;         // a stage
+  static constexpr int kCopies = kBytes / 4096;     // per wave and step
+  static constexpr int kRow = 2 * ROWS;             // bytes of a transposed stage's row
+  static constexpr int kMask = kRow % 256 == 0 ? 7 : 3;   // 32-byte blocks that are XORed together
+
+  const char* base;    // first byte of step 0
+  int64_t step;        // bytes per step
+  int64_t left;        // bytes from `base` to the operand's end (the tile's, for [rows, C])
+  int row_bytes;
+  int voff[kCopies];   // of this lane's 16 bytes, relative to the step
+
+  // XOR of a transposed stage's blocks in contraction row r: the rows 8q + i of a read
+  // differ in i = r % 4 and q
+  __device__ static int xor_of(int r) {
+    return kMask == 7 ? (r & 3) | ((r >> 3 & 1) << 2) : (r >> 1 & 1) | ((r >> 3 & 1) << 1);
+  }
+  // XOR of the chunks of row r
+  __device__ static int chunk_xor(int r) { return (r >> 1 & 7) ^ ((r & 1) << 2); }
+
+  __device__ void init(const uint16_t* p, int64_t stride, int first, int rows, int C, int wave, int lane) {
+    row_bytes = (int)(2 * stride);
+    if constexpr (TRANS) {
+      base = reinterpret_cast<const char*>(p + first);
+      step = (int64_t)64 * row_bytes;
+      left = (int64_t)C * row_bytes - 2 * first;
+    } else {
+      base = reinterpret_cast<const char*>(p + first * stride);
+      step = 128;
+      left = (int64_t)min(ROWS, rows - first) * row_bytes;
+    }
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      const int b = (kCopies * wave + i) * 1024 + lane * 16;   // byte of the stage that this lane fills
+      if constexpr (TRANS) {
+        const int r = b / kRow, chunk = b % kRow / 16;
+        voff[i] = r * row_bytes + ((chunk ^ (xor_of(r) << 1)) << 4);
+      } else {
+        const int r = b / 128, chunk = b % 128 / 16;
+        voff[i] = r * row_bytes + ((chunk ^ chunk_xor(r)) << 4);
+      }
+    }
+  }
+  // the buffer resource of step s; size 0 from `end` on
+  __device__ v4i_s rsrc(int s, int end) const {
+    int64_t bytes = left - s * step;
+    const int64_t most = (int64_t)(TRANS ? 64 : ROWS) * row_bytes;   // keeps the size in 32 bits
+    bytes = bytes < 0 ? 0 : bytes > most ? most : bytes;
+    return rsrc4(base + s * step, s < end ? (uint32_t)bytes : 0u);
+  }
+  __device__ void copy(v4i_s r, uint8_t* stage, int wave, int i) const {
+    dma16(r, lds_addr(stage + (kCopies * wave + i) * 1024), voff[i], 0);
+  }
+};
+
+// A lane's view of the fragments of a stage: fragment f is 16 tile rows from 16 f on,
+// half h the contraction index's 32 h .. 32 h + 31.
+template <int ROWS, bool TRANS>
+struct FragReader {
+  int lane_off[2], x;
+  __device__ void init(int lane) {
+    const int c = lane & 15, q = lane >> 4;
+    if constexpr (TRANS) {
+      const int r = 8 * q + (c >> 2);
+      lane_off[0] = r * 2 * ROWS + 8 * (c & 3);
+      lane_off[1] = lane_off[0] + 32 * 2 * ROWS;
+      x = Operand<ROWS, true>::xor_of(r);   // the same for r + 4 and r + 32
+    } else {
+      const int sw = Operand<ROWS, false>::chunk_xor(c);
+      lane_off[0] = c * 128 + ((q ^ sw) << 4);
+      lane_off[1] = c * 128 + (((4 + q) ^ sw) << 4);
+      x = 0;
+    }
+  }
+  template <int H>
+  __device__ v4i read(const uint8_t* stage, int f) const {
+    if constexpr (TRANS) {
+      typedef __attribute__((address_space(3))) v4h* lds4;
+      const uint8_t* p = stage + lane_off[H] + ((f ^ x) << 5);
+      const v4h lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p);
+      const v4h hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * 2 * ROWS));
+      const int2 a = __builtin_bit_cast(int2, lo), b = __builtin_bit_cast(int2, hi);
+      return v4i{a.x, a.y, b.x, b.y};
+    } else {
+      return *reinterpret_cast<const v4i*>(stage + lane_off[H] + f * 2048);
+    }
+  }
+};
+
+template <int FT, int FW, bool XT, bool WT>
+__global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, int m_tiles, int n_tiles) {
+  constexpr int kRows = 32 * FT, kCols = 32 * FW;
+  constexpr int kXStages = 3, kWStages = 2;
+  typedef Operand<kRows, XT> X;
+  typedef Operand<kCols, WT> W;
+  constexpr int kRing = kXStages * X::kBytes + kWStages * W::kBytes;
+  constexpr int kOutRow = 16 * FW + 4;   // floats per row of a wave's staged result: 16 rows in distinct banks
+  constexpr int kOut = 64 * kOutRow * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing > 4 * kOut ? kRing : 4 * kOut];
+  uint8_t* const smem_w = smem + kXStages * X::kBytes;
+
+  // Workgroups are dealt to the XCDs in turn; give each XCD a contiguous run of the
+  // tile order (split, group of kGroup row tiles, column tile, row tile), so that the
+  // tiles that share operand rows share an L2.
+  const int tiles = m_tiles * n_tiles, total = tiles * a.splits;
+  const int run = (total + kXcds - 1) / kXcds;
+  const int id = (blockIdx.x % kXcds) * run + blockIdx.x / kXcds;
+  if ((int)(blockIdx.x / kXcds) >= run || id >= total) return;
+  const int split = id / tiles, tile = id % tiles;
+  const int group = tile / (kGroup * n_tiles), in_group = tile % (kGroup * n_tiles);
+  const int rows_in_group = min(kGroup, m_tiles - group * kGroup);
+  const int mt = group * kGroup + in_group % rows_in_group, nt = in_group / rows_in_group;
+  const int m0 = mt * kRows, n0 = nt * kCols;
+
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  // this split's steps, dealt as evenly as they go
+  const int steps = (a.C + 63) / 64;
+  const int s0 = (int)((int64_t)steps * split / a.splits), s1 = (int)((int64_t)steps * (split + 1) / a.splits);
+
+  X ox;
+  W ow;
+  ox.init(a.x, a.xs, m0, a.M, a.C, wave, lane);
+  ow.init(a.w, a.ws, n0, a.N, a.w_rows, wave, lane);
+  FragReader<kRows, XT> rx;
+  FragReader<kCols, WT> rw;
+  rx.init(lane);
+  rw.init(lane);
+
+  v4f acc[FW][FT];
+#pragma unroll
+  for (int i = 0; i < FW; ++i)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  struct Ops {
+    v4i w[FW];
+    v4i x[FT];
+  };
+  Ops ops[2];
+  auto copy_x = [&](v4i_s r, int buf, int i) { ox.copy(r, smem + buf * X::kBytes, wave, i); };
+  auto copy_w = [&](v4i_s r, int buf, int i) { ow.copy(r, smem_w + buf * W::kBytes, wave, i); };
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const v4i_s rw0 = ow.rsrc(s0 + b, s1), rx0 = ox.rsrc(s0 + b, s1);
+#pragma unroll
+    for (int i = 0; i < W::kCopies; ++i) copy_w(rw0, b, i);
+#pragma unroll
+    for (int i = 0; i < X::kCopies; ++i) copy_x(rx0, b, i);
+  }
+  wait_vmcnt<X::kCopies + W::kCopies>();
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < FT; ++j) ops[0].x[j] = rx.template read<0>(smem, FT * wm + j);
+#pragma unroll
+  for (int i = 0; i < FW; ++i) ops[0].w[i] = rw.template read<0>(smem_w, FW * wn + i);
+
+  int xb = 0, wb = 0;   // stages of step s
+  for (int s = s0; s < s1; ++s) {
+    const int xb1 = xb + 1 == kXStages ? 0 : xb + 1, xb2 = xb1 + 1 == kXStages ? 0 : xb1 + 1;
+    const v4i_s rx2 = ox.rsrc(s + 2, s1), rw2 = ow.rsrc(s + 2, s1);
+    const uint8_t *px = smem + xb * X::kBytes, *pw = smem_w + wb * W::kBytes;
+#pragma unroll
+    for (int p = 0; p < FW; ++p) {   // half A
+#pragma unroll
+      for (int j = p * FT / FW; j < (p + 1) * FT / FW; ++j) ops[1].x[j] = rx.template read<1>(px, FT * wm + j);
+      ops[1].w[p] = rw.template read<1>(pw, FW * wn + p);
+#pragma unroll
+      for (int i = p * X::kCopies / FW; i < (p + 1) * X::kCopies / FW; ++i) copy_x(rx2, xb2, i);
+#pragma unroll
+      for (int j = 0; j < FT; ++j) mma_agpr(acc[p][j], ops[0].w[p], ops[0].x[j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_vmcnt<X::kCopies>();
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    px = smem + xb1 * X::kBytes;
+    pw = smem_w + (wb ^ 1) * W::kBytes;
+#pragma unroll
+    for (int p = 0; p < FW; ++p) {   // half B
+#pragma unroll
+      for (int j = p * FT / FW; j < (p + 1) * FT / FW; ++j) ops[0].x[j] = rx.template read<0>(px, FT * wm + j);
+      ops[0].w[p] = rw.template read<0>(pw, FW * wn + p);
+#pragma unroll
+      for (int i = p * W::kCopies / FW; i < (p + 1) * W::kCopies / FW; ++i) copy_w(rw2, wb, i);
+#pragma unroll
+      for (int j = 0; j < FT; ++j) mma_agpr(acc[p][j], ops[1].w[p], ops[1].x[j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    xb = xb1;
+    wb ^= 1;
+  }
+  wait_vmcnt<0>();   // no copy may land in the staged result
+  // The compiler does not see the MFMAs, so it inserts no wait states before the
+  // accumulators are read: 64 of them here.
+  __builtin_amdgcn_sched_barrier(0);
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+#endif
+  __builtin_amdgcn_sched_barrier(0);
+  __syncthreads();
+
+  // Results, 64 rows of the wave at a time, through the wave's own part of LDS, so that
+  // stores walk whole rows: 2 FW lanes hold 8 columns each of a row.
+  float* const out = reinterpret_cast<float*>(smem + wave * kOut);
+#pragma unroll
+  for (int j0 = 0; j0 < FT; j0 += 4) {
+    constexpr int kGroups = 2 * FW;
+    const int frags = FT - j0 < 4 ? FT - j0 : 4;
+#pragma unroll
+    for (int j = j0; j < j0 + 4 && j < FT; ++j)
+#pragma unroll
+      for (int i = 0; i < FW; ++i)
+        *reinterpret_cast<v4f*>(out + (16 * (j - j0) + c) * kOutRow + 16 * i + 4 * q) = acc[i][j];
+    __syncthreads();
+#pragma unroll 1
+    for (int g = lane; g < 16 * frags * kGroups; g += 64) {
+      const int r = g / kGroups, col = 8 * (g % kGroups);
+      const int64_t m = m0 + 16 * FT * wm + 16 * j0 + r;
+      const int n = n0 + 16 * FW * wn + col;
+      const v4f lo = *reinterpret_cast<const v4f*>(out + r * kOutRow + col);
+      const v4f hi = *reinterpret_cast<const v4f*>(out + r * kOutRow + col + 4);
+      if (a.splits == 1) {
+        finish8(a, m, n, lo, hi);
+      } else if (m < a.M && n < a.N) {
+        float* dst = a.parts + ((int64_t)split * a.M + m) * a.N + n;
+        if (a.N % 4 == 0) {
+          *reinterpret_cast<v4f*>(dst) = lo;
+          if (n + 4 < a.N) *reinterpret_cast<v4f*>(dst + 4) = hi;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (n + k < a.N) dst[k] = k < 4 ? lo[k & 3] : hi[k & 3];
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <int FT, int FW, bool XT, bool WT>
+void run(const LinearArgs& a, hipStream_t s) {
+  const int m_tiles = (int)ceil_div(a.M, 32 * FT), n_tiles = (int)ceil_div(a.N, 32 * FW);
+  const int64_t total = (int64_t)m_tiles * n_tiles * a.splits;
+  hipLaunchKernelGGL((k_linear_tile<FT, FW, XT, WT>), dim3((unsigned)(ceil_div(total, kXcds) * kXcds)),
+                     dim3(kTileThreads), 0, s, a, m_tiles, n_tiles);
+}
+
+template <bool XT, bool WT>
+void by_tile(const LinearArgs& a, const LinearPlan& p, hipStream_t s) {
+  if (p.ft == 8 && p.fw == 8) run<8, 8, XT, WT>(a, s);
+  else if (p.ft == 8) run<8, 6, XT, WT>(a, s);
+  else if (p.ft == 6) run<6, 8, XT, WT>(a, s);
+  else run<4, 4, XT, WT>(a, s);
+}
+
+}  // namespace
+
+void launch_tiles(const LinearArgs& a, const LinearPlan& p, Layout l, hipStream_t s) {
+  if (l == Layout::kRows) by_tile<false, false>(a, p, s);
+  else if (l == Layout::kWTrans) by_tile<false, true>(a, p, s);
+  else by_tile<true, true>(a, p, s);
+}
+
+}  // namespace moe
