@@ -43,13 +43,27 @@ void launch_tiles(const LinearArgs& a, const LinearPlan& p, Layout l, hipStream_
 
 __device__ __forceinline__ float sigmoid_f(float z) { return 1.f / (1.f + expf(-z)); }
 
-__device__ __forceinline__ float activate(float z, int act) {
+// act of N values: one branch for all of them.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
   switch (act) {
-    case MOE_ACT_RELU: return z < 0.f ? 0.f : z;   // NaN stays NaN
-    case MOE_ACT_SILU: return z * sigmoid_f(z);
-    case MOE_ACT_GELU: return 0.5f * z * erfcf(z * -0.707106781f);
-    case MOE_ACT_SIGMOID: return sigmoid_f(z);
-    default: return z;
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // NaN stays NaN
+      break;
+    case MOE_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] * sigmoid_f(v[i]);
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * erfcf(v[i] * -0.707106781f);
+      break;
+    case MOE_ACT_SIGMOID:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = sigmoid_f(v[i]);
+      break;
+    default: break;
   }
 }
 
@@ -69,76 +83,92 @@ __device__ __forceinline__ float activate_slope(float z, int act) {
   }
 }
 
-// The epilogue of columns n .. n + 3 of row m (those below N), from their sums.
-__device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int n, v4f v) {
-  if (m >= a.M || n >= a.N) return;
+// The epilogue of V (4 or 8) neighbouring columns n .. n + V - 1 of row m, those below
+// N. The residual is loaded apart, so that a caller can have several on their way.
+template <int V>
+struct Residual {
+  float v[V];
+};
+
+template <int V>
+__device__ __forceinline__ Residual<V> load_residual(const LinearArgs& a, int64_t m, int n) {
+  Residual<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.v[i] = 0.f;
+  if (!a.res || m >= a.M || n >= a.N) return r;
   const int64_t at = m * a.N + n;
-  if (a.N % 4 == 0) {
-    if (a.bias) v += *reinterpret_cast<const v4f*>(a.bias + n);
-    if (a.z) *reinterpret_cast<v4f*>(a.z + at) = v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = activate(v[i], a.act);
+  if (a.N % V == 0) {
     if (a.out_f32) {
-      if (a.res) v += *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(a.res) + at);
-      *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + at) = v;
-    } else {
-      if (a.res) {
-        const uint2 r = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.res) + at);
-        v += v4f{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
-                 __uint_as_float(r.y & 0xFFFF0000u)};
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        const v4f t = *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(a.res) + at + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.v[k + i] = t[i];
       }
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + at) =
-          make_uint2(bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]));
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n + i >= a.N) break;
-    float f = v[i] + (a.bias ? a.bias[n + i] : 0.f);
-    if (a.z) a.z[at + i] = f;
-    f = activate(f, a.act);
-    if (a.out_f32) {
-      if (a.res) f += reinterpret_cast<const float*>(a.res)[at + i];
-      reinterpret_cast<float*>(a.y)[at + i] = f;
     } else {
-      if (a.res) f += bf16_to_float(reinterpret_cast<const uint16_t*>(a.res)[at + i]);
-      reinterpret_cast<uint16_t*>(a.y)[at + i] = (uint16_t)bf16_pack2(f, 0.f);
+      uint32_t t[V / 2];
+      if constexpr (V == 8) {
+        const v4i x = *reinterpret_cast<const v4i*>(reinterpret_cast<const uint16_t*>(a.res) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = (uint32_t)x[i];
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.res) + at);
+        t[0] = x.x;
+        t[1] = x.y;
+      }
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        r.v[2 * i] = __uint_as_float(t[i] << 16);
+        r.v[2 * i + 1] = __uint_as_float(t[i] & 0xFFFF0000u);
+      }
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (n + i < a.N)
+        r.v[i] = a.out_f32 ? reinterpret_cast<const float*>(a.res)[at + i]
+                           : bf16_to_float(reinterpret_cast<const uint16_t*>(a.res)[at + i]);
   }
+  return r;
 }
 
-// The same for columns n .. n + 7.
-__device__ __forceinline__ void finish8(const LinearArgs& a, int64_t m, int n, v4f lo, v4f hi) {
-  if (a.N % 8 != 0 || a.out_f32) {
-    finish4(a, m, n, lo);
-    finish4(a, m, n + 4, hi);
-    return;
-  }
+template <int V>
+__device__ __forceinline__ void finish(const LinearArgs& a, int64_t m, int n, float (&v)[V], const Residual<V>& r) {
   if (m >= a.M || n >= a.N) return;
   const int64_t at = m * a.N + n;
+  const bool whole = a.N % V == 0;
   if (a.bias) {
-    lo += *reinterpret_cast<const v4f*>(a.bias + n);
-    hi += *reinterpret_cast<const v4f*>(a.bias + n + 4);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (whole || n + i < a.N) v[i] += a.bias[n + i];
   }
   if (a.z) {
-    *reinterpret_cast<v4f*>(a.z + at) = lo;
-    *reinterpret_cast<v4f*>(a.z + at + 4) = hi;
-  }
-  v4i r{0, 0, 0, 0};
-  if (a.res) r = *reinterpret_cast<const v4i*>(reinterpret_cast<const uint16_t*>(a.res) + at);
-  v4i o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float v0 = activate(i < 2 ? lo[2 * i] : hi[2 * i - 4], a.act);
-    float v1 = activate(i < 2 ? lo[2 * i + 1] : hi[2 * i - 3], a.act);
-    if (a.res) {
-      v0 += __uint_as_float((uint32_t)r[i] << 16);
-      v1 += __uint_as_float((uint32_t)r[i] & 0xFFFF0000u);
-    }
-    o[i] = (int)bf16_pack2(v0, v1);
+    for (int i = 0; i < V; ++i)
+      if (whole || n + i < a.N) a.z[at + i] = v[i];
   }
-  *reinterpret_cast<v4i*>(reinterpret_cast<uint16_t*>(a.y) + at) = o;
+  activate(v, a.act);
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = a.res ? v[i] + r.v[i] : v[i];
+  if (whole && a.out_f32) {
+#pragma unroll
+    for (int k = 0; k < V; k += 4)
+      *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + at + k) = v4f{v[k], v[k + 1], v[k + 2], v[k + 3]};
+  } else if (whole) {
+    uint16_t* dst = reinterpret_cast<uint16_t*>(a.y) + at;
+    if constexpr (V == 8)
+      *reinterpret_cast<v4i*>(dst) = v4i{(int)bf16_pack2(v[0], v[1]), (int)bf16_pack2(v[2], v[3]),
+                                         (int)bf16_pack2(v[4], v[5]), (int)bf16_pack2(v[6], v[7])};
+    else
+      *reinterpret_cast<uint2*>(dst) = make_uint2(bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (n + i < a.N) {
+        if (a.out_f32) reinterpret_cast<float*>(a.y)[at + i] = v[i];
+        else reinterpret_cast<uint16_t*>(a.y)[at + i] = (uint16_t)bf16_pack2(v[i], 0.f);
+      }
+  }
 }
 
 }  // namespace moe

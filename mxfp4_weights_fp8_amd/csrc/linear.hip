@@ -68,7 +68,9 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_linear_small(LinearArgs a)
     v4f v = part[i];
     for (int k = 1; k < waves; ++k) v += part[k * FT * 64 + i];
     const int f = i >> 6, l = i & 63;
-    finish4(a, 16 * f + (l & 15), n0 + 4 * (l >> 4), v);
+    const int m = 16 * f + (l & 15), n = n0 + 4 * (l >> 4);
+    float o[4] = {v[0], v[1], v[2], v[3]};
+    finish<4>(a, m, n, o, load_residual<4>(a, m, n));
   }
 }
 
@@ -79,6 +81,7 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a) {
   if (g >= (int64_t)a.M * groups) return;
   const int64_t m = g / groups;
   const int n = 4 * (int)(g - m * groups);
+  const Residual<4> r = load_residual<4>(a, m, n);
   v4f v{0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < a.splits; ++s) {
     const float* src = a.parts + ((int64_t)s * a.M + m) * a.N + n;
@@ -86,37 +89,39 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a) {
       v += *reinterpret_cast<const v4f*>(src);
     } else {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (n + r < a.N) v[r] += src[r];
+      for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) v[i] += src[i];
     }
   }
-  finish4(a, m, n, v);
+  float o[4] = {v[0], v[1], v[2], v[3]};
+  finish<4>(a, m, n, o, r);
 }
 
 }  // namespace
 
-// Tile shape: the one whose tiles fill the 256 CUs in the least time, a tile's time
-// taken as its fragments' MFMAs plus an overhead of prologue and epilogue worth 5
-// steps. Where even the smallest tiles leave CUs empty, the contraction is split,
-// at least 4 steps each.
+// Tile shape and splits of the contraction: the least estimated time. Measured with
+// every CU busy, in 10 ns: a step of 64 takes `step` (two workgroups of the smallest
+// tile share a CU), prologue and epilogue `fixed` per round of tiles, and joining the
+// parts of a split product 4 us and its traffic at 4 TB/s. (8192^3: 256 x 256 tiles 851
+// us, 128 x 128 971; 8191 x 7168 x 2048: 310 and 266; 4096 x 2048 x 7168: 256 x 256 split
+// in two 112, 128 x 128 110, unsplit 256 x 256 168.)
 LinearPlan linear_plan(int M, int N, int C, Layout l) {
   if (M <= 64 && l == Layout::kRows) return LinearPlan{true, 0, 0, 1};
   static const struct {
-    int ft, fw, per_cu;
-  } kShapes[] = {{8, 8, 1}, {8, 6, 1}, {6, 8, 1}, {4, 4, 2}};
+    int ft, fw, per_cu, step, fixed;
+  } kShapes[] = {{8, 8, 1, 170, 2200}, {8, 6, 1, 145, 1500}, {6, 8, 1, 145, 1500}, {4, 4, 2, 98, 800}};
   const int64_t steps = ceil_div(C, 64);
   LinearPlan best{false, 0, 0, 1};
   int64_t least = -1;
   for (const auto& t : kShapes) {
-    const int64_t tiles = ceil_div(M, 32 * t.ft) * ceil_div(N, 32 * t.fw);
-    int64_t splits = tiles < 256 * t.per_cu ? 256 * t.per_cu / tiles : 1;
-    if (splits > steps / 4) splits = steps / 4;
-    if (splits < 1) splits = 1;
-    const int64_t rounds = ceil_div(tiles * splits, 256 * t.per_cu);
-    const int64_t time = rounds * t.per_cu * t.ft * t.fw * (ceil_div(steps, splits) + 5) + (splits > 1 ? 64 * 4 : 0);
-    if (least < 0 || time < least) {
-      least = time;
-      best = LinearPlan{false, t.ft, t.fw, (int)splits};
+    const int64_t tiles = ceil_div(M, 32 * t.ft) * ceil_div(N, 32 * t.fw), slots = 256 * t.per_cu;
+    for (int64_t splits = 1; splits == 1 || (splits <= steps / 4 && tiles * splits <= 2 * slots); ++splits) {
+      int64_t time = ceil_div(tiles * splits, slots) * (ceil_div(steps, splits) * t.step + t.fixed);
+      if (splits > 1) time += 400 + splits * M * N * 8 / 40000;
+      if (least < 0 || time < least) {
+        least = time;
+        best = LinearPlan{false, t.ft, t.fw, (int)splits};
+      }
     }
   }
   return best;

@@ -258,11 +258,12 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
   __syncthreads();
 
   // Results, 64 rows of the wave at a time, through the wave's own part of LDS, so that
-  // stores walk whole rows: 2 FW lanes hold 8 columns each of a row.
+  // stores walk whole rows: 2 FW lanes hold 8 columns each of a row. Four groups at a
+  // time, their residuals loaded ahead.
   float* const out = reinterpret_cast<float*>(smem + wave * kOut);
 #pragma unroll
   for (int j0 = 0; j0 < FT; j0 += 4) {
-    constexpr int kGroups = 2 * FW;
+    constexpr int kGroups = 2 * FW, kAtOnce = 4;
     const int frags = FT - j0 < 4 ? FT - j0 : 4;
 #pragma unroll
     for (int j = j0; j < j0 + 4 && j < FT; ++j)
@@ -271,23 +272,35 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
         *reinterpret_cast<v4f*>(out + (16 * (j - j0) + c) * kOutRow + 16 * i + 4 * q) = acc[i][j];
     __syncthreads();
 #pragma unroll 1
-    for (int g = lane; g < 16 * frags * kGroups; g += 64) {
-      const int r = g / kGroups, col = 8 * (g % kGroups);
-      const int64_t m = m0 + 16 * FT * wm + 16 * j0 + r;
-      const int n = n0 + 16 * FW * wn + col;
-      const v4f lo = *reinterpret_cast<const v4f*>(out + r * kOutRow + col);
-      const v4f hi = *reinterpret_cast<const v4f*>(out + r * kOutRow + col + 4);
-      if (a.splits == 1) {
-        finish8(a, m, n, lo, hi);
-      } else if (m < a.M && n < a.N) {
-        float* dst = a.parts + ((int64_t)split * a.M + m) * a.N + n;
-        if (a.N % 4 == 0) {
-          *reinterpret_cast<v4f*>(dst) = lo;
-          if (n + 4 < a.N) *reinterpret_cast<v4f*>(dst + 4) = hi;
-        } else {
+    for (int g0 = lane; g0 < 16 * frags * kGroups; g0 += 64 * kAtOnce) {   // a multiple of 64 * kAtOnce
+      Residual<8> res[kAtOnce];
+      int row[kAtOnce], col[kAtOnce];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (n + k < a.N) dst[k] = k < 4 ? lo[k & 3] : hi[k & 3];
+      for (int u = 0; u < kAtOnce; ++u) {
+        row[u] = (g0 + 64 * u) / kGroups;
+        col[u] = 8 * ((g0 + 64 * u) % kGroups);
+        if (a.splits == 1)
+          res[u] = load_residual<8>(a, m0 + 16 * FT * wm + 16 * j0 + row[u], n0 + 16 * FW * wn + col[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t m = m0 + 16 * FT * wm + 16 * j0 + row[u];
+        const int n = n0 + 16 * FW * wn + col[u];
+        const v4f lo = *reinterpret_cast<const v4f*>(out + row[u] * kOutRow + col[u]);
+        const v4f hi = *reinterpret_cast<const v4f*>(out + row[u] * kOutRow + col[u] + 4);
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        if (a.splits == 1) {
+          finish<8>(a, m, n, v, res[u]);
+        } else if (m < a.M && n < a.N) {
+          float* dst = a.parts + ((int64_t)split * a.M + m) * a.N + n;
+          if (a.N % 4 == 0) {
+            *reinterpret_cast<v4f*>(dst) = lo;
+            if (n + 4 < a.N) *reinterpret_cast<v4f*>(dst + 4) = hi;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (n + k < a.N) dst[k] = v[k];
+          }
         }
       }
     }
