@@ -22,13 +22,14 @@ struct BalanceArgs {
   double* parts;        // one per workgroup
   float* loss;
   int64_t T;
-  int E, K, B, rows;    // rows: tokens per workgroup
+  int E, K, B;
   float alpha;
 };
 
 __device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t T) { return v < 0 ? 0 : v > T ? T : v; }
 
-// The sequence that holds token t, or -1 (off is ascending).
+// The sequence that holds token t, or -1 (off is ascending; whatever it holds, the
+// answer b >= 0 has off[b] <= t < off[b + 1]).
 __device__ __forceinline__ int find_seq(const BalanceArgs& a, int64_t t) {
   if (!a.off) return 0;
   if (t < a.off[0] || t >= a.off[a.B]) return -1;
@@ -41,34 +42,110 @@ __device__ __forceinline__ int find_seq(const BalanceArgs& a, int64_t t) {
   return lo;
 }
 
+// a_be = factor * c_be
+__device__ __forceinline__ float seq_factor(const BalanceArgs& a, int b) {
+  const float n = a.off ? (float)(a.off[b + 1] - a.off[b]) : (float)a.T;
+  return (a.alpha / (float)a.B) * ((float)a.E / (float)a.K) / n / n;
+}
+
+template <int LPR, int NV, bool VEC>
+__device__ __forceinline__ void load_coef(const int32_t* counts, int E, float factor, int lane, float (&coef)[NV][4]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e0 = 4 * (j * LPR + lane);
+    v4i c{0, 0, 0, 0};
+    if constexpr (VEC) {
+      if (e0 < E) c = *reinterpret_cast<const v4i*>(counts + e0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e0 + i < E) c[i] = counts[e0 + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) coef[j][i] = factor * (float)c[i];
+  }
+}
+
+// One token: writes its gradient, returns its part of the loss.
+template <int LPR, int NV, int SCORE, bool BF16, bool VEC>
+__device__ __forceinline__ float balance_row(const BalanceArgs& a, int64_t t, int lane, const float (&coef)[NV][4]) {
+  const char* row = reinterpret_cast<const char*>(a.logits) + t * a.E * (BF16 ? 2 : 4);
+  float* dl = a.dl + t * a.E;
+  float s[NV][4], k[NV][4];   // scores, and what multiplies (a - d) / sum in the gradient
+#pragma unroll
+  for (int j = 0; j < NV; ++j) load_logits4<BF16, VEC>(row, 4 * (j * LPR + lane), a.E, s[j]);
+  float top = kNone;
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[j][i]);
+    top = row_max<LPR>(top);
+  }
+  float sum = 0.f, dot = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float l = s[j][i];
+      if constexpr (SCORE == MOE_SCORE_SOFTMAX) s[j][i] = k[j][i] = l == kNone ? 0.f : exp_f(l - top);
+      else score_and_slope<SCORE>(l, s[j][i], k[j][i]);
+      sum += s[j][i];
+      dot += s[j][i] * coef[j][i];
+    }
+  sum = row_sum<LPR>(sum);
+  dot = row_sum<LPR>(dot);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  dot *= inv;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e0 = 4 * (j * LPR + lane);
+    float o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = k[j][i] * ((coef[j][i] - dot) * inv);
+    if constexpr (VEC) {
+      if (e0 < a.E) *reinterpret_cast<v4f*>(dl + e0) = v4f{o[0], o[1], o[2], o[3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e0 + i < a.E) dl[e0 + i] = o[i];
+    }
+  }
+  return dot;
+}
+
 __global__ __launch_bounds__(256) void k_fill_zero(int32_t* p, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
 }
 
-// counts, one workgroup per a.rows tokens: an LDS histogram per sequence that the
+// Picks of tokens [first, end) into an LDS histogram.
+__device__ __forceinline__ void count_picks(const BalanceArgs& a, int64_t first, int64_t end, int32_t* hist) {
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
+  __syncthreads();
+  for (int64_t i = first * a.K + threadIdx.x; i < end * a.K; i += blockDim.x) {
+    const int id = a.ids[i];
+    if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);
+  }
+  __syncthreads();
+}
+
+// counts, one workgroup per kCountRows tokens: an LDS histogram per sequence that the
 // tokens touch, added to the global one (integers: any order gives the same).
+constexpr int kCountRows = 256;
 __global__ __launch_bounds__(256) void k_balance_count(BalanceArgs a) {
   extern __shared__ int32_t hist[];
-  const int64_t first = (int64_t)blockIdx.x * a.rows;
-  const int64_t end = first + a.rows < a.T ? first + a.rows : a.T;
+  const int64_t first = (int64_t)blockIdx.x * kCountRows;
+  const int64_t end = first + kCountRows < a.T ? first + kCountRows : a.T;
   for (int64_t t = first; t < end;) {
     const int b = find_seq(a, t);
     if (b < 0) {
-      if (a.off && t < a.off[0]) {
-        t = clamp_row(a.off[0], a.T);
-        continue;
-      }
-      break;
+      if (t >= a.off[0]) break;   // behind the last sequence
+      t = clamp_row(a.off[0], a.T);
+      continue;
     }
     int64_t stop = a.off ? clamp_row(a.off[b + 1], a.T) : a.T;
     if (stop > end) stop = end;
-    for (int e = threadIdx.x; e < a.E; e += 256) hist[e] = 0;
-    __syncthreads();
-    for (int64_t i = t * a.K + threadIdx.x; i < stop * a.K; i += 256) {
-      const int id = a.ids[i];
-      if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);
-    }
-    __syncthreads();
+    count_picks(a, t, stop, hist);
     for (int e = threadIdx.x; e < a.E; e += 256)
       if (hist[e]) atomicAdd(&a.counts[(int64_t)b * a.E + e], hist[e]);
     __syncthreads();
@@ -76,80 +153,30 @@ __global__ __launch_bounds__(256) void k_balance_count(BalanceArgs a) {
   }
 }
 
+// The tokens' gradients and parts of the loss, after the counts: kBalanceRows tokens
+// per workgroup. A row's lanes keep the coefficients of the sequence they are in.
+constexpr int kBalanceRows = 32;
 template <int LPR, int NV, int SCORE, bool BF16, bool VEC>
 __global__ __launch_bounds__(kGateThreads) void k_balance(BalanceArgs a) {
-  __shared__ double red[kGateThreads / LPR];
   constexpr int kRows = kGateThreads / LPR;   // rows in flight
+  __shared__ double red[kRows];
   const int lane = threadIdx.x & (LPR - 1), sub = threadIdx.x / LPR;
-  const int64_t first = (int64_t)blockIdx.x * a.rows;
-  const int64_t end = first + a.rows < a.T ? first + a.rows : a.T;
+  const int64_t first = (int64_t)blockIdx.x * kBalanceRows;
+  const int64_t end = first + kBalanceRows < a.T ? first + kBalanceRows : a.T;
   double mine = 0.0;
-  int seq = -2;
+  int64_t stop = -1;   // end of the sequence whose coefficients are held
   float coef[NV][4];
   for (int64_t t = first + sub; t < end; t += kRows) {
-    const int b = find_seq(a, t);
-    float l[NV][4];
-    const char* row = reinterpret_cast<const char*>(a.logits) + t * a.E * (BF16 ? 2 : 4);
-    float* dl = a.dl + t * a.E;
-    if (b < 0) {   // behind the last sequence or before the first
-      for (int e = lane; e < a.E; e += LPR) dl[e] = 0.f;
-      continue;
-    }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) load_logits4<BF16, VEC>(row, 4 * (j * LPR + lane), a.E, l[j]);
-    if (b != seq) {
-      seq = b;
-      const float n = a.off ? (float)(a.off[b + 1] - a.off[b]) : (float)a.T;
-      const float c = (a.alpha / (float)a.B) * ((float)a.E / (float)a.K) / n / n;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = 4 * (j * LPR + lane) + i;
-          coef[j][i] = e < a.E ? c * (float)a.counts[(int64_t)b * a.E + e] : 0.f;
-        }
-    }
-    float top = kNone;
-    if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, l[j][i]);
-      top = row_max<LPR>(top);
-    }
-    float sum = 0.f, dot = 0.f, s[NV][4];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (SCORE == MOE_SCORE_SOFTMAX) s[j][i] = l[j][i] == kNone ? 0.f : exp_f(l[j][i] - top);
-        else s[j][i] = score_f32<SCORE>(l[j][i], top, 1.f);
-        sum += s[j][i];
-        dot += s[j][i] * coef[j][i];
+    if (t >= stop) {
+      const int b = find_seq(a, t);
+      if (b < 0) {   // in front of the first sequence or behind the last
+        for (int e = lane; e < a.E; e += LPR) a.dl[t * a.E + e] = 0.f;
+        continue;
       }
-    sum = row_sum<LPR>(sum);
-    dot = row_sum<LPR>(dot);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    dot *= inv;
-    if (lane == 0) mine += (double)dot;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e0 = 4 * (j * LPR + lane);
-      float o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float g = (coef[j][i] - dot) * inv;
-        if constexpr (SCORE == MOE_SCORE_SOFTMAX) o[i] = s[j][i] * g;
-        else o[i] = l[j][i] == kNone ? 0.f : g * score_slope<SCORE>(l[j][i], s[j][i]);
-      }
-      if constexpr (VEC) {
-        if (e0 < a.E) *reinterpret_cast<v4f*>(dl + e0) = v4f{o[0], o[1], o[2], o[3]};
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (e0 + i < a.E) dl[e0 + i] = o[i];
-      }
+      stop = a.off ? a.off[b + 1] : a.T;
+      load_coef<LPR, NV, VEC>(a.counts + (int64_t)b * a.E, a.E, seq_factor(a, b), lane, coef);
     }
+    mine += (double)balance_row<LPR, NV, SCORE, BF16, VEC>(a, t, lane, coef);
   }
   if (lane == 0) red[sub] = mine;
   __syncthreads();
@@ -160,38 +187,96 @@ __global__ __launch_bounds__(kGateThreads) void k_balance(BalanceArgs a) {
   }
 }
 
-__global__ __launch_bounds__(64) void k_balance_sum(const double* __restrict__ parts, int n, float* loss) {
+__global__ __launch_bounds__(256) void k_balance_sum(const double* __restrict__ parts, int n, float* loss) {
+  __shared__ double red[4];
   double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += 64) s += parts[i];
+  for (int i = threadIdx.x; i < n; i += 256) s += parts[i];
   s = row_sum<64>(s);
-  if (threadIdx.x == 0) *loss = (float)s;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) *loss = (float)(red[0] + red[1] + red[2] + red[3]);
 }
+
+// Small batches of few sequences in one launch of one workgroup: sequence by sequence,
+// the histogram, then its tokens.
+constexpr int kOneThreads = 1024;
+template <int LPR, int NV, int SCORE, bool BF16, bool VEC>
+__global__ __launch_bounds__(kOneThreads) void k_balance_one(BalanceArgs a) {
+  constexpr int kRows = kOneThreads / LPR;
+  __shared__ __attribute__((aligned(16))) int32_t hist[4 * LPR * NV];   // E at most
+  __shared__ double red[kRows];
+  const int lane = threadIdx.x & (LPR - 1), sub = threadIdx.x / LPR;
+  double mine = 0.0;
+  auto clear = [&](int64_t lo, int64_t hi) {   // rows in no sequence
+    for (int64_t i = lo * a.E + threadIdx.x; i < hi * a.E; i += kOneThreads) a.dl[i] = 0.f;
+  };
+  if (a.off) {
+    clear(0, clamp_row(a.off[0], a.T));
+    clear(clamp_row(a.off[a.B], a.T), a.T);
+  }
+  for (int b = 0; b < a.B; ++b) {
+    const int64_t lo = a.off ? clamp_row(a.off[b], a.T) : 0, hi = a.off ? clamp_row(a.off[b + 1], a.T) : a.T;
+    count_picks(a, lo, hi, hist);
+    for (int e = threadIdx.x; e < a.E; e += kOneThreads) a.counts[(int64_t)b * a.E + e] = hist[e];
+    if (hi > lo) {   // the same for everybody
+      float coef[NV][4];
+      load_coef<LPR, NV, VEC>(hist, a.E, seq_factor(a, b), lane, coef);
+      for (int64_t t = lo + sub; t < hi; t += kRows)
+        mine += (double)balance_row<LPR, NV, SCORE, BF16, VEC>(a, t, lane, coef);
+    }
+    __syncthreads();   // the histogram is read before the next sequence clears it
+  }
+  if (lane == 0) red[sub] = mine;
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < kRows; i += 64) s += red[i];
+    s = row_sum<64>(s);
+    if (threadIdx.x == 0) *a.loss = (float)s;
+  }
+}
+
+// One workgroup where it needs at most 8 rounds of 64 tokens and 4 sequences (256 x 64
+// top-6: 22 us per call with the launches below, bound by the host).
+inline bool one_workgroup(const moe_gate_dims& d, int B) { return d.T <= 512 && d.E <= 512 && B <= 4; }
 
 }  // namespace
 
-constexpr int kBalanceRows = 64;   // tokens per workgroup
 int balance_parts(const moe_gate_dims& d) { return (int)ceil_div(d.T, kBalanceRows); }
 
 hipError_t launch_balance(const moe_gate_dims& d, int B, float alpha, const void* logits, const int32_t* ids,
                           const int32_t* off, float* loss, int32_t* counts, float* dl, double* parts, hipStream_t s) {
-  const int rows = kBalanceRows, n = balance_parts(d);
-  const BalanceArgs a{logits, ids, off, counts, dl, parts, loss, d.T, d.E, d.K, B, rows, alpha};
+  const int n = balance_parts(d);
+  const BalanceArgs a{logits, ids, off, counts, dl, parts, loss, d.T, d.E, d.K, B, alpha};
+  const bool bf = d.logits_type == MOE_TYPE_BF16, vec = d.E % 4 == 0;
+  if (one_workgroup(d, B)) {
+    by_few_experts(d.E, [&](auto nv) {
+      by_score(d.score, [&](auto score) {
+        by_layout(bf, vec, [&](auto bf16, auto v) {
+          hipLaunchKernelGGL((k_balance_one<16, decltype(nv)::value, decltype(score)::value, decltype(bf16)::value != 0,
+                                            decltype(v)::value != 0>),
+                             dim3(1), dim3(kOneThreads), 0, s, a);
+        });
+      });
+    });
+    return hipGetLastError();
+  }
   const int64_t nc = (int64_t)B * d.E;
   hipLaunchKernelGGL(k_fill_zero, dim3((unsigned)(ceil_div(nc, 256) < 1024 ? ceil_div(nc, 256) : 1024)), dim3(256), 0,
                      s, counts, nc);
   if (n > 0) {
-    hipLaunchKernelGGL(k_balance_count, dim3((unsigned)n), dim3(256), sizeof(int32_t) * d.E, s, a);
+    hipLaunchKernelGGL(k_balance_count, dim3((unsigned)ceil_div(d.T, kCountRows)), dim3(256), sizeof(int32_t) * d.E, s, a);
     by_experts(d.E, false, [&](auto lpr, auto nv) {
       by_score(d.score, [&](auto score) {
-        by_layout(d.logits_type == MOE_TYPE_BF16, d.E % 4 == 0, [&](auto bf16, auto vec) {
+        by_layout(bf, vec, [&](auto bf16, auto v) {
           hipLaunchKernelGGL((k_balance<decltype(lpr)::value, decltype(nv)::value, decltype(score)::value,
-                                        decltype(bf16)::value != 0, decltype(vec)::value != 0>),
+                                        decltype(bf16)::value != 0, decltype(v)::value != 0>),
                              dim3((unsigned)n), dim3(kGateThreads), 0, s, a);
         });
       });
     });
   }
-  hipLaunchKernelGGL(k_balance_sum, dim3(1), dim3(64), 0, s, parts, n, loss);
+  hipLaunchKernelGGL(k_balance_sum, dim3(1), dim3(256), 0, s, parts, n, loss);
   return hipGetLastError();
 }
 

@@ -56,7 +56,7 @@ int moe_add_norm(int32_t T, int32_t H, float eps, const uint16_t* x, const uint1
 
 size_t moe_add_norm_grad_workspace_bytes(int32_t T, int32_t H) {
   if (check_norm(T, H, 0.f, MOE_TYPE_F32) != MOE_OK) return 0;
-  return sizeof(float) * (size_t)norm_grad_parts(T) * H;
+  return sizeof(float) * (size_t)norm_grad_parts(T, H) * H;
 }
 
 int moe_add_norm_grad(int32_t T, int32_t H, float eps, const uint16_t* dy, const uint16_t* h, const void* weight,

@@ -51,7 +51,9 @@ __global__ __launch_bounds__(kGateThreads) void k_gate_grad(GateGradArgs a) {
   int id = lane < a.K ? a.ids[t * a.K + lane] : -1;
   if (id < 0 || id >= a.E) id = -1;
   const float lg = id >= 0 ? load_logit<BF16>(row, id) : kNone;
-  const float s = score_f32<SCORE>(lg, top, sum);
+  float s, slope = 0.f;
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) s = score_f32<SCORE>(lg, top, sum);
+  else score_and_slope<SCORE>(lg, s, slope);
   float dc = id >= 0 ? a.dw[t * a.K + lane] : 0.f;
   if (a.renorm) {
     const float S = row_sum<LPR>(s) + 1e-20f;
@@ -60,7 +62,7 @@ __global__ __launch_bounds__(kGateThreads) void k_gate_grad(GateGradArgs a) {
   dc = id >= 0 ? dc * a.scale : 0.f;
   float pd = 0.f;
   if constexpr (SCORE == MOE_SCORE_SOFTMAX) pd = row_sum<LPR>(dc * s);
-  else dc = lg == kNone ? 0.f : dc * score_slope<SCORE>(lg, s);
+  else dc *= slope;
 
   float g[NV][4];
 #pragma unroll

@@ -218,7 +218,7 @@ hipError_t launch_dequant_act(const uint8_t* x_q, const uint8_t* x_s, uint16_t* 
 // Residual add + RMS norm; res, h, y and the pair x_q, x_s are optional.
 hipError_t launch_add_norm(const uint16_t* x, const uint16_t* res, const void* w, bool w_f32, uint16_t* h,
                            uint16_t* y, uint8_t* x_q, uint8_t* x_s, int T, int H, float eps, hipStream_t s);
-int norm_grad_parts(int T);   // rows of the fp32 workspace [parts, H] of its gradient
+int norm_grad_parts(int T, int H);   // rows of the fp32 workspace [parts, H] of its gradient
 hipError_t launch_add_norm_grad(const uint16_t* dy, const uint16_t* h, const void* w, bool w_f32, const uint16_t* dh,
                                 uint16_t* dx, float* dw, float* parts, int T, int H, float eps, hipStream_t s);
 // out[c] = sum over p of parts[p][c], c < n, in a fixed order.

@@ -11,12 +11,10 @@
 // block and its amax is a 16-lane butterfly.
 #include "device_common.h"
 #include "host_internal.h"
+#include "lane_reduce.h"
 
 namespace moe {
 namespace {
-
-constexpr int kNormThreads = 256;
-constexpr int kNormWaves = kNormThreads / 64;
 
 __device__ __forceinline__ void unpack8(const v4i raw, float (&v)[8]) {
 #pragma unroll
@@ -48,14 +46,13 @@ __device__ __forceinline__ void load_weight8(const void* w, int vec, float (&v)[
   }
 }
 
-// Sum over the workgroup of N values per thread, the same in every thread: lane
-// butterflies, then the waves' sums in wave order.
-template <int N>
+// Sum over a workgroup of WAVES waves of N values per thread, the same in every thread:
+// lane reductions, then the waves' sums in wave order.
+template <int WAVES, int N>
 __device__ __forceinline__ void block_sum(float (&s)[N], float* red) {
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1)
-#pragma unroll
-    for (int n = 0; n < N; ++n) s[n] += __shfl_xor(s[n], m);
+  for (int n = 0; n < N; ++n) s[n] = row_sum<64>(s[n]);
+  if constexpr (WAVES == 1) return;
   if ((threadIdx.x & 63) == 0)
 #pragma unroll
     for (int n = 0; n < N; ++n) red[(threadIdx.x >> 6) * N + n] = s[n];
@@ -64,7 +61,7 @@ __device__ __forceinline__ void block_sum(float (&s)[N], float* red) {
   for (int n = 0; n < N; ++n) {
     s[n] = red[n];
 #pragma unroll
-    for (int w = 1; w < kNormWaves; ++w) s[n] += red[w * N + n];
+    for (int w = 1; w < WAVES; ++w) s[n] += red[w * N + n];
   }
 }
 
@@ -80,17 +77,17 @@ struct NormArgs {
   float eps;
 };
 
-// One workgroup per row; thread t holds vectors t, t + 256, ... (VPT of them, the
+// One workgroup per row; thread t holds vectors t, t + THREADS, ... (VPT of them, the
 // last ones past H / 8 empty).
-template <int VPT, bool WF32>
-__global__ __launch_bounds__(kNormThreads) void k_add_norm(NormArgs a) {
-  __shared__ float red[kNormWaves];
+template <int THREADS, int VPT, bool WF32>
+__global__ __launch_bounds__(THREADS) void k_add_norm(NormArgs a) {
+  __shared__ float red[THREADS / 64];
   const int nv = a.H / 8, tid = threadIdx.x;
   const int64_t row0 = (int64_t)blockIdx.x * a.H;
   float h[VPT][8], s[1] = {0.f};
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int vec = tid + i * kNormThreads;
+    const int vec = tid + i * THREADS;
     if (vec < nv) {
       unpack8(load16_nt(a.x + row0 + vec * 8), h[i]);
       if (a.res) {
@@ -104,11 +101,11 @@ __global__ __launch_bounds__(kNormThreads) void k_add_norm(NormArgs a) {
       if (a.h) *reinterpret_cast<v4i*>(a.h + row0 + vec * 8) = pack8(h[i]);
     }
   }
-  block_sum(s, red);
+  block_sum<THREADS / 64>(s, red);
   const float r = 1.0f / sqrtf(s[0] / (float)a.H + a.eps);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int vec = tid + i * kNormThreads;
+    const int vec = tid + i * THREADS;
     if (vec < nv) {   // H is a multiple of 128: the 16 lanes of a block agree
       float w[8];
       load_weight8<WF32>(a.w, vec, w);
@@ -120,8 +117,7 @@ __global__ __launch_bounds__(kNormThreads) void k_add_norm(NormArgs a) {
       }
       if (a.y) *reinterpret_cast<v4i*>(a.y + row0 + vec * 8) = pack8(h[i]);
       if (a.x_q) {
-#pragma unroll
-        for (int m = 1; m < 16; m <<= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
+        amax = row_max<16>(amax);
         const int e = e8m0_exponent(amax);
         const float inv = exp2_neg(e);
         *reinterpret_cast<uint2*>(a.x_q + row0 + vec * 8) =
@@ -133,85 +129,106 @@ __global__ __launch_bounds__(kNormThreads) void k_add_norm(NormArgs a) {
   }
 }
 
+// Threads per row: four vectors each at most, so that a short row does not leave most
+// of a workgroup idle (64 threads up to H 2048); eight vectors above H 8192.
 template <bool WF32>
-hipError_t add_norm_by_width(const NormArgs& a, int T, hipStream_t s) {
-  const int vpt = (int)ceil_div(a.H / 8, kNormThreads);
-  const dim3 grid((unsigned)T), block(kNormThreads);
-  if (vpt <= 1) hipLaunchKernelGGL((k_add_norm<1, WF32>), grid, block, 0, s, a);
-  else if (vpt <= 2) hipLaunchKernelGGL((k_add_norm<2, WF32>), grid, block, 0, s, a);
-  else if (vpt <= 4) hipLaunchKernelGGL((k_add_norm<4, WF32>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_add_norm<8, WF32>), grid, block, 0, s, a);
+hipError_t launch_fwd(const NormArgs& a, int T, hipStream_t s) {
+  const int nv = a.H / 8;
+  const dim3 grid((unsigned)T);
+  if (nv <= 64) hipLaunchKernelGGL((k_add_norm<64, 1, WF32>), grid, dim3(64), 0, s, a);
+  else if (nv <= 256) hipLaunchKernelGGL((k_add_norm<64, 4, WF32>), grid, dim3(64), 0, s, a);
+  else if (nv <= 512) hipLaunchKernelGGL((k_add_norm<128, 4, WF32>), grid, dim3(128), 0, s, a);
+  else if (nv <= 1024) hipLaunchKernelGGL((k_add_norm<256, 4, WF32>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_add_norm<256, 8, WF32>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 // Gradient. With n = h r and g = dy w:
 //   dx = r (g - n mean_H(g n)) + dh,   dw = sum over rows of dy n.
 // mean(g n) = r mean(g h), so one pass over a row gives both sums. Each workgroup
-// walks rows b, b + gridDim, ... and keeps its part of dw in registers; the parts
-// go to the workspace as [gridDim, H] and k_sum_parts adds them in order.
+// walks rows b, b + gridDim, ..., the next row's values on their way while a row is
+// reduced, and keeps its part of dw in registers; the parts go to the workspace as
+// [gridDim, H] and k_sum_parts adds them in order.
 struct NormGradArgs {
   const uint16_t* dy;
   const uint16_t* h;
   const void* w;
   const uint16_t* dh;   // optional; may be dx
-  uint16_t* dx;
+  uint16_t* dx;         // may be dy
   float* parts;         // [gridDim, H]
   int T, H;
   float eps;
 };
 
-template <int VPT, bool WF32>
-__global__ __launch_bounds__(kNormThreads) void k_add_norm_grad(NormGradArgs a) {
-  __shared__ float red[2][2 * kNormWaves];   // alternating, so one barrier per row is enough
+template <int THREADS, int VPT, bool WF32>
+__global__ __launch_bounds__(THREADS) void k_add_norm_grad(NormGradArgs a) {
+  __shared__ float red[2][2 * (THREADS / 64)];   // alternating, so one barrier per row is enough
   const int nv = a.H / 8, tid = threadIdx.x;
   float dw[VPT][8] = {};
-  int turn = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
-    const int64_t row0 = t * a.H;
-    float h[VPT][8], dy[VPT][8], s[2] = {0.f, 0.f};
+  v4i rh[VPT], ry[VPT], rd[VPT];
+  auto load = [&](int64_t t) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int vec = tid + i * kNormThreads;
-      if (vec < nv) {
-        unpack8(load16_nt(a.h + row0 + vec * 8), h[i]);
-        unpack8(load16_nt(a.dy + row0 + vec * 8), dy[i]);
+      const int vec = tid + i * THREADS;
+      if (vec < nv && t < a.T) {
+        rh[i] = load16_nt(a.h + t * a.H + vec * 8);
+        ry[i] = load16_nt(a.dy + t * a.H + vec * 8);
+        if (a.dh) rd[i] = load16_nt(a.dh + t * a.H + vec * 8);
       }
     }
+  };
+  load(blockIdx.x);
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+    float h[VPT][8], g[VPT][8], o[VPT][8], s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int vec = tid + i * kNormThreads;
+      const int vec = tid + i * THREADS;
+      if (vec < nv) {
+        unpack8(rh[i], h[i]);
+        unpack8(ry[i], g[i]);
+        if (a.dh) {
+          unpack8(rd[i], o[i]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[i][k] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[0] += h[i][k] * h[i][k];
+      }
+    }
+    load(t + gridDim.x);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int vec = tid + i * THREADS;
+      if (vec < nv) {
+        float w[8];
+        load_weight8<WF32>(a.w, vec, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[1] += g[i][k] * w[k] * h[i][k];
+      }
+    }
+    block_sum<THREADS / 64>(s, red[turn]);
+    const float r = 1.0f / sqrtf(s[0] / (float)a.H + a.eps);
+    const float c = r * r * (s[1] / (float)a.H);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int vec = tid + i * THREADS;
       if (vec < nv) {
         float w[8];
         load_weight8<WF32>(a.w, vec, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          s[0] += h[i][k] * h[i][k];
-          s[1] += dy[i][k] * w[k] * h[i][k];
+          o[i][k] += r * (g[i][k] * w[k] - h[i][k] * c);
+          dw[i][k] += g[i][k] * (h[i][k] * r);
         }
-      }
-    }
-    block_sum(s, red[turn]);
-    const float r = 1.0f / sqrtf(s[0] / (float)a.H + a.eps);
-    const float c = r * r * (s[1] / (float)a.H);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int vec = tid + i * kNormThreads;
-      if (vec < nv) {
-        float w[8], o[8] = {};
-        load_weight8<WF32>(a.w, vec, w);
-        if (a.dh) unpack8(load16_nt(a.dh + row0 + vec * 8), o);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          o[k] += r * (dy[i][k] * w[k] - h[i][k] * c);
-          dw[i][k] += dy[i][k] * (h[i][k] * r);
-        }
-        *reinterpret_cast<v4i*>(a.dx + row0 + vec * 8) = pack8(o);
+        *reinterpret_cast<v4i*>(a.dx + t * a.H + vec * 8) = pack8(o[i]);
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int vec = tid + i * kNormThreads;
+    const int vec = tid + i * THREADS;
     if (vec < nv) {
       v4f* dst = reinterpret_cast<v4f*>(a.parts + (int64_t)blockIdx.x * a.H + vec * 8);
       dst[0] = v4f{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
@@ -220,32 +237,37 @@ __global__ __launch_bounds__(kNormThreads) void k_add_norm_grad(NormGradArgs a) 
   }
 }
 
+// Two vectors per thread at most up to H 8192 (the row, the next row and dw in
+// registers), four above.
 template <bool WF32>
-void add_norm_grad_by_width(const NormGradArgs& a, int ctas, hipStream_t s) {
-  const int vpt = (int)ceil_div(a.H / 8, kNormThreads);
-  const dim3 grid((unsigned)ctas), block(kNormThreads);
-  if (vpt <= 1) hipLaunchKernelGGL((k_add_norm_grad<1, WF32>), grid, block, 0, s, a);
-  else if (vpt <= 2) hipLaunchKernelGGL((k_add_norm_grad<2, WF32>), grid, block, 0, s, a);
-  else if (vpt <= 4) hipLaunchKernelGGL((k_add_norm_grad<4, WF32>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_add_norm_grad<8, WF32>), grid, block, 0, s, a);
+void launch_grad(const NormGradArgs& a, int ctas, hipStream_t s) {
+  const int nv = a.H / 8;
+  const dim3 grid((unsigned)ctas);
+  if (nv <= 128) hipLaunchKernelGGL((k_add_norm_grad<64, 2, WF32>), grid, dim3(64), 0, s, a);
+  else if (nv <= 256) hipLaunchKernelGGL((k_add_norm_grad<128, 2, WF32>), grid, dim3(128), 0, s, a);
+  else if (nv <= 512) hipLaunchKernelGGL((k_add_norm_grad<256, 2, WF32>), grid, dim3(256), 0, s, a);
+  else if (nv <= 1024) hipLaunchKernelGGL((k_add_norm_grad<512, 2, WF32>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((k_add_norm_grad<512, 4, WF32>), grid, dim3(512), 0, s, a);
 }
 
 // out[c] = sum over p of parts[p][c], c < n: 64 columns per workgroup; each of its 16
-// waves adds every 16th part, four at a time, then their sums are added in order.
+// waves adds every 16th part, eight at a time, then their sums are added in order.
 constexpr int kSumWaves = 16;
 __global__ __launch_bounds__(64 * kSumWaves) void k_sum_parts(const float* __restrict__ parts, int n_parts, int n,
                                                                float* __restrict__ out) {
   __shared__ float red[kSumWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  float s[8] = {};
   if (c < n)
-    for (int p = wave; p < n_parts; p += 4 * kSumWaves) {
+    for (int p = wave; p < n_parts; p += 8 * kSumWaves) {
+      float v[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (p + u * kSumWaves < n_parts) s[u] += parts[(int64_t)(p + u * kSumWaves) * n + c];
+      for (int u = 0; u < 8; ++u) v[u] = p + u * kSumWaves < n_parts ? parts[(int64_t)(p + u * kSumWaves) * n + c] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s[u] += v[u];
     }
-  red[wave][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+  red[wave][lane] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
   __syncthreads();
   if (wave == 0 && c < n) {
     float sum = red[0][lane];
@@ -259,18 +281,22 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_sum_parts(const float* __res
 hipError_t launch_add_norm(const uint16_t* x, const uint16_t* res, const void* w, bool w_f32, uint16_t* h,
                            uint16_t* y, uint8_t* x_q, uint8_t* x_s, int T, int H, float eps, hipStream_t s) {
   const NormArgs a{x, res, w, h, y, x_q, x_s, H, eps};
-  return w_f32 ? add_norm_by_width<true>(a, T, s) : add_norm_by_width<false>(a, T, s);
+  return w_f32 ? launch_fwd<true>(a, T, s) : launch_fwd<false>(a, T, s);
 }
 
-int norm_grad_parts(int T) { return T < 1024 ? T : 1024; }
+// Workgroups of the gradient: about 16 waves per CU, at most a row each.
+int norm_grad_parts(int T, int H) {
+  const int most = H <= 1024 ? 4096 : H <= 2048 ? 2048 : H <= 4096 ? 1024 : 512;
+  return T < most ? T : most;
+}
 
 hipError_t launch_add_norm_grad(const uint16_t* dy, const uint16_t* h, const void* w, bool w_f32, const uint16_t* dh,
                                 uint16_t* dx, float* dw, float* parts, int T, int H, float eps, hipStream_t s) {
-  const int n = norm_grad_parts(T);
+  const int n = norm_grad_parts(T, H);
   if (n > 0) {
     const NormGradArgs a{dy, h, w, dh, dx, parts, T, H, eps};
-    if (w_f32) add_norm_grad_by_width<true>(a, n, s);
-    else add_norm_grad_by_width<false>(a, n, s);
+    if (w_f32) launch_grad<true>(a, n, s);
+    else launch_grad<false>(a, n, s);
   }
   return launch_sum_parts(parts, n, H, dw, s);
 }

@@ -12,6 +12,7 @@
 
 #include "device_common.h"
 #include "host_internal.h"
+#include "lane_reduce.h"
 
 namespace moe {
 
@@ -85,48 +86,7 @@ __device__ __forceinline__ float load_logit(const void* row, int e) {
                     : reinterpret_cast<const float*>(row)[e]);
 }
 
-// Reductions over the LPR lanes of a row, the result in all of them: within 16 lanes
-// by DPP (xor 1, xor 2, then mirrored halves and rows, which cost no LDS access as a
-// shuffle does), then gfx950's lane-half swaps.
-template <int CTRL>
-__device__ __forceinline__ int dpp(int v) {
-  return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, true);
-}
-template <int LPR, typename F>
-__device__ __forceinline__ int row_reduce(int v, F f) {
-  static_assert(LPR == 16 || LPR == 64, "lanes per row");
-  v = f(v, dpp<0xB1>(v));    // quad_perm [1, 0, 3, 2]
-  v = f(v, dpp<0x4E>(v));    // quad_perm [2, 3, 0, 1]
-  v = f(v, dpp<0x141>(v));   // row_half_mirror
-  v = f(v, dpp<0x140>(v));   // row_mirror
-  if constexpr (LPR == 64) {
-    const auto a = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
-    v = f((int)a[0], (int)a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
-    v = f((int)b[0], (int)b[1]);
-  }
-  return v;
-}
-template <int LPR>
-__device__ __forceinline__ int row_max(int v) {
-  return row_reduce<LPR>(v, [](int a, int b) { return max(a, b); });
-}
-template <int LPR>
-__device__ __forceinline__ int row_min(int v) {
-  return row_reduce<LPR>(v, [](int a, int b) { return min(a, b); });
-}
-template <int LPR>
-__device__ __forceinline__ float row_max(float v) {
-  return __int_as_float(row_reduce<LPR>(__float_as_int(v), [](int a, int b) {
-    return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
-  }));
-}
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
-  return __int_as_float(row_reduce<LPR>(__float_as_int(v), [](int a, int b) {
-    return __float_as_int(__int_as_float(a) + __int_as_float(b));
-  }));
-}
+// Doubles: by shuffles (only rows with close keys, and one sum per workgroup).
 template <int LPR>
 __device__ __forceinline__ double row_max(double v) {
 #pragma unroll
@@ -140,12 +100,25 @@ __device__ __forceinline__ double row_sum(double v) {
   return v;
 }
 
-// d score / d logit, for the scores that depend on their own logit alone.
+// A score that depends on its own logit alone, and its slope d score / d logit, from one
+// exponential: with e = e^-|l| and r = 1 / (1 + e), sigmoid(l) is r or e r, its slope
+// e r^2, and softplus(l) = max(l, 0) + log(1 + e), the logarithm as log(u) e / (u - 1)
+// with u = 1 + e rounded, which takes the rounding of u out again.
 template <int SCORE>
-__device__ __forceinline__ float score_slope(float l, float s) {
-  if constexpr (SCORE == MOE_SCORE_SIGMOID) return s * (1.f / (1.f + expf(l)));
-  // sqrt(softplus): sigmoid(l) / (2 s); far below zero s^2 = e^l, so this is s / 2
-  return l < kFarBelow ? 0.5f * s : 1.f / (1.f + expf(-l)) / (2.f * s);
+__device__ __forceinline__ void score_and_slope(float l, float& s, float& slope) {
+  const float e = exp_f(-fabsf(l)), u = 1.f + e, r = __builtin_amdgcn_rcpf(u);
+  const float sig = l >= 0.f ? r : e * r;
+  if constexpr (SCORE == MOE_SCORE_SIGMOID) {
+    s = sig;
+    slope = e * r * r;
+  } else {
+    const float lg = u == 1.f ? e : __builtin_amdgcn_logf(u) * 0.693147181f * e * __builtin_amdgcn_rcpf(u - 1.f);
+    const float half = exp_f(0.5f * fminf(l, 0.f));
+    const bool far = l < kFarBelow;   // s^2 = e^l there
+    s = far ? half : sqrtf(fmaxf(l, 0.f) + lg);
+    slope = far ? 0.5f * half : sig * 0.5f * __builtin_amdgcn_rcpf(s);
+  }
+  if (l == kNone) s = slope = 0.f;
 }
 
 // Calls f with (LPR, NV) as integral constants: 16 lanes per row for at most 512
@@ -156,13 +129,17 @@ struct Int {
   static constexpr int value = V;
 };
 template <typename F>
+void by_few_experts(int E, F f) {   // 16 lanes per row, E <= 512
+  if (E <= 64) f(Int<1>{});
+  else if (E <= 128) f(Int<2>{});
+  else if (E <= 256) f(Int<4>{});
+  else if (E <= 384) f(Int<6>{});
+  else f(Int<8>{});
+}
+template <typename F>
 void by_experts(int E, bool wide, F f) {
   if (E <= 512 && !wide) {
-    if (E <= 64) f(Int<16>{}, Int<1>{});
-    else if (E <= 128) f(Int<16>{}, Int<2>{});
-    else if (E <= 256) f(Int<16>{}, Int<4>{});
-    else if (E <= 384) f(Int<16>{}, Int<6>{});
-    else f(Int<16>{}, Int<8>{});
+    by_few_experts(E, [&](auto nv) { f(Int<16>{}, nv); });
   } else {
     if (E <= 512) f(Int<64>{}, Int<2>{});
     else if (E <= 1024) f(Int<64>{}, Int<4>{});

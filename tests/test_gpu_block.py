@@ -472,8 +472,9 @@ def test_balance_loss_masks_and_empty(dev, score):
 
 
 def test_balance_loss_no_tokens(dev):
-    loss, counts, dl = moe.balance_loss(torch.empty(0, 8, device=dev), torch.empty(0, 2, dtype=torch.int32, device=dev), 1.0)
-    assert float(loss) == 0 and bool((counts == 0).all()) and dl.shape == (0, 8)
+    for E in (8, 600):
+        loss, counts, dl = moe.balance_loss(torch.empty(0, E, device=dev), torch.empty(0, 2, dtype=torch.int32, device=dev), 1.0)
+        assert float(loss) == 0 and bool((counts == 0).all()) and dl.shape == (0, E)
 
 
 def test_balance_loss_unordered_offsets_stay_in_bounds(dev):
