@@ -420,16 +420,19 @@ def ffn_quantized(x_q: torch.Tensor, x_s: torch.Tensor, topk_weights: torch.Tens
 
 # ------------------------------------------------------------------ in front of the FFN
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # absent in CPU-only builds of torch
+
+
 def _enqueue(name: str, dev: torch.device, *args):
     """Call an entry point with the current stream of `dev` as its last argument, with
     that device current, so that tensors may live on another than the current one."""
     fn = getattr(_lib or lib(), name)
     index = dev.index
     if index == torch.cuda.current_device():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            rc = fn(*args, _raw_stream(index))
     if rc != MOE_OK:
         raise MoEError(rc, name)
 
@@ -487,22 +490,31 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     wt = _one_of(TYPES, weight.dtype, "weight type")
     wp = _tensor(weight, weight.dtype, (H,), dev, "weight")
     h, y, q, s = out if out is not None else (None, None, None, None)
+    hp = yp = qp = sp = None
     if residual is None:
-        h, hp = x, None
+        h = x
+    elif h is None:
+        h = torch.empty_like(x)
+        hp = h.data_ptr()
     else:
-        h = torch.empty_like(x) if h is None else h
         hp = _tensor(h, torch.bfloat16, shape, dev, "out.h")
-    if bf16:
-        y = torch.empty_like(x) if y is None else y
-    else:
+    if not bf16:
         y = None
-    if fp8:
-        q = torch.empty(shape, dtype=torch.uint8, device=dev) if q is None else q
-        s = torch.empty((T, H // 128), dtype=torch.uint8, device=dev) if s is None else s
+    elif y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
     else:
+        yp = _tensor(y, torch.bfloat16, shape, dev, "out.y")
+    if not fp8:
         q = s = None
-    _enqueue("moe_add_norm", dev, T, H, eps, xp, rp, wp, wt, hp, _tensor(y, torch.bfloat16, shape, dev, "out.y"),
-             _tensor(q, torch.uint8, shape, dev, "out.x_q"), _tensor(s, torch.uint8, (T, H // 128), dev, "out.x_s"))
+    else:
+        if q is None:
+            q = torch.empty(shape, dtype=torch.uint8, device=dev)
+        if s is None:
+            s = torch.empty((T, H // 128), dtype=torch.uint8, device=dev)
+        qp = _tensor(q, torch.uint8, shape, dev, "out.x_q")
+        sp = _tensor(s, torch.uint8, (T, H // 128), dev, "out.x_s")
+    _enqueue("moe_add_norm", dev, T, H, eps, xp, rp, wp, wt, hp, yp, qp, sp)
     return Normed(h, y, q, s)
 
 

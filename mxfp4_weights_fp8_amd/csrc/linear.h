@@ -29,11 +29,12 @@ struct LinearArgs {
 };
 enum class Layout { kRows, kWTrans, kBothTrans };   // neither, w, or both as [C, rows]
 
-// How a product runs: `small` (weights streamed, the contraction split over the waves
-// of a workgroup), or in tiles of 32 ft rows x 32 fw columns, the contraction split
-// `splits` times over workgroups.
+// How a product runs: few rows on the vector units (kDot) or with the weights streamed
+// past the matrix cores (kSmall), or in tiles of 32 ft rows x 32 fw columns; the
+// contraction split `splits` times over workgroups (kSmall and kTiles).
+enum class Path { kDot, kSmall, kTiles };
 struct LinearPlan {
-  bool small;
+  Path path;
   int ft, fw, splits;
 };
 LinearPlan linear_plan(int M, int N, int C, Layout l);
@@ -83,7 +84,7 @@ __device__ __forceinline__ float activate_slope(float z, int act) {
   }
 }
 
-// The epilogue of V (4 or 8) neighbouring columns n .. n + V - 1 of row m, those below
+// The epilogue of V (1, 4 or 8) neighbouring columns n .. n + V - 1 of row m, those below
 // N. The residual is loaded apart, so that a caller can have several on their way.
 template <int V>
 struct Residual {
@@ -97,21 +98,21 @@ __device__ __forceinline__ Residual<V> load_residual(const LinearArgs& a, int64_
   for (int i = 0; i < V; ++i) r.v[i] = 0.f;
   if (!a.res || m >= a.M || n >= a.N) return r;
   const int64_t at = m * a.N + n;
-  if (a.N % V == 0) {
+  if (V > 1 && a.N % V == 0) {
     if (a.out_f32) {
 #pragma unroll
-      for (int k = 0; k < V; k += 4) {
+      for (int k = 0; k < V / 4 * 4; k += 4) {
         const v4f t = *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(a.res) + at + k);
 #pragma unroll
         for (int i = 0; i < 4; ++i) r.v[k + i] = t[i];
       }
     } else {
-      uint32_t t[V / 2];
+      uint32_t t[V / 2 + 1];
       if constexpr (V == 8) {
         const v4i x = *reinterpret_cast<const v4i*>(reinterpret_cast<const uint16_t*>(a.res) + at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] = (uint32_t)x[i];
-      } else {
+      } else if constexpr (V == 4) {
         const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.res) + at);
         t[0] = x.x;
         t[1] = x.y;
@@ -150,16 +151,16 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int64_t m, int n, fl
   activate(v, a.act);
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = a.res ? v[i] + r.v[i] : v[i];
-  if (whole && a.out_f32) {
+  if (V > 1 && whole && a.out_f32) {
 #pragma unroll
-    for (int k = 0; k < V; k += 4)
+    for (int k = 0; k < V / 4 * 4; k += 4)
       *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + at + k) = v4f{v[k], v[k + 1], v[k + 2], v[k + 3]};
-  } else if (whole) {
+  } else if (V > 1 && whole) {
     uint16_t* dst = reinterpret_cast<uint16_t*>(a.y) + at;
     if constexpr (V == 8)
       *reinterpret_cast<v4i*>(dst) = v4i{(int)bf16_pack2(v[0], v[1]), (int)bf16_pack2(v[2], v[3]),
                                          (int)bf16_pack2(v[4], v[5]), (int)bf16_pack2(v[6], v[7])};
-    else
+    else if constexpr (V == 4)
       *reinterpret_cast<uint2*>(dst) = make_uint2(bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]));
   } else {
 #pragma unroll
@@ -168,6 +169,22 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int64_t m, int n, fl
         if (a.out_f32) reinterpret_cast<float*>(a.y)[at + i] = v[i];
         else reinterpret_cast<uint16_t*>(a.y)[at + i] = (uint16_t)bf16_pack2(v[i], 0.f);
       }
+  }
+}
+
+// Partial sums of V (4 or 8) neighbouring columns of a split product.
+template <int V>
+__device__ __forceinline__ void store_part(const LinearArgs& a, int split, int64_t m, int n, const float (&v)[V]) {
+  if (m >= a.M || n >= a.N) return;
+  float* dst = a.parts + ((int64_t)split * a.M + m) * a.N + n;
+  if (a.N % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < V; k += 4)
+      if (n + k < a.N) *reinterpret_cast<v4f*>(dst + k) = v4f{v[k], v[k + 1], v[k + 2], v[k + 3]};
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (n + k < a.N) dst[k] = v[k];
   }
 }
 

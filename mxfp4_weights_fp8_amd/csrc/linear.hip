@@ -7,6 +7,7 @@
 // (c, q) = (l % 16, l / 16) holds columns 4q .. 4q+3 of token c: each lane stores
 // four neighbouring outputs.
 #include "linear.h"
+#include "lane_reduce.h"
 
 namespace moe {
 namespace {
@@ -18,11 +19,68 @@ __device__ __forceinline__ v4f mfma_bf16(const v4i a, const v4i b, v4f c) {
 }
 
 // ------------------------------------------------------------------ few rows
-// At most 64 rows: bound by reading the weights (or by latency). A workgroup owns 16
-// output columns; its waves take every W-th step of 64 K, straight from memory into
-// registers, and add their sums through LDS in wave order. Lane (c, q) reads bytes
-// 32q .. 32q+31 of its row's 128-byte step: as K is summed, the two operands only
-// have to agree on which K a lane holds.
+// At most 8 rows and few columns (a router's decode step): bound by latency, so the
+// weights are spread over as many CUs as give each workgroup R columns, and every load
+// of a wave is in flight at once. A lane multiplies 8 of a 512-long chunk of K (wave w
+// takes chunks w, w + waves, ...) in fp32: R weights' and MT rows' 16 bytes give R MT
+// sums, added over the lanes, then over the waves in order.
+// 7 x 384 x 7168: 24 workgroups of 16 columns on the matrix cores took 12.3 us.
+constexpr int kDotWaves = 16;
+
+__device__ __forceinline__ void unpack8(const v4i raw, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float((uint32_t)raw[i] << 16);
+    v[2 * i + 1] = __uint_as_float((uint32_t)raw[i] & 0xFFFF0000u);
+  }
+}
+
+template <int MT, int R>
+__global__ __launch_bounds__(64 * kDotWaves) void k_linear_dot(LinearArgs a) {
+  __shared__ float red[kDotWaves][MT * R];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int n0 = blockIdx.x * R;
+  float acc[MT][R] = {};
+  for (int k = (wave * 64 + lane) * 8; k < a.C; k += waves * 512) {
+    v4i wv[R], xv[MT];
+#pragma unroll
+    for (int r = 0; r < R; ++r) wv[r] = load16(a.w + min(n0 + r, a.N - 1) * a.ws + k);   // rows past the end: any valid row
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xv[m] = load16(a.x + min(m, a.M - 1) * a.xs + k);
+    float wf[R][8];
+#pragma unroll
+    for (int r = 0; r < R; ++r) unpack8(wv[r], wf[r]);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float xf[8];
+      unpack8(xv[m], xf);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[m][r] += xf[i] * wf[r][i];
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float s = row_sum<64>(acc[m][r]);
+      if (lane == 0) red[wave][m * R + r] = s;
+    }
+  __syncthreads();
+  if (threadIdx.x < MT * R) {
+    float v[1] = {red[0][threadIdx.x]};
+    for (int w = 1; w < waves; ++w) v[0] += red[w][threadIdx.x];
+    const int m = threadIdx.x / R, n = n0 + threadIdx.x % R;
+    finish<1>(a, m, n, v, load_residual<1>(a, m, n));
+  }
+}
+
+// At most 64 rows: bound by reading the weights. A workgroup owns 16 output columns and
+// one of a.splits shares of the contraction; its waves take every W-th step of 64 K,
+// straight from memory into registers, and add their sums through LDS in wave order.
+// Lane (c, q) reads bytes 32q .. 32q+31 of its row's 128-byte step: as K is summed, the
+// two operands only have to agree on which K a lane holds.
 constexpr int kSmallWaves = 16;
 
 template <int FT>
@@ -31,13 +89,14 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_linear_small(LinearArgs a)
   extern __shared__ __attribute__((aligned(16))) float red[];   // [wave][FT][64 lanes][4]
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const int n0 = blockIdx.x * 16, steps = a.C / 64;
+  const int n0 = blockIdx.x * 16, split = blockIdx.y;
+  const int first = a.C / 64 * split / a.splits, steps = a.C / 64 * (split + 1) / a.splits;
   const uint16_t* w = a.w + (int64_t)min(n0 + c, a.N - 1) * a.ws + q * 16;   // rows past the end: any valid row
   const uint16_t* x[FT];
 #pragma unroll
   for (int f = 0; f < FT; ++f) x[f] = a.x + (int64_t)min(16 * f + c, a.M - 1) * a.xs + q * 16;
   v4f acc[FT] = {};
-  for (int s = wave; s < steps; s += waves * kSmallDepth) {
+  for (int s = first + wave; s < steps; s += waves * kSmallDepth) {
     v4i wv[kSmallDepth][2], xv[kSmallDepth][FT][2];
 #pragma unroll
     for (int d = 0; d < kSmallDepth; ++d) {
@@ -70,7 +129,8 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_linear_small(LinearArgs a)
     const int f = i >> 6, l = i & 63;
     const int m = 16 * f + (l & 15), n = n0 + 4 * (l >> 4);
     float o[4] = {v[0], v[1], v[2], v[3]};
-    finish<4>(a, m, n, o, load_residual<4>(a, m, n));
+    if (a.splits == 1) finish<4>(a, m, n, o, load_residual<4>(a, m, n));
+    else store_part<4>(a, split, m, n, o);
   }
 }
 
@@ -106,12 +166,19 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a) {
 // us, 128 x 128 971; 8191 x 7168 x 2048: 310 and 266; 4096 x 2048 x 7168: 256 x 256 split
 // in two 112, 128 x 128 110, unsplit 256 x 256 168.)
 LinearPlan linear_plan(int M, int N, int C, Layout l) {
-  if (M <= 64 && l == Layout::kRows) return LinearPlan{true, 0, 0, 1};
+  if (M <= 64 && l == Layout::kRows) {
+    const int64_t tiles = ceil_div(N, 16), steps = C / 64;
+    if (M <= 8 && N <= 2048) return LinearPlan{Path::kDot, 0, 0, 1};
+    // fewer workgroups than CUs: split the contraction, at least 8 steps each
+    int64_t splits = 256 / tiles;
+    if (splits > steps / 8) splits = steps / 8;
+    return LinearPlan{Path::kSmall, 0, 0, splits > 1 ? (int)splits : 1};
+  }
   static const struct {
     int ft, fw, per_cu, step, fixed;
   } kShapes[] = {{8, 8, 1, 170, 2200}, {8, 6, 1, 145, 1500}, {6, 8, 1, 145, 1500}, {4, 4, 2, 98, 800}};
   const int64_t steps = ceil_div(C, 64);
-  LinearPlan best{false, 0, 0, 1};
+  LinearPlan best{Path::kTiles, 0, 0, 1};
   int64_t least = -1;
   for (const auto& t : kShapes) {
     const int64_t tiles = ceil_div(M, 32 * t.ft) * ceil_div(N, 32 * t.fw), slots = 256 * t.per_cu;
@@ -120,7 +187,7 @@ LinearPlan linear_plan(int M, int N, int C, Layout l) {
       if (splits > 1) time += 400 + splits * M * N * 8 / 40000;
       if (least < 0 || time < least) {
         least = time;
-        best = LinearPlan{false, t.ft, t.fw, (int)splits};
+        best = LinearPlan{Path::kTiles, t.ft, t.fw, (int)splits};
       }
     }
   }
@@ -138,18 +205,33 @@ size_t linear_parts_bytes(int M, int N, int K) {
 hipError_t launch_linear_plan(const LinearArgs& in, const LinearPlan& p, Layout l, hipStream_t s) {
   LinearArgs a = in;
   a.splits = p.splits;
-  if (p.small) {
-    const int steps = a.C / 64;
+  if (p.path == Path::kDot) {
+    const int64_t chunks = ceil_div(a.C, 512);
+    const dim3 block(64 * (unsigned)(chunks < kDotWaves ? chunks : kDotWaves));
+    auto run = [&](auto kernel, int r) { hipLaunchKernelGGL(kernel, dim3((unsigned)ceil_div(a.N, r)), block, 0, s, a); };
+    if (a.N <= 768) {   // 192 workgroups for 384 columns
+      if (a.M == 1) run(k_linear_dot<1, 2>, 2);
+      else if (a.M <= 4) run(k_linear_dot<4, 2>, 2);
+      else run(k_linear_dot<8, 2>, 2);
+    } else {
+      if (a.M == 1) run(k_linear_dot<1, 4>, 4);
+      else if (a.M <= 4) run(k_linear_dot<4, 4>, 4);
+      else run(k_linear_dot<8, 4>, 4);
+    }
+    return hipGetLastError();
+  }
+  if (p.path == Path::kSmall) {
+    const int steps = (int)ceil_div(a.C / 64, p.splits);
     const int waves = steps < kSmallWaves ? steps : kSmallWaves;
-    const dim3 grid((unsigned)ceil_div(a.N, 16)), block(64 * waves);
+    const dim3 grid((unsigned)ceil_div(a.N, 16), p.splits), block(64 * waves);
     const int ft = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
     const size_t lds = (size_t)waves * ft * 1024;
     if (ft == 1) hipLaunchKernelGGL(k_linear_small<1>, grid, block, lds, s, a);
     else if (ft == 2) hipLaunchKernelGGL(k_linear_small<2>, grid, block, lds, s, a);
     else hipLaunchKernelGGL(k_linear_small<4>, grid, block, lds, s, a);
-    return hipGetLastError();
+  } else {
+    launch_tiles(a, p, l, s);
   }
-  launch_tiles(a, p, l, s);
   if (p.splits > 1) {
     const int64_t n = (int64_t)a.M * ceil_div(a.N, 4);
     hipLaunchKernelGGL(k_linear_join, dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, s, a);

@@ -291,16 +291,8 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
         float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         if (a.splits == 1) {
           finish<8>(a, m, n, v, res[u]);
-        } else if (m < a.M && n < a.N) {
-          float* dst = a.parts + ((int64_t)split * a.M + m) * a.N + n;
-          if (a.N % 4 == 0) {
-            *reinterpret_cast<v4f*>(dst) = lo;
-            if (n + 4 < a.N) *reinterpret_cast<v4f*>(dst + 4) = hi;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (n + k < a.N) dst[k] = v[k];
-          }
+        } else {
+          store_part<8>(a, split, m, n, v);
         }
       }
     }
