@@ -22,30 +22,30 @@
 namespace moe {
 namespace {
 
-constexpr int kNoKey = -0x7FFFFFFF - 1;   // a masked expert, or a key that is taken
+constexpr int kNoKey = (int)0x807FFFFF;   // to_key(-inf): a masked expert, or a key that is taken
 constexpr int kNoIndex = 0x7FFFFFFF;
 
-// Floats as integers of the same order (-0 counts as 0).
+// Floats as integers of the same order (-0 counts as 0, NaN as -inf).
 __device__ __forceinline__ int to_key(float f) {
-  const int b = __float_as_int(f + 0.f);
+  const int b = __float_as_int(fmaxf(f, kNone) + 0.f);
   return b ^ ((b >> 31) & 0x7FFFFFFF);
 }
 __device__ __forceinline__ float from_key(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)); }
 
 // Scores from the hardware's exp2, log2, rcp and sqrt (1 ulp each): the product
 // l log2(e) is off by 2^-24 of itself, at most 127 * 2^-24 where e^l is not out of
-// range, so e^l is off by at most 6e-6 of itself, and 1 + e^l, its reciprocal, its
-// logarithm (from a series where e^l is below 0.01: at most 7e-6 of log(1 + e^l))
-// and its root by no more. Results below 2^-126 are 0 (1e-19 after the root).
-constexpr float kSlack = 1.5e-5f;   // twice that, relative to score + |bias|
+// range, so e^l is off by at most 6e-6 of itself, and what follows by no more:
+// kSlack (score + |bias|) is twice a key's error. One exception: 1 + e^l of
+// sqrt(softplus) is rounded to 2^-24, which moves a score s below kLowScore by up to
+// 2^-25 / s, or s itself where that is less: by up to 2.5e-4 (kLowSlack is twice
+// that).
+constexpr float kSlack = 1.5e-5f, kLowScore = 0.1f, kLowSlack = 5e-4f;
 template <int SCORE>
 __device__ __forceinline__ float score_fast(float l) {
   if constexpr (SCORE == MOE_SCORE_SIGMOID)
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l * -kLog2e));
   const float e = __builtin_amdgcn_exp2f(fabsf(l) * -kLog2e);
-  const float series = e * (1.f - e * (0.5f - e * 0.333333333f));
-  const float full = __builtin_amdgcn_logf(1.f + e) * 0.693147181f;
-  return __builtin_amdgcn_sqrtf(fmaxf(l, 0.f) + (e < 0.01f ? series : full));
+  return __builtin_amdgcn_sqrtf(fmaxf(l, 0.f) + __builtin_amdgcn_logf(1.f + e) * 0.693147181f);
 }
 template <int SCORE>
 __device__ __forceinline__ double score_f64(double l, double top, double inv_sum) {
@@ -116,11 +116,10 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
   };
   if constexpr (SCORE == MOE_SCORE_SOFTMAX) softmax();
 
-  int best_of[NV];   // largest key of each group
-  float slack = 0.f;
+  int best_of[NV];       // largest key of each group
+  float bias_size = 0.f;  // largest |bias| of the row's unmasked experts
   if (a.bias) {
     const float inv_sum = 1.f / sum;
-    float size = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int e0 = 4 * (j * LPR + lane);
@@ -135,25 +134,31 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
       v4i k;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float b = bias[i];
         const bool masked = SCORE == MOE_SCORE_SOFTMAX ? l[j][i] < 0.f : l[j][i] == kNone;
         float s;
         if constexpr (SCORE == MOE_SCORE_SOFTMAX) s = l[j][i] * inv_sum;
         else s = score_fast<SCORE>(l[j][i]);
-        const float key = s + b;
-        k[i] = masked || !(key > kNone) ? kNoKey : to_key(key);
-        size = fmaxf(size, k[i] == kNoKey ? 0.f : s + fabsf(b));
+        k[i] = to_key(masked ? kNone : s + bias[i]);
       }
       groups[j][threadIdx.x] = k;
       best_of[j] = max(max(k[0], k[1]), max(k[2], k[3]));
+      bias_size = fmaxf(fmaxf(bias_size, fmaxf(fabsf(bias[0]), fabsf(bias[1]))), fmaxf(fabsf(bias[2]), fabsf(bias[3])));
     }
-    slack = kSlack * row_max<LPR>(size) + 1e-18f;
+    bias_size = row_max<LPR>(bias_size);
+    if (bias_size == INFINITY) {   // experts masked by their bias: the largest of the others
+      bias_size = 0.f;
+      for (int e = lane; e < a.E; e += LPR) {
+        const float b = a.bias[e];
+        bias_size = b == kNone || !(b == b) ? bias_size : fmaxf(bias_size, fabsf(b));
+      }
+      bias_size = row_max<LPR>(bias_size);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       v4i k;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) k[i] = l[j][i] == kNone ? kNoKey : to_key(l[j][i]);
+      for (int i = 0; i < 4; ++i) k[i] = to_key(l[j][i]);
       groups[j][threadIdx.x] = k;
       best_of[j] = max(max(k[0], k[1]), max(k[2], k[3]));
     }
@@ -198,21 +203,30 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
       mine = j == lane ? index : mine;
     }
   } else {
-    bool more = true, close = false;
-    float before = INFINITY, least = kNone;   // the key before, and what a candidate needs from K on
+    bool more = true;
+    // the key before, the smallest step between keys, the errors' bound (from the best
+    // key: no score is above it by more than bias_size), and what a candidate needs
+    // once there are K
+    float before = INFINITY, step = INFINITY, slack = 0.f, least = kNone;
     for (int j = 0; j < LPR && __any(more); ++j) {
       const int best = row_best();
-      const float f = best == kNoKey ? kNone : from_key(best);
+      const float f = from_key(best);
       more = more && best != kNoKey && !(f < least);
       if (!more) continue;   // the same in all lanes of the row
-      close = close || !(before - f > slack);
+      if (j == 0) slack = kSlack * (fabsf(f) + 2.f * bias_size) + 1e-18f;
+      if (j == a.K - 1) {
+        if (SCORE == MOE_SCORE_SQRTSOFTPLUS && !(f > kLowScore + kLowSlack + bias_size + slack)) slack += kLowSlack;
+        least = f - slack;
+      }
+      step = fminf(step, before - f);
       before = f;
       const int index = take(best);
       mine = j == lane ? index : mine;
-      if (j == a.K - 1) least = f - slack;
     }
+    if (SCORE == MOE_SCORE_SQRTSOFTPLUS && least == kNone) slack += kLowSlack;   // fewer than K experts
     const int left = row_best();
     const bool crowd = more && left != kNoKey && !(from_key(left) < least);
+    const bool close = !(step > slack);
     if (close || crowd) {
       double dtop = top, inv = 1.0;
       if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
@@ -262,7 +276,7 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
 
   // weight of the lane's pick, from its logit again
   const bool pick = pos < a.K;
-  const float s = !pick || mine == kNoIndex ? 0.f : score_f32<SCORE>(load_logit<BF16>(row, mine), top, sum);
+  const float s = !pick || mine == kNoIndex ? 0.f : score_of<SCORE>(load_logit<BF16>(row, mine), top, sum);
   float mul = a.scale;
   if (a.renorm) mul = a.scale / (row_sum<LPR>(s) + 1e-20f);
   if (pick) {

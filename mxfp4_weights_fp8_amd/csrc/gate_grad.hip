@@ -52,7 +52,7 @@ __global__ __launch_bounds__(kGateThreads) void k_gate_grad(GateGradArgs a) {
   if (id < 0 || id >= a.E) id = -1;
   const float lg = id >= 0 ? load_logit<BF16>(row, id) : kNone;
   float s, slope = 0.f;
-  if constexpr (SCORE == MOE_SCORE_SOFTMAX) s = score_f32<SCORE>(lg, top, sum);
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) s = score_of<SCORE>(lg, top, sum);
   else score_and_slope<SCORE>(lg, s, slope);
   float dc = id >= 0 ? a.dw[t * a.K + lane] : 0.f;
   if (a.renorm) {

@@ -31,21 +31,8 @@ __device__ __forceinline__ float exp_f(float x) {
   return __builtin_fmaf(e, err * 0.693147181f, e);
 }
 
-// A score as a function of its own logit (softmax: also of the row's largest logit
-// `top` and the sum of e^(l - top)).
-template <int SCORE>
-__device__ __forceinline__ float score_f32(float l, float top, float sum) {
-  if (l == kNone) return 0.f;
-  if constexpr (SCORE == MOE_SCORE_SOFTMAX) return expf(l - top) / sum;
-  if constexpr (SCORE == MOE_SCORE_SIGMOID) return 1.f / (1.f + expf(-l));
-  if (l < kFarBelow) return expf(0.5f * l);
-  return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
-}
-
-__device__ __forceinline__ float clean(float l) {   // NaN -> masked, +inf -> largest float
-  l = l == l ? l : kNone;
-  return fminf(l, FLT_MAX);
-}
+// NaN -> masked (the maximum is the other operand), +inf -> largest float
+__device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, kNone), FLT_MAX); }
 
 // Four logits of experts e0 .. e0 + 3 of a row; experts from E on are masked.
 template <bool BF16, bool VEC>
@@ -119,6 +106,16 @@ __device__ __forceinline__ void score_and_slope(float l, float& s, float& slope)
     slope = far ? 0.5f * half : sig * 0.5f * __builtin_amdgcn_rcpf(s);
   }
   if (l == kNone) s = slope = 0.f;
+}
+
+// The score of one logit (softmax: with the row's largest logit and the sum of
+// e^(l - top)).
+template <int SCORE>
+__device__ __forceinline__ float score_of(float l, float top, float sum) {
+  float s, slope;
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) s = l == kNone ? 0.f : exp_f(l - top) / sum;
+  else score_and_slope<SCORE>(l, s, slope);
+  return s;
 }
 
 // Calls f with (LPR, NV) as integral constants: 16 lanes per row for at most 512
