@@ -30,16 +30,20 @@ struct LinearArgs {
 enum class Layout { kRows, kWTrans, kBothTrans };   // neither, w, or both as [C, rows]
 
 // How a product runs: few rows on the vector units (kDot) or with the weights streamed
-// past the matrix cores (kSmall), or in tiles of 32 ft rows x 32 fw columns; the
+// past the matrix cores (kSmall), a contraction of at most 384 with rows of x kept in
+// registers (kShort), or in tiles of 32 ft rows x 32 fw columns; the
 // contraction split `splits` times over workgroups (kSmall and kTiles).
-enum class Path { kDot, kSmall, kTiles };
+enum class Path { kDot, kSmall, kShort, kTiles };
 struct LinearPlan {
   Path path;
   int ft, fw, splits;
 };
-LinearPlan linear_plan(int M, int N, int C, Layout l);
+// plain: no bias, residual, activation or z.
+LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain);
 size_t linear_plan_parts(int M, int N, const LinearPlan& p);   // bytes of `parts`
 hipError_t launch_linear_plan(const LinearArgs& a, const LinearPlan& p, Layout l, hipStream_t s);
+int short_tiles_per_cta(int M, int N);
+void launch_short(const LinearArgs& a, Layout l, hipStream_t s);
 void launch_tiles(const LinearArgs& a, const LinearPlan& p, Layout l, hipStream_t s);
 
 __device__ __forceinline__ float sigmoid_f(float z) { return 1.f / (1.f + expf(-z)); }
@@ -169,6 +173,65 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int64_t m, int n, fl
         if (a.out_f32) reinterpret_cast<float*>(a.y)[at + i] = v[i];
         else reinterpret_cast<uint16_t*>(a.y)[at + i] = (uint16_t)bf16_pack2(v[i], 0.f);
       }
+  }
+}
+
+// The tiled kernels' epilogue of products without activation and without z, N a multiple
+// of 8: bias and residual only, little code, so that it unrolls. RES: there is a
+// residual; F32: of y and the residual.
+inline __device__ bool is_affine(const LinearArgs& a) { return a.N % 8 == 0 && !a.z && a.act == MOE_ACT_NONE; }
+
+template <bool RES, bool F32>
+struct Residual8 {
+  v4i r[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const LinearArgs& a, int64_t m, int n) {
+    if (!RES || m >= a.M || n >= a.N) return;
+    const char* p = reinterpret_cast<const char*>(a.res) + (m * a.N + n) * (F32 ? 4 : 2);
+    r[0] = load16(p);
+    if constexpr (F32) r[1] = load16(p + 16);
+  }
+};
+
+template <bool BIAS = true, bool RES, bool F32>
+__device__ __forceinline__ void finish_affine(const LinearArgs& a, int64_t m, int n, v4f lo, v4f hi,
+                                              const Residual8<RES, F32>& res) {
+  if (m >= a.M || n >= a.N) return;
+  if (BIAS && a.bias) {
+    lo += *reinterpret_cast<const v4f*>(a.bias + n);
+    hi += *reinterpret_cast<const v4f*>(a.bias + n + 4);
+  }
+  char* p = reinterpret_cast<char*>(a.y) + (m * a.N + n) * (F32 ? 4 : 2);
+  if constexpr (F32) {
+    if constexpr (RES) {
+      lo += __builtin_bit_cast(v4f, res.r[0]);
+      hi += __builtin_bit_cast(v4f, res.r[1]);
+    }
+    *reinterpret_cast<v4f*>(p) = lo;
+    *reinterpret_cast<v4f*>(p + 16) = hi;
+  } else {
+    v4i o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v0 = i < 2 ? lo[2 * i] : hi[2 * i - 4], v1 = i < 2 ? lo[2 * i + 1] : hi[2 * i - 3];
+      if constexpr (RES) {
+        v0 += __uint_as_float((uint32_t)res.r[0][i] << 16);
+        v1 += __uint_as_float((uint32_t)res.r[0][i] & 0xFFFF0000u);
+      }
+      o[i] = (int)bf16_pack2(v0, v1);
+    }
+    *reinterpret_cast<v4i*>(p) = o;
+  }
+}
+
+// Calls f<RES, F32>() for a product's residual and type.
+template <typename F>
+__device__ __forceinline__ void by_affine(const LinearArgs& a, F f) {
+  if (a.res) {
+    if (a.out_f32) f(Residual8<true, true>{});
+    else f(Residual8<true, false>{});
+  } else {
+    if (a.out_f32) f(Residual8<false, true>{});
+    else f(Residual8<false, false>{});
   }
 }
 

@@ -165,7 +165,7 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a) {
 // parts of a split product 4 us and its traffic at 4 TB/s. (8192^3: 256 x 256 tiles 851
 // us, 128 x 128 971; 8191 x 7168 x 2048: 310 and 266; 4096 x 2048 x 7168: 256 x 256 split
 // in two 112, 128 x 128 110, unsplit 256 x 256 168.)
-LinearPlan linear_plan(int M, int N, int C, Layout l) {
+LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain) {
   if (M <= 64 && l == Layout::kRows) {
     const int64_t tiles = ceil_div(N, 16), steps = C / 64;
     if (M <= 8 && N <= 2048) return LinearPlan{Path::kDot, 0, 0, 1};
@@ -191,6 +191,11 @@ LinearPlan linear_plan(int M, int N, int C, Layout l) {
       }
     }
   }
+  if (C <= 384 && N % 8 == 0 && plain && l != Layout::kBothTrans) {   // C is a multiple of 128
+    const int64_t n_tiles = ceil_div(N, 128), per = short_tiles_per_cta(M, N);
+    const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(n_tiles, per), 256);
+    if (rounds * (500 + per * (steps * 45 + 70)) < least) return LinearPlan{Path::kShort, 0, 0, 1};
+  }
   return best;
 }
 
@@ -198,8 +203,10 @@ size_t linear_plan_parts(int M, int N, const LinearPlan& p) {
   return p.splits > 1 ? sizeof(float) * (size_t)p.splits * M * N : 0;
 }
 
-size_t linear_parts_bytes(int M, int N, int K) {
-  return linear_plan_parts(M, N, linear_plan(M, N, K, Layout::kRows));
+size_t linear_parts_bytes(int M, int N, int K) {   // the larger of the two plans
+  const size_t a = linear_plan_parts(M, N, linear_plan(M, N, K, Layout::kRows, false)),
+               b = linear_plan_parts(M, N, linear_plan(M, N, K, Layout::kRows, true));
+  return a > b ? a : b;
 }
 
 hipError_t launch_linear_plan(const LinearArgs& in, const LinearPlan& p, Layout l, hipStream_t s) {
@@ -229,6 +236,8 @@ hipError_t launch_linear_plan(const LinearArgs& in, const LinearPlan& p, Layout 
     if (ft == 1) hipLaunchKernelGGL(k_linear_small<1>, grid, block, lds, s, a);
     else if (ft == 2) hipLaunchKernelGGL(k_linear_small<2>, grid, block, lds, s, a);
     else hipLaunchKernelGGL(k_linear_small<4>, grid, block, lds, s, a);
+  } else if (p.path == Path::kShort) {
+    launch_short(a, l, s);
   } else {
     launch_tiles(a, p, l, s);
   }
@@ -243,7 +252,8 @@ hipError_t launch_linear(const moe_linear_dims& d, const uint16_t* x, const uint
                          const void* res, void* y, float* z, float* parts, hipStream_t s) {
   const LinearArgs a{x, w, d.K, d.K, bias, res, y, z, parts, d.M, d.N, d.K, d.K,
                      d.act, 1, d.type == MOE_TYPE_F32};
-  return launch_linear_plan(a, linear_plan(d.M, d.N, d.K, Layout::kRows), Layout::kRows, s);
+  const bool plain = !bias && !res && !z && d.act == MOE_ACT_NONE;
+  return launch_linear_plan(a, linear_plan(d.M, d.N, d.K, Layout::kRows, plain), Layout::kRows, s);
 }
 
 }  // namespace moe

@@ -61,8 +61,8 @@ size_t grad_ws_layout(int M, int N, int K, void* base, GradWs* out) {
     return o;
   };
   const size_t o_dz = take(2 * (size_t)M * Np), o_db = take(sizeof(float) * (size_t)ceil_div(M, 64) * N);
-  const size_t px = linear_plan_parts(M, K, linear_plan(M, K, Np, Layout::kWTrans)),
-               pw = linear_plan_parts(N, K, linear_plan(N, K, M, Layout::kBothTrans));
+  const size_t px = linear_plan_parts(M, K, linear_plan(M, K, Np, Layout::kWTrans, true)),
+               pw = linear_plan_parts(N, K, linear_plan(N, K, M, Layout::kBothTrans, true));
   const size_t o_parts = take(px > pw ? px : pw);
   if (out) {
     char* b = static_cast<char*>(base);
@@ -94,12 +94,12 @@ hipError_t launch_linear_grad(const moe_linear_dims& d, const void* dy, const ui
   if (err == hipSuccess && dx) {   // [M, K] = dz [M, Np] . w [N, K], contracted over N
     const LinearArgs a{g.dz, w, Np, d.K, nullptr, nullptr, dx, nullptr, g.parts, d.M, d.K, Np, d.N,
                        MOE_ACT_NONE, 1, false};
-    err = launch_linear_plan(a, linear_plan(d.M, d.K, Np, Layout::kWTrans), Layout::kWTrans, s);
+    err = launch_linear_plan(a, linear_plan(d.M, d.K, Np, Layout::kWTrans, true), Layout::kWTrans, s);
   }
   if (err == hipSuccess && dw) {   // [N, K] = dz [M, N] . x [M, K], contracted over M
     const LinearArgs a{g.dz, x, Np, d.K, nullptr, nullptr, dw, nullptr, g.parts, d.N, d.K, d.M, d.M,
                        MOE_ACT_NONE, 1, false};
-    err = launch_linear_plan(a, linear_plan(d.N, d.K, d.M, Layout::kBothTrans), Layout::kBothTrans, s);
+    err = launch_linear_plan(a, linear_plan(d.N, d.K, d.M, Layout::kBothTrans, true), Layout::kBothTrans, s);
   }
   return err;
 }

@@ -1,0 +1,201 @@
+// The dense product with a short contraction (at most 384: the gradient of a router's
+// input, contracted over its experts): bound by writing the result, and with square
+// tiles by the copies into LDS.
+//
+// A workgroup keeps 256 rows of x in registers, 64 per wave and the whole contraction
+// (at C = 384 192 registers, in the AGPR file as the MFMAs' second operand), and walks
+// a run of 128-column tiles. Only w goes through LDS: a ring of kRing one-step stages
+// (64 x 128) that runs on across the tiles, so that the next tile's columns arrive
+// during the epilogue. Per 256 x 128 outputs 96 KB are copied, against 4 x 192 KB for
+// the same outputs in 128 x 128 tiles (16384 x 7168 x 384: 152 us in those).
+//
+// Step g (tile g / KS, step g % KS): the MFMAs of its first half and the reads of its
+// second; wait for this wave's copies of step g + 1 and barrier, which frees g's stage;
+// the MFMAs of the second half, the reads of step g + 1's first half and the copies of
+// step g + kRing. The wait counts the loads issued after those of g + 1; stores that
+// are still on their way only make it wait longer. The epilogue loads nothing (no bias,
+// residual or activation): the wait for a load would be a wait for every copy.
+#include "linear.h"
+#include "linear_stage.h"
+
+namespace moe {
+namespace {
+
+constexpr int kShortThreads = 256;
+constexpr int kShortRows = 256, kShortCols = 128;
+constexpr int kRing = 7;
+constexpr int kXcds = 8;
+
+// acc += W X: acc and w in VGPRs, x in AGPRs. The compiler does not know that the
+// statement is an MFMA: s_nop provides the wait states after a VALU write.
+__device__ __forceinline__ void mma_x_agpr(v4f& acc, const v4i& w, const v4i& x) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(w), "a"(x));
+#endif
+}
+
+template <int KS, bool WT, bool F32>
+__global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a, int m_tiles, int n_tiles, int per_cta,
+                                                                    int total) {
+  constexpr int FT = 4, FW = 8;
+  typedef Operand<kShortCols, WT> W;
+  constexpr int kCopies = W::kCopies;
+  constexpr int kOutRow = kShortCols + 4;   // floats per staged row: 16 rows in distinct banks
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing * W::kBytes + 4 * 16 * kOutRow * 4];
+
+  // (column run, row tile), each XCD a contiguous share: its L2 holds few column runs
+  const int run = (total + kXcds - 1) / kXcds;
+  const int id = (blockIdx.x % kXcds) * run + blockIdx.x / kXcds;
+  if ((int)(blockIdx.x / kXcds) >= run || id >= total) return;
+  const int m0 = id % m_tiles * kShortRows, t0 = id / m_tiles * per_cta, t1 = min(t0 + per_cta, n_tiles);
+
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  W ow;
+  ow.init(a.ws, wave, lane);
+  FragReader<kShortCols, WT> rw;
+  rw.init(lane);
+
+  const int steps = (t1 - t0) * KS;
+  int ct = t0, cs = 0, cbuf = 0, issued = 0;   // the copies' tile, step and stage
+  ow.place(a.w, a.ws, ct * kShortCols, a.N, a.w_rows);
+  auto next_rsrc = [&]() { return ow.rsrc(cs, issued < steps ? KS : 0); };
+  auto advance = [&]() {
+    ++issued;
+    cbuf = cbuf + 1 == kRing ? 0 : cbuf + 1;
+    if (++cs == KS) {
+      cs = 0;
+      ++ct;
+      ow.place(a.w, a.ws, min(ct, n_tiles - 1) * kShortCols, a.N, a.w_rows);
+    }
+  };
+#pragma unroll 1
+  for (int s = 0; s < kRing; ++s) {
+    const v4i_s r = next_rsrc();
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) ow.copy(r, smem + cbuf * W::kBytes, wave, i);
+    advance();
+  }
+  // x: lane (c, q) holds contraction 64 s + 32 h + 8q .. + 7 of rows 16 j + c; rows past
+  // the end repeat the last one and are not stored
+  v4i x[FT][KS][2];
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    const uint16_t* row = a.x + (int64_t)min(m0 + 64 * wave + 16 * j + c, a.M - 1) * a.xs + 8 * q;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) x[j][s][h] = load16(row + 64 * s + 32 * h);
+  }
+#pragma unroll
+  for (int j = 0; j < FT; ++j)
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) asm volatile("; in an AGPR from here" : "+a"(x[j][s][h]));
+  wait_vmcnt<0>();
+  __syncthreads();
+
+  v4f acc[FW][FT];
+#pragma unroll
+  for (int i = 0; i < FW; ++i)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  v4i w0[FW], w1[FW];
+#pragma unroll
+  for (int i = 0; i < FW; ++i) w0[i] = rw.template read<0>(smem, i);
+
+  float* const out = reinterpret_cast<float*>(smem + kRing * W::kBytes + wave * 16 * kOutRow * 4);
+  int buf = 0;   // stage of step g
+  for (int t = t0; t < t1; ++t) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint8_t* stage = smem + buf * W::kBytes;
+      const int nbuf = buf + 1 == kRing ? 0 : buf + 1;
+      const uint8_t* next = smem + nbuf * W::kBytes;
+#pragma unroll
+      for (int i = 0; i < FW; ++i) {
+        w1[i] = rw.template read<1>(stage, i);
+#pragma unroll
+        for (int j = 0; j < FT; ++j) mma_x_agpr(acc[i][j], w0[i], x[j][s][0]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      wait_vmcnt<(kRing - 2) * kCopies>();
+      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);
+      const v4i_s r = next_rsrc();
+#pragma unroll
+      for (int i = 0; i < FW; ++i) {
+        w0[i] = rw.template read<0>(next, i);
+        if (i % 2 == 0 && i / 2 < kCopies) ow.copy(r, smem + cbuf * W::kBytes, wave, i / 2);
+#pragma unroll
+        for (int j = 0; j < FT; ++j) mma_x_agpr(acc[i][j], w1[i], x[j][s][1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      advance();
+      buf = nbuf;
+    }
+    // The compiler does not see the MFMAs, so it inserts no wait states before the
+    // accumulators are read: 64 of them here.
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+#endif
+    __builtin_amdgcn_sched_barrier(0);
+    // results, 16 rows at a time through the wave's own LDS rows, 8 columns per lane
+#pragma unroll
+    for (int j = 0; j < FT; ++j) {
+#pragma unroll
+      for (int i = 0; i < FW; ++i) *reinterpret_cast<v4f*>(out + c * kOutRow + 16 * i + 4 * q) = acc[i][j];
+      __builtin_amdgcn_wave_barrier();
+      const int64_t mw = m0 + 64 * wave + 16 * j + q;
+      const int n = t * kShortCols + 8 * c;
+      const float* src = out + q * kOutRow + 8 * c;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        finish_affine<false>(a, mw + 4 * u, n, *reinterpret_cast<const v4f*>(src + 4 * u * kOutRow),
+                      *reinterpret_cast<const v4f*>(src + 4 * u * kOutRow + 4), Residual8<false, F32>{});
+      __builtin_amdgcn_wave_barrier();
+    }
+#pragma unroll
+    for (int i = 0; i < FW; ++i)
+#pragma unroll
+      for (int j = 0; j < FT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+  wait_vmcnt<0>();   // no copy may be in flight when the workgroup's LDS is given away
+}
+
+template <int KS>
+void run(const LinearArgs& a, bool w_trans, hipStream_t s) {
+  const int m_tiles = (int)ceil_div(a.M, kShortRows), n_tiles = (int)ceil_div(a.N, kShortCols);
+  const int per = short_tiles_per_cta(a.M, a.N);
+  const int total = m_tiles * (int)ceil_div(n_tiles, per);
+  const dim3 grid((unsigned)(ceil_div(total, kXcds) * kXcds)), block(kShortThreads);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a, m_tiles, n_tiles, per, total); };
+  if (w_trans) {
+    if (a.out_f32) go(k_linear_short<KS, true, true>);
+    else go(k_linear_short<KS, true, false>);
+  } else {
+    if (a.out_f32) go(k_linear_short<KS, false, true>);
+    else go(k_linear_short<KS, false, false>);
+  }
+}
+
+}  // namespace
+
+// Column tiles per workgroup: as many as leave one workgroup per CU.
+int short_tiles_per_cta(int M, int N) {
+  const int64_t m_tiles = ceil_div(M, kShortRows), n_tiles = ceil_div(N, kShortCols);
+  int64_t runs = 256 / m_tiles;
+  runs = runs < 1 ? 1 : runs > n_tiles ? n_tiles : runs;
+  return (int)ceil_div(n_tiles, runs);
+}
+
+void launch_short(const LinearArgs& a, Layout l, hipStream_t s) {
+  const bool wt = l == Layout::kWTrans;
+  if (a.C == 128) run<2>(a, wt, s);
+  else if (a.C == 256) run<4>(a, wt, s);
+  else run<6>(a, wt, s);
+}
+
+}  // namespace moe

@@ -20,20 +20,8 @@
 // bytes of a row: with stages of 32 (64-byte pieces) the copies' issue took most of the
 // loop (32768 x 384 x 7168: 208 us).
 //
-// An operand stored [rows, C] is staged as 128-byte rows, 16-byte chunks XORed by a
-// function of the row (the 8 or 16 lanes that LDS serves together then hit every bank
-// once), and a fragment is one ds_read_b128 per lane. One stored [C, rows] is staged as
-// 64 rows of the contraction, and a fragment is two ds_read_b64_tr_b16: lane
-// (4i + g, q) reads columns 4g .. 4g+3 of contraction row 8q + i (then 8q + 4 + i), and
-// the transpose within 16 lanes leaves lane c with four contraction values of column c.
-// The 16 rows of a read lie a multiple of 128 bytes apart, so 32-byte blocks are XORed
-// by a function of the row that spreads them over the banks.
-//
-// Copies past an operand's end, or past this workgroup's share of the contraction, are
-// zeros from the buffer resource's bounds check. A transposed operand's columns past
-// its last one are the next row's values: they only reach outputs that are not stored.
 #include "linear.h"
-#include "lds_copy.h"
+#include "linear_stage.h"
 
 namespace moe {
 namespace {
@@ -42,8 +30,6 @@ constexpr int kTileThreads = 256;
 constexpr int kXcds = 8;
 constexpr int kGroup = 8;   // row tiles that share a pass over the column tiles
 
-typedef short v4h __attribute__((ext_vector_type(4)));
-
 // acc += A B, acc in AGPRs. The compiler does not know that the statement is an MFMA
 // and inserts no wait states after a VALU write of an operand: s_nop provides them.
 __device__ __forceinline__ void mma_agpr(v4f& acc, const v4i& a, const v4i& b) {
@@ -51,97 +37,6 @@ __device__ __forceinline__ void mma_agpr(v4f& acc, const v4i& a, const v4i& b) {
   asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 #endif
 }
-
-// One operand's steps: ROWS tile rows (columns of the result for w).
-template <int ROWS, bool TRANS>
-struct Operand {
-  static constexpr int kBytes = ROWS * 128;         // a stage
-  static constexpr int kCopies = kBytes / 4096;     // per wave and step
-  static constexpr int kRow = 2 * ROWS;             // bytes of a transposed stage's row
-  static constexpr int kMask = kRow % 256 == 0 ? 7 : 3;   // 32-byte blocks that are XORed together
-
-  const char* base;    // first byte of step 0
-  int64_t step;        // bytes per step
-  int64_t left;        // bytes from `base` to the operand's end (the tile's, for [rows, C])
-  int row_bytes;
-  int voff[kCopies];   // of this lane's 16 bytes, relative to the step
-
-  // XOR of a transposed stage's blocks in contraction row r: the rows 8q + i of a read
-  // differ in i = r % 4 and q
-  __device__ static int xor_of(int r) {
-    return kMask == 7 ? (r & 3) | ((r >> 3 & 1) << 2) : (r >> 1 & 1) | ((r >> 3 & 1) << 1);
-  }
-  // XOR of the chunks of row r
-  __device__ static int chunk_xor(int r) { return (r >> 1 & 7) ^ ((r & 1) << 2); }
-
-  __device__ void init(const uint16_t* p, int64_t stride, int first, int rows, int C, int wave, int lane) {
-    row_bytes = (int)(2 * stride);
-    if constexpr (TRANS) {
-      base = reinterpret_cast<const char*>(p + first);
-      step = (int64_t)64 * row_bytes;
-      left = (int64_t)C * row_bytes - 2 * first;
-    } else {
-      base = reinterpret_cast<const char*>(p + first * stride);
-      step = 128;
-      left = (int64_t)min(ROWS, rows - first) * row_bytes;
-    }
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const int b = (kCopies * wave + i) * 1024 + lane * 16;   // byte of the stage that this lane fills
-      if constexpr (TRANS) {
-        const int r = b / kRow, chunk = b % kRow / 16;
-        voff[i] = r * row_bytes + ((chunk ^ (xor_of(r) << 1)) << 4);
-      } else {
-        const int r = b / 128, chunk = b % 128 / 16;
-        voff[i] = r * row_bytes + ((chunk ^ chunk_xor(r)) << 4);
-      }
-    }
-  }
-  // the buffer resource of step s; size 0 from `end` on
-  __device__ v4i_s rsrc(int s, int end) const {
-    int64_t bytes = left - s * step;
-    const int64_t most = (int64_t)(TRANS ? 64 : ROWS) * row_bytes;   // keeps the size in 32 bits
-    bytes = bytes < 0 ? 0 : bytes > most ? most : bytes;
-    return rsrc4(base + s * step, s < end ? (uint32_t)bytes : 0u);
-  }
-  __device__ void copy(v4i_s r, uint8_t* stage, int wave, int i) const {
-    dma16(r, lds_addr(stage + (kCopies * wave + i) * 1024), voff[i], 0);
-  }
-};
-
-// A lane's view of the fragments of a stage: fragment f is 16 tile rows from 16 f on,
-// half h the contraction index's 32 h .. 32 h + 31.
-template <int ROWS, bool TRANS>
-struct FragReader {
-  int lane_off[2], x;
-  __device__ void init(int lane) {
-    const int c = lane & 15, q = lane >> 4;
-    if constexpr (TRANS) {
-      const int r = 8 * q + (c >> 2);
-      lane_off[0] = r * 2 * ROWS + 8 * (c & 3);
-      lane_off[1] = lane_off[0] + 32 * 2 * ROWS;
-      x = Operand<ROWS, true>::xor_of(r);   // the same for r + 4 and r + 32
-    } else {
-      const int sw = Operand<ROWS, false>::chunk_xor(c);
-      lane_off[0] = c * 128 + ((q ^ sw) << 4);
-      lane_off[1] = c * 128 + (((4 + q) ^ sw) << 4);
-      x = 0;
-    }
-  }
-  template <int H>
-  __device__ v4i read(const uint8_t* stage, int f) const {
-    if constexpr (TRANS) {
-      typedef __attribute__((address_space(3))) v4h* lds4;
-      const uint8_t* p = stage + lane_off[H] + ((f ^ x) << 5);
-      const v4h lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p);
-      const v4h hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * 2 * ROWS));
-      const int2 a = __builtin_bit_cast(int2, lo), b = __builtin_bit_cast(int2, hi);
-      return v4i{a.x, a.y, b.x, b.y};
-    } else {
-      return *reinterpret_cast<const v4i*>(stage + lane_off[H] + f * 2048);
-    }
-  }
-};
 
 template <int FT, int FW, bool XT, bool WT>
 __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, int m_tiles, int n_tiles) {
@@ -177,8 +72,10 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
 
   X ox;
   W ow;
-  ox.init(a.x, a.xs, m0, a.M, a.C, wave, lane);
-  ow.init(a.w, a.ws, n0, a.N, a.w_rows, wave, lane);
+  ox.init(a.xs, wave, lane);
+  ox.place(a.x, a.xs, m0, a.M, a.C);
+  ow.init(a.ws, wave, lane);
+  ow.place(a.w, a.ws, n0, a.N, a.w_rows);
   FragReader<kRows, XT> rx;
   FragReader<kCols, WT> rw;
   rx.init(lane);
@@ -258,42 +155,49 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
   __syncthreads();
 
   // Results, 64 rows of the wave at a time, through the wave's own part of LDS, so that
-  // stores walk whole rows: 2 FW lanes hold 8 columns each of a row. Four groups at a
-  // time, their residuals loaded ahead.
+  // stores walk whole rows: 2 FW lanes hold 8 columns each of a row. Without activation
+  // four groups at a time, their residuals loaded ahead.
+  constexpr int kGroups = 2 * FW, kAtOnce = 4;
   float* const out = reinterpret_cast<float*>(smem + wave * kOut);
+  const bool affine = a.splits == 1 && is_affine(a);
 #pragma unroll
   for (int j0 = 0; j0 < FT; j0 += 4) {
-    constexpr int kGroups = 2 * FW, kAtOnce = 4;
-    const int frags = FT - j0 < 4 ? FT - j0 : 4;
+    const int groups = 16 * (FT - j0 < 4 ? FT - j0 : 4) * kGroups;   // a multiple of 64 * kAtOnce
 #pragma unroll
     for (int j = j0; j < j0 + 4 && j < FT; ++j)
 #pragma unroll
       for (int i = 0; i < FW; ++i)
         *reinterpret_cast<v4f*>(out + (16 * (j - j0) + c) * kOutRow + 16 * i + 4 * q) = acc[i][j];
     __syncthreads();
+    const int64_t mw = m0 + 16 * FT * wm + 16 * j0;
+    const int nw = n0 + 16 * FW * wn;
+    if (affine) {
+      by_affine(a, [&](auto residual) {
+        typedef decltype(residual) Res;
 #pragma unroll 1
-    for (int g0 = lane; g0 < 16 * frags * kGroups; g0 += 64 * kAtOnce) {   // a multiple of 64 * kAtOnce
-      Residual<8> res[kAtOnce];
-      int row[kAtOnce], col[kAtOnce];
+        for (int g0 = lane; g0 < groups; g0 += 64 * kAtOnce) {
+          Res res[kAtOnce];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        row[u] = (g0 + 64 * u) / kGroups;
-        col[u] = 8 * ((g0 + 64 * u) % kGroups);
-        if (a.splits == 1)
-          res[u] = load_residual<8>(a, m0 + 16 * FT * wm + 16 * j0 + row[u], n0 + 16 * FW * wn + col[u]);
-      }
+          for (int u = 0; u < kAtOnce; ++u)
+            res[u].load(a, mw + (g0 + 64 * u) / kGroups, nw + 8 * ((g0 + 64 * u) % kGroups));
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int64_t m = m0 + 16 * FT * wm + 16 * j0 + row[u];
-        const int n = n0 + 16 * FW * wn + col[u];
-        const v4f lo = *reinterpret_cast<const v4f*>(out + row[u] * kOutRow + col[u]);
-        const v4f hi = *reinterpret_cast<const v4f*>(out + row[u] * kOutRow + col[u] + 4);
-        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        if (a.splits == 1) {
-          finish<8>(a, m, n, v, res[u]);
-        } else {
-          store_part<8>(a, split, m, n, v);
+          for (int u = 0; u < kAtOnce; ++u) {
+            const int r = (g0 + 64 * u) / kGroups, col = 8 * ((g0 + 64 * u) % kGroups);
+            const float* src = out + r * kOutRow + col;
+            finish_affine(a, mw + r, nw + col, *reinterpret_cast<const v4f*>(src),
+                          *reinterpret_cast<const v4f*>(src + 4), res[u]);
+          }
         }
+      });
+    } else {
+#pragma unroll 1
+      for (int g = lane; g < groups; g += 64) {
+        const int r = g / kGroups, col = 8 * (g % kGroups);
+        const v4f lo = *reinterpret_cast<const v4f*>(out + r * kOutRow + col);
+        const v4f hi = *reinterpret_cast<const v4f*>(out + r * kOutRow + col + 4);
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        if (a.splits > 1) store_part<8>(a, split, mw + r, nw + col, v);
+        else finish<8>(a, mw + r, nw + col, v, load_residual<8>(a, mw + r, nw + col));
       }
     }
     __syncthreads();

@@ -207,6 +207,19 @@ def test_linear_tiles(dev, M, N, K, dtype):
     check_linear(dev, M, N, K, dtype=dtype, bias=M % 2 == 0, res=N % 2 == 1, seed=M + N)
 
 
+@pytest.mark.parametrize("M,N,K", [(1000, 8197, 512), (12003, 1000, 512), (16500, 700, 2048),   # 256 x 192, 192 x 256, 256 x 256
+                                   (1001, 8200, 128), (8203, 777, 256)])
+def test_linear_large_tiles(dev, M, N, K):
+    check_linear(dev, M, N, K, act="silu", bias=True, res=True, dtype=F32 if N % 2 else BF16, z=N % 2 == 1, seed=N)
+
+
+@pytest.mark.parametrize("M,N,K", [(1001, 8200, 128), (8203, 776, 256), (16390, 2504, 384), (70, 8, 128), (257, 120, 384),
+                                   (12003, 1000, 512), (129, 640, 2048)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_linear_without_epilogue(dev, M, N, K, dtype):
+    check_linear(dev, M, N, K, dtype=dtype, seed=N)
+
+
 @pytest.mark.parametrize("M,N", [(9, 33), (150, 72)])
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "sigmoid"])
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -244,7 +257,11 @@ def test_linear_no_rows(dev):
 @pytest.mark.parametrize("M,N,K,act,dtype", [
     (1, 1, 128, "none", F32), (7, 384, 256, "none", F32), (300, 384, 512, "none", BF16), (129, 70, 384, "silu", BF16),
     (1000, 33, 256, "gelu", F32), (65, 130, 128, "sigmoid", F32), (500, 8, 1024, "relu", BF16),
-    (4100, 40, 256, "none", F32), (64, 1000, 128, "none", BF16)])
+    (4100, 40, 256, "none", F32), (64, 1000, 128, "none", BF16),
+    # every tile shape of both gradients, and runs of column tiles for a short contraction
+    (128, 1000, 8192, "none", F32), (128, 12001, 1024, "none", BF16), (2048, 16500, 768, "none", BF16),
+    (1000, 500, 8192, "relu", BF16), (12000, 500, 1024, "none", BF16), (16500, 2000, 768, "none", BF16),
+    (5003, 300, 2048, "silu", F32), (3001, 120, 4096, "none", BF16)])
 def test_linear_grad(dev, M, N, K, act, dtype):
     x, w = randn(M, K, seed=1, dtype=BF16), randn(N, K, seed=2, scale=1 / math.sqrt(K), dtype=BF16)
     dy = randn(M, N, seed=3, dtype=dtype)
