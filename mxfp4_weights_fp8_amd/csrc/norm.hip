@@ -13,8 +13,12 @@
 #include "host_internal.h"
 #include "lane_reduce.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
+
+typedef int v2i __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ void unpack8(const v4i raw, float (&v)[8]) {
 #pragma unroll
@@ -46,24 +50,51 @@ __device__ __forceinline__ void load_weight8(const void* w, int vec, float (&v)[
   }
 }
 
-// Sum over a workgroup of WAVES waves of N values per thread, the same in every thread:
-// lane reductions, then the waves' sums in wave order.
-template <int WAVES, int N>
-__device__ __forceinline__ void block_sum(float (&s)[N], float* red) {
+// A row belongs to TPR threads: 16 lanes (H up to 512), a wave, or 128, 256 or 512
+// threads; a workgroup holds 256 threads' worth of rows at least.
+template <int TPR>
+struct Rows {
+  static constexpr int kThreads = TPR > 256 ? TPR : 256;
+  static constexpr int kRows = kThreads / TPR;
+  static constexpr int kWaves = TPR / 64;   // of a row, where it has more than one
+};
+
+// Sums over a row's threads of N values per thread, the same in all of them: lane
+// reductions, then the waves' sums in wave order. red: this row's kWaves * N floats.
+// With more than one wave per row every thread of the workgroup has to call it.
+template <int TPR, int N>
+__device__ __forceinline__ void sum_over_row(float (&s)[N], float* red) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) s[n] = row_sum<64>(s[n]);
-  if constexpr (WAVES == 1) return;
-  if ((threadIdx.x & 63) == 0)
+  for (int n = 0; n < N; ++n) s[n] = row_sum<(TPR < 64 ? 16 : 64)>(s[n]);
+  if constexpr (TPR > 64) {
+    constexpr int W = Rows<TPR>::kWaves;
+    const int wave = (threadIdx.x % TPR) >> 6;
+    if ((threadIdx.x & 63) == 0)
 #pragma unroll
-    for (int n = 0; n < N; ++n) red[(threadIdx.x >> 6) * N + n] = s[n];
-  __syncthreads();
+      for (int n = 0; n < N; ++n) red[wave * N + n] = s[n];
+    __syncthreads();
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    s[n] = red[n];
+    for (int n = 0; n < N; ++n) {
+      s[n] = red[n];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) s[n] += red[w * N + n];
+      for (int w = 1; w < W; ++w) s[n] += red[w * N + n];
+    }
   }
 }
+
+// Loads and stores of the row tensors. NT: nontemporal, for tensors that do not fit the
+// 256 MB last-level cache anyway (32768 x 7168: 336 us against 387 us; 4096 x 7168, whose
+// outputs stay cached for the next kernel: 49 against 47 us).
+template <bool NT>
+__device__ __forceinline__ v4i load_row(const uint16_t* p) {
+  return NT ? load16_nt(p) : load16(p);
+}
+template <bool NT>
+__device__ __forceinline__ void store_row(uint16_t* p, const v4i v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(p));
+  else *reinterpret_cast<v4i*>(p) = v;
+}
+inline bool past_cache(int T, int H) { return (int64_t)T * H > 50000000; }
 
 struct NormArgs {
   const uint16_t* x;
@@ -73,40 +104,42 @@ struct NormArgs {
   uint16_t* y;           // optional; may be x
   uint8_t* x_q;          // optional, with x_s
   uint8_t* x_s;
-  int H;
+  int T, H;
   float eps;
 };
 
-// One workgroup per row; thread t holds vectors t, t + THREADS, ... (VPT of them, the
-// last ones past H / 8 empty).
-template <int THREADS, int VPT, bool WF32>
-__global__ __launch_bounds__(THREADS) void k_add_norm(NormArgs a) {
-  __shared__ float red[THREADS / 64];
-  const int nv = a.H / 8, tid = threadIdx.x;
-  const int64_t row0 = (int64_t)blockIdx.x * a.H;
+// Thread t of a row holds vectors t, t + TPR, ... (VPT of them, the last ones past H / 8
+// empty).
+template <int TPR, int VPT, bool WF32, bool NT>
+__global__ __launch_bounds__(Rows<TPR>::kThreads) void k_add_norm(NormArgs a) {
+  __shared__ float red[Rows<TPR>::kRows][TPR / 64 + 1];
+  const int nv = a.H / 8, tid = threadIdx.x % TPR, sub = Rows<TPR>::kRows == 1 ? 0 : threadIdx.x / TPR;
+  const int64_t t = (int64_t)blockIdx.x * Rows<TPR>::kRows + sub;
+  const int64_t row0 = t * a.H;
+  const int mine = t < a.T ? nv : 0;   // vectors of this row
   float h[VPT][8], s[1] = {0.f};
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int vec = tid + i * THREADS;
-    if (vec < nv) {
-      unpack8(load16_nt(a.x + row0 + vec * 8), h[i]);
+    const int vec = tid + i * TPR;
+    if (vec < mine) {
+      unpack8(load_row<NT>(a.x + row0 + vec * 8), h[i]);
       if (a.res) {
         float r[8];
-        unpack8(load16_nt(a.res + row0 + vec * 8), r);
+        unpack8(load_row<NT>(a.res + row0 + vec * 8), r);
 #pragma unroll
         for (int k = 0; k < 8; ++k) h[i][k] += r[k];
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) s[0] += h[i][k] * h[i][k];
-      if (a.h) *reinterpret_cast<v4i*>(a.h + row0 + vec * 8) = pack8(h[i]);
+      if (a.h) store_row<NT>(a.h + row0 + vec * 8, pack8(h[i]));
     }
   }
-  block_sum<THREADS / 64>(s, red);
+  sum_over_row<TPR>(s, red[sub]);
   const float r = 1.0f / sqrtf(s[0] / (float)a.H + a.eps);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int vec = tid + i * THREADS;
-    if (vec < nv) {   // H is a multiple of 128: the 16 lanes of a block agree
+    const int vec = tid + i * TPR;
+    if (vec < mine) {   // H is a multiple of 128: the 16 lanes of a block agree
       float w[8];
       load_weight8<WF32>(a.w, vec, w);
       float amax = 0.f;
@@ -115,40 +148,42 @@ __global__ __launch_bounds__(THREADS) void k_add_norm(NormArgs a) {
         h[i][k] = h[i][k] * r * w[k];
         amax = fmaxf(amax, fabsf(h[i][k]));
       }
-      if (a.y) *reinterpret_cast<v4i*>(a.y + row0 + vec * 8) = pack8(h[i]);
+      if (a.y) store_row<NT>(a.y + row0 + vec * 8, pack8(h[i]));
       if (a.x_q) {
         amax = row_max<16>(amax);
         const int e = e8m0_exponent(amax);
         const float inv = exp2_neg(e);
-        *reinterpret_cast<uint2*>(a.x_q + row0 + vec * 8) =
-            make_uint2(e4m3_pack4(h[i][0] * inv, h[i][1] * inv, h[i][2] * inv, h[i][3] * inv),
-                       e4m3_pack4(h[i][4] * inv, h[i][5] * inv, h[i][6] * inv, h[i][7] * inv));
+        const v2i q{(int)e4m3_pack4(h[i][0] * inv, h[i][1] * inv, h[i][2] * inv, h[i][3] * inv),
+                    (int)e4m3_pack4(h[i][4] * inv, h[i][5] * inv, h[i][6] * inv, h[i][7] * inv)};
+        *reinterpret_cast<v2i*>(a.x_q + row0 + vec * 8) = q;   // 8-byte pieces: left to the L2 to merge
         if ((tid & 15) == 0) a.x_s[(row0 + vec * 8) / 128] = (uint8_t)(e + 127);
       }
     }
   }
 }
 
-// Threads per row: four vectors each at most, so that a short row does not leave most
-// of a workgroup idle (64 threads up to H 2048); eight vectors above H 8192.
-template <bool WF32>
-hipError_t launch_fwd(const NormArgs& a, int T, hipStream_t s) {
+// Threads per row: four vectors each at most, so that short rows share a workgroup (32768
+// x 128 on 64 threads per row 14.8 us); eight vectors above H 8192.
+template <bool WF32, bool NT>
+void launch_fwd(const NormArgs& a, hipStream_t s) {
+  auto go = [&](auto kernel, int rows) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)ceil_div(a.T, rows)), dim3(256), 0, s, a);
+  };
   const int nv = a.H / 8;
-  const dim3 grid((unsigned)T);
-  if (nv <= 64) hipLaunchKernelGGL((k_add_norm<64, 1, WF32>), grid, dim3(64), 0, s, a);
-  else if (nv <= 256) hipLaunchKernelGGL((k_add_norm<64, 4, WF32>), grid, dim3(64), 0, s, a);
-  else if (nv <= 512) hipLaunchKernelGGL((k_add_norm<128, 4, WF32>), grid, dim3(128), 0, s, a);
-  else if (nv <= 1024) hipLaunchKernelGGL((k_add_norm<256, 4, WF32>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_add_norm<256, 8, WF32>), grid, dim3(256), 0, s, a);
-  return hipGetLastError();
+  if (nv <= 16) go(k_add_norm<16, 1, WF32, NT>, 16);
+  else if (nv <= 64) go(k_add_norm<16, 4, WF32, NT>, 16);
+  else if (nv <= 256) go(k_add_norm<64, 4, WF32, NT>, 4);
+  else if (nv <= 512) go(k_add_norm<128, 4, WF32, NT>, 2);
+  else if (nv <= 1024) go(k_add_norm<256, 4, WF32, NT>, 1);
+  else go(k_add_norm<256, 8, WF32, NT>, 1);
 }
 
 // Gradient. With n = h r and g = dy w:
 //   dx = r (g - n mean_H(g n)) + dh,   dw = sum over rows of dy n.
-// mean(g n) = r mean(g h), so one pass over a row gives both sums. Each workgroup
-// walks rows b, b + gridDim, ..., the next row's values on their way while a row is
-// reduced, and keeps its part of dw in registers; the parts go to the workspace as
-// [gridDim, H] and k_sum_parts adds them in order.
+// mean(g n) = r mean(g h), so one pass over a row gives both sums. A row's threads
+// walk every gridDim * kRows-th row, the next row's values on their way while a row is
+// reduced, and keep their part of dw in registers; the parts of a workgroup are added
+// through LDS, go to the workspace as [gridDim, H], and k_sum_parts adds them in order.
 struct NormGradArgs {
   const uint16_t* dy;
   const uint16_t* h;
@@ -160,94 +195,133 @@ struct NormGradArgs {
   float eps;
 };
 
-template <int THREADS, int VPT, bool WF32>
-__global__ __launch_bounds__(THREADS) void k_add_norm_grad(NormGradArgs a) {
-  __shared__ float red[2][2 * (THREADS / 64)];   // alternating, so one barrier per row is enough
-  const int nv = a.H / 8, tid = threadIdx.x;
+// Up to two vectors per thread 128 registers, so that 16 waves share a CU.
+template <int TPR, int VPT, bool WF32, bool NT>
+__global__ __launch_bounds__(Rows<TPR>::kThreads, VPT <= 2 ? 4 : 2) void k_add_norm_grad(NormGradArgs a) {
+  constexpr int kRows = Rows<TPR>::kRows;
+  __shared__ float red[2][kRows][2 * (TPR / 64) + 1];   // alternating, so one barrier per row is enough
+  extern __shared__ float dw_rows[];                    // [kRows, H] where kRows > 1
+  const int nv = a.H / 8, tid = threadIdx.x % TPR, sub = Rows<TPR>::kRows == 1 ? 0 : threadIdx.x / TPR;
+  const int64_t stride = (int64_t)gridDim.x * kRows;
   float dw[VPT][8] = {};
   v4i rh[VPT], ry[VPT], rd[VPT];
   auto load = [&](int64_t t) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int vec = tid + i * THREADS;
+      const int vec = tid + i * TPR;
       if (vec < nv && t < a.T) {
-        rh[i] = load16_nt(a.h + t * a.H + vec * 8);
-        ry[i] = load16_nt(a.dy + t * a.H + vec * 8);
-        if (a.dh) rd[i] = load16_nt(a.dh + t * a.H + vec * 8);
+        rh[i] = load_row<NT>(a.h + t * a.H + vec * 8);
+        ry[i] = load_row<NT>(a.dy + t * a.H + vec * 8);
+        if (a.dh) rd[i] = load_row<NT>(a.dh + t * a.H + vec * 8);
       }
     }
   };
-  load(blockIdx.x);
+  load((int64_t)blockIdx.x * kRows + sub);
   int turn = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
-    float h[VPT][8], g[VPT][8], o[VPT][8], s[2] = {0.f, 0.f};
+  // every row of a workgroup takes part in each turn, those past the end without vectors
+  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < a.T; t0 += stride, turn ^= 1) {
+    const int64_t t = t0 + sub;
+    const int mine = kRows == 1 || t < a.T ? nv : 0;
+    v4i ch[VPT], cy[VPT], cd[VPT];   // this row, unpacked where it is used
+    float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int vec = tid + i * THREADS;
-      if (vec < nv) {
-        unpack8(rh[i], h[i]);
-        unpack8(ry[i], g[i]);
-        if (a.dh) {
-          unpack8(rd[i], o[i]);
-        } else {
+      ch[i] = rh[i];
+      cy[i] = ry[i];
+      cd[i] = rd[i];
+      const int vec = tid + i * TPR;
+      if (vec < mine) {
+        float h[8];
+        unpack8(ch[i], h);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[i][k] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s[0] += h[i][k] * h[i][k];
+        for (int k = 0; k < 8; ++k) s[0] += h[k] * h[k];
       }
     }
-    load(t + gridDim.x);
+    load(t + stride);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int vec = tid + i * THREADS;
-      if (vec < nv) {
-        float w[8];
+      const int vec = tid + i * TPR;
+      if (vec < mine) {
+        float w[8], h[8], g[8];
         load_weight8<WF32>(a.w, vec, w);
+        unpack8(ch[i], h);
+        unpack8(cy[i], g);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s[1] += g[i][k] * w[k] * h[i][k];
+        for (int k = 0; k < 8; ++k) s[1] += g[k] * w[k] * h[k];
       }
     }
-    block_sum<THREADS / 64>(s, red[turn]);
+    sum_over_row<TPR>(s, red[turn][sub]);
     const float r = 1.0f / sqrtf(s[0] / (float)a.H + a.eps);
     const float c = r * r * (s[1] / (float)a.H);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int vec = tid + i * THREADS;
-      if (vec < nv) {
-        float w[8];
+      const int vec = tid + i * TPR;
+      if (vec < mine) {
+        float w[8], h[8], g[8], o[8] = {};
         load_weight8<WF32>(a.w, vec, w);
+        unpack8(ch[i], h);
+        unpack8(cy[i], g);
+        if (a.dh) unpack8(cd[i], o);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          o[i][k] += r * (g[i][k] * w[k] - h[i][k] * c);
-          dw[i][k] += g[i][k] * (h[i][k] * r);
+          o[k] += r * (g[k] * w[k] - h[k] * c);
+          dw[i][k] += g[k] * (h[k] * r);
         }
-        *reinterpret_cast<v4i*>(a.dx + t * a.H + vec * 8) = pack8(o[i]);
+        store_row<NT>(a.dx + t * a.H + vec * 8, pack8(o));
       }
     }
   }
+  float* part = a.parts + (int64_t)blockIdx.x * a.H;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int vec = tid + i * THREADS;
+    const int vec = tid + i * TPR;
     if (vec < nv) {
-      v4f* dst = reinterpret_cast<v4f*>(a.parts + (int64_t)blockIdx.x * a.H + vec * 8);
+      v4f* dst = reinterpret_cast<v4f*>((kRows > 1 ? dw_rows + sub * a.H : part) + vec * 8);
       dst[0] = v4f{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
       dst[1] = v4f{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
     }
   }
+  if constexpr (kRows > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.H; c += Rows<TPR>::kThreads) {
+      float v = dw_rows[c];
+#pragma unroll
+      for (int k = 1; k < kRows; ++k) v += dw_rows[k * a.H + c];
+      part[c] = v;
+    }
+  }
 }
 
-// Two vectors per thread at most up to H 8192 (the row, the next row and dw in
-// registers), four above.
-template <bool WF32>
+// Rows of a workgroup by width: two vectors per thread at most up to H 8192 (the row,
+// the next row and dw in registers), four above.
+inline int grad_rows(int H) { return H <= 256 ? 16 : H <= 1024 ? 4 : H <= 2048 ? 2 : 1; }
+
+template <bool WF32, bool NT>
 void launch_grad(const NormGradArgs& a, int ctas, hipStream_t s) {
-  const int nv = a.H / 8;
-  const dim3 grid((unsigned)ctas);
-  if (nv <= 128) hipLaunchKernelGGL((k_add_norm_grad<64, 2, WF32>), grid, dim3(64), 0, s, a);
-  else if (nv <= 256) hipLaunchKernelGGL((k_add_norm_grad<128, 2, WF32>), grid, dim3(128), 0, s, a);
-  else if (nv <= 512) hipLaunchKernelGGL((k_add_norm_grad<256, 2, WF32>), grid, dim3(256), 0, s, a);
-  else if (nv <= 1024) hipLaunchKernelGGL((k_add_norm_grad<512, 2, WF32>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((k_add_norm_grad<512, 4, WF32>), grid, dim3(512), 0, s, a);
+  const int nv = a.H / 8, rows = grad_rows(a.H);
+  auto go = [&](auto kernel, int threads) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)ctas), dim3(threads), rows > 1 ? sizeof(float) * rows * a.H : 0, s, a);
+  };
+  if (nv <= 16) go(k_add_norm_grad<16, 1, WF32, NT>, 256);
+  else if (nv <= 32) go(k_add_norm_grad<16, 2, WF32, NT>, 256);
+  else if (nv <= 64) go(k_add_norm_grad<64, 1, WF32, NT>, 256);
+  else if (nv <= 128) go(k_add_norm_grad<64, 2, WF32, NT>, 256);
+  else if (nv <= 256) go(k_add_norm_grad<128, 2, WF32, NT>, 256);
+  else if (nv <= 512) go(k_add_norm_grad<256, 2, WF32, NT>, 256);
+  else if (nv <= 1024) go(k_add_norm_grad<512, 2, WF32, NT>, 512);
+  else go(k_add_norm_grad<512, 4, WF32, NT>, 512);
+}
+
+// f<weights fp32, past the cache>()
+template <typename F>
+void by_kind(bool w_f32, bool nt, F f) {
+  if (w_f32) {
+    if (nt) f(std::true_type{}, std::true_type{});
+    else f(std::true_type{}, std::false_type{});
+  } else {
+    if (nt) f(std::false_type{}, std::true_type{});
+    else f(std::false_type{}, std::false_type{});
+  }
 }
 
 // out[c] = sum over p of parts[p][c], c < n: 64 columns per workgroup; each of its 16
@@ -280,14 +354,15 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_sum_parts(const float* __res
 
 hipError_t launch_add_norm(const uint16_t* x, const uint16_t* res, const void* w, bool w_f32, uint16_t* h,
                            uint16_t* y, uint8_t* x_q, uint8_t* x_s, int T, int H, float eps, hipStream_t s) {
-  const NormArgs a{x, res, w, h, y, x_q, x_s, H, eps};
-  return w_f32 ? launch_fwd<true>(a, T, s) : launch_fwd<false>(a, T, s);
+  const NormArgs a{x, res, w, h, y, x_q, x_s, T, H, eps};
+  by_kind(w_f32, past_cache(T, H), [&](auto f, auto nt) { launch_fwd<decltype(f)::value, decltype(nt)::value>(a, s); });
+  return hipGetLastError();
 }
 
-// Workgroups of the gradient: about 16 waves per CU, at most a row each.
+// Workgroups of the gradient: about 16 waves per CU, at most a turn of rows each.
 int norm_grad_parts(int T, int H) {
-  const int most = H <= 1024 ? 4096 : H <= 2048 ? 2048 : H <= 4096 ? 1024 : 512;
-  return T < most ? T : most;
+  const int64_t most = H > 4096 ? 512 : 1024, turns = ceil_div(T, grad_rows(H));
+  return (int)(turns < most ? turns : most);
 }
 
 hipError_t launch_add_norm_grad(const uint16_t* dy, const uint16_t* h, const void* w, bool w_f32, const uint16_t* dh,
@@ -295,8 +370,7 @@ hipError_t launch_add_norm_grad(const uint16_t* dy, const uint16_t* h, const voi
   const int n = norm_grad_parts(T, H);
   if (n > 0) {
     const NormGradArgs a{dy, h, w, dh, dx, parts, T, H, eps};
-    if (w_f32) launch_grad<true>(a, n, s);
-    else launch_grad<false>(a, n, s);
+    by_kind(w_f32, past_cache(T, H), [&](auto f, auto nt) { launch_grad<decltype(f)::value, decltype(nt)::value>(a, n, s); });
   }
   return launch_sum_parts(parts, n, H, dw, s);
 }

@@ -83,7 +83,8 @@ def check_normed(out, x, w, res, eps, what):
 
 
 @pytest.mark.parametrize("T,H", [(1, 128), (1, 16384), (7, 7168), (3, 256), (5, 2048), (5, 2176), (2, 4096), (33, 4224),
-                                 (2, 8192), (301, 1152), (1, 8320), (2050, 384)])
+                                 (2, 8192), (301, 1152), (1, 8320), (2050, 384), (17, 128), (35, 512), (9, 640), (3, 1024),
+                                 (49000, 1024)])
 @pytest.mark.parametrize("wtype", [BF16, F32])
 def test_add_norm(dev, T, H, wtype):
     x, res = randn(T, H, seed=T + H, dtype=BF16), randn(T, H, seed=T + H + 1, scale=3.0, dtype=BF16)
@@ -124,7 +125,8 @@ def test_add_norm_rows_of_zeros_infinities_and_large_values(dev):
     within(out.y.cpu()[keep], ref, ref.abs() * (BF + 60 * U) + 1e-38, "rows beside non-finite ones")
 
 
-@pytest.mark.parametrize("T,H", [(1, 128), (7, 7168), (2, 16384), (1100, 384), (37, 2304), (5, 4096)])
+@pytest.mark.parametrize("T,H", [(1, 128), (7, 7168), (2, 16384), (1100, 384), (37, 2304), (5, 4096), (19, 128),
+                                 (16500, 256), (5003, 1024), (3, 2048), (49000, 1024), (70, 512), (1025, 8320)])
 @pytest.mark.parametrize("wtype,with_dh", [(BF16, True), (F32, False)])
 def test_add_norm_grad(dev, T, H, wtype, with_dh):
     dy, h = randn(T, H, seed=1, dtype=BF16), randn(T, H, seed=2, scale=2.0, dtype=BF16)
@@ -139,7 +141,7 @@ def test_add_norm_grad(dev, T, H, wtype, with_dh):
     r = 1 / ((h64 * h64).mean(1, keepdim=True) + 1e-5).sqrt()
     mag = r * g + r ** 3 * h64 * (g * h64).mean(1, keepdim=True)   # the terms dx adds up
     within(dx, rdx, rdx.abs() * BF + (mag + (0 if dh is None else dh.to(F64).abs())) * (2 * NORM_TERMS + 32) * U, "dx")
-    terms = -(-T // 1) if T < 1024 else T // 1024 + 1024
+    terms = min(T, T // 512 + 1024)      # rows of a workgroup, then the workgroups' parts
     within(dw, rdw, (dy.to(F64).abs() * h64 * r).sum(0) * (terms + NORM_TERMS + 16) * U, "dweight")
     again, dw2 = moe.add_norm_grad(dyd, hd, wd, eps=1e-5, dh=dhd)
     assert torch.equal(dx, again) and torch.equal(dw, dw2)
