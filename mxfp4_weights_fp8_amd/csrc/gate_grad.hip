@@ -19,21 +19,34 @@ struct GateGradArgs {
   float scale;
 };
 
+// The picks' gradients are spread over the row through
+// LDS, one pick after another (so that equal ids add up in a fixed order): about 60
+// instructions, where comparing 24 experts per lane with 8 picks took 480.
 template <int LPR, int NV, int SCORE, bool BF16, bool VEC>
 __global__ __launch_bounds__(kGateThreads) void k_gate_grad(GateGradArgs a) {
+  __shared__ v4f spread[NV][kGateThreads];   // [j][row, lane]: experts 4 (j LPR + lane) ..  of a row
   const int lane = threadIdx.x & (LPR - 1);
   const int64_t t = (int64_t)blockIdx.x * (kGateThreads / LPR) + threadIdx.x / LPR;
   if (t >= a.T) return;
   const char* row = reinterpret_cast<const char*>(a.logits) + t * a.E * (BF16 ? 2 : 4);
+  // lane j holds pick j (K <= LPR)
+  int id = lane < a.K ? a.ids[t * a.K + lane] : -1;
+  if (id < 0 || id >= a.E) id = -1;
+  float dc = id >= 0 ? a.dw[t * a.K + lane] : 0.f;
+  const float lg = id >= 0 ? load_logit<BF16>(row, id) : kNone;
   float l[SCORE == MOE_SCORE_SOFTMAX ? NV : 1][4];
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_logits4<BF16, VEC>(row, 4 * (j * LPR + lane), a.E, l[j]);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) spread[j][threadIdx.x] = v4f{0.f, 0.f, 0.f, 0.f};
+
   float top = kNone, sum = 1.f;
   if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      load_logits4<BF16, VEC>(row, 4 * (j * LPR + lane), a.E, l[j]);
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, l[j][i]);
-    }
     top = row_max<LPR>(top);
     sum = 0.f;
 #pragma unroll
@@ -47,14 +60,9 @@ __global__ __launch_bounds__(kGateThreads) void k_gate_grad(GateGradArgs a) {
   }
   const float inv_sum = sum > 0.f ? 1.f / sum : 0.f;
 
-  // lane j holds pick j (K <= LPR): its score and upstream gradient
-  int id = lane < a.K ? a.ids[t * a.K + lane] : -1;
-  if (id < 0 || id >= a.E) id = -1;
-  const float lg = id >= 0 ? load_logit<BF16>(row, id) : kNone;
   float s, slope = 0.f;
   if constexpr (SCORE == MOE_SCORE_SOFTMAX) s = score_of<SCORE>(lg, top, sum);
   else score_and_slope<SCORE>(lg, s, slope);
-  float dc = id >= 0 ? a.dw[t * a.K + lane] : 0.f;
   if (a.renorm) {
     const float S = row_sum<LPR>(s) + 1e-20f;
     dc = (dc - row_sum<LPR>(dc * s) / S) / S;
@@ -64,36 +72,50 @@ __global__ __launch_bounds__(kGateThreads) void k_gate_grad(GateGradArgs a) {
   if constexpr (SCORE == MOE_SCORE_SOFTMAX) pd = row_sum<LPR>(dc * s);
   else dc *= slope;
 
-  float g[NV][4];
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) g[j][i] = 0.f;
-  const int group = (threadIdx.x & 63) & ~(LPR - 1);   // first lane of this row in the wave
+  __builtin_amdgcn_wave_barrier();
+  float* flat = reinterpret_cast<float*>(spread);
+  const int group = id >= 0 ? id >> 2 : 0;   // expert 4 group + i is spread[group / LPR][row's lane group % LPR][i]
+  float* mine = flat + 4 * (group / LPR * kGateThreads + (threadIdx.x & ~(LPR - 1)) + (group & (LPR - 1))) + (id & 3);
   for (int k = 0; k < a.K; ++k) {
-    const int idk = __shfl(id, group + k);
-    const float dck = __shfl(dc, group + k);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) g[j][i] += 4 * (j * LPR + lane) + i == idk ? dck : 0.f;
+    if (lane == k && id >= 0) *mine += dc;
+    __builtin_amdgcn_wave_barrier();
   }
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int e0 = 4 * (j * LPR + lane);
+  auto gradient = [&](int j) {
+    v4f g = spread[j][threadIdx.x];
     if constexpr (SCORE == MOE_SCORE_SOFTMAX)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) g[j][i] = l[j][i] * inv_sum * (g[j][i] - pd);
-    if constexpr (VEC) {
-      if (e0 < a.E) {
-        v4f o{g[j][0], g[j][1], g[j][2], g[j][3]};
-        if (a.add) o += *reinterpret_cast<const v4f*>(a.add + t * a.E + e0);
-        *reinterpret_cast<v4f*>(a.dl + t * a.E + e0) = o;
+      for (int i = 0; i < 4; ++i) g[i] = l[j][i] * inv_sum * (g[i] - pd);
+    return g;
+  };
+  float* dl = a.dl + t * a.E;
+  if constexpr (VEC) {
+    if (a.add) {   // every load ahead of the stores, which may go to the same tensor
+      v4f add[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e0 = 4 * (j * LPR + lane);   // past the end: any of the row
+        add[j] = *reinterpret_cast<const v4f*>(a.add + t * a.E + (e0 < a.E ? e0 : 0));
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e0 = 4 * (j * LPR + lane);
+        if (e0 < a.E) *reinterpret_cast<v4f*>(dl + e0) = gradient(j) + add[j];
       }
     } else {
 #pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e0 = 4 * (j * LPR + lane);
+        if (e0 < a.E) *reinterpret_cast<v4f*>(dl + e0) = gradient(j);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e0 = 4 * (j * LPR + lane);
+      const v4f g = gradient(j);
+#pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (e0 + i < a.E) a.dl[t * a.E + e0 + i] = g[j][i] + (a.add ? a.add[t * a.E + e0 + i] : 0.f);
+        if (e0 + i < a.E) dl[e0 + i] = g[i] + (a.add ? a.add[t * a.E + e0 + i] : 0.f);
     }
   }
 }
