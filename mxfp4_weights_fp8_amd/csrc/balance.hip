@@ -55,7 +55,7 @@ __device__ __forceinline__ void load_coef(const int32_t* counts, int E, float fa
     const int e0 = 4 * (j * LPR + lane);
     v4i c{0, 0, 0, 0};
     if constexpr (VEC) {
-      if (e0 < E) c = *reinterpret_cast<const v4i*>(counts + e0);
+      c = *reinterpret_cast<const v4i*>(counts + (e0 < E ? e0 : 0));   // groups past the end have no scores
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)

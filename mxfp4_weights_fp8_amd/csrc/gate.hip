@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
       const int e0 = 4 * (j * LPR + lane);
       v4f bias{0.f, 0.f, 0.f, 0.f};
       if constexpr (VEC) {
-        if (e0 < a.E) bias = *reinterpret_cast<const v4f*>(a.bias + e0);
+        bias = *reinterpret_cast<const v4f*>(a.bias + (e0 < a.E ? e0 : 0));   // groups past the end are masked
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

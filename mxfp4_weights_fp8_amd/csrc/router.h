@@ -37,25 +37,22 @@ __device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, kNone), 
 // Four logits of experts e0 .. e0 + 3 of a row; experts from E on are masked.
 template <bool BF16, bool VEC>
 __device__ __forceinline__ void load_logits4(const void* row, int e0, int E, float (&v)[4]) {
-  if constexpr (VEC) {   // E % 4 == 0
-    if (e0 < E) {
-      if constexpr (BF16) {
-        const uint2 r = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(row) + e0);
-        v[0] = __uint_as_float(r.x << 16);
-        v[1] = __uint_as_float(r.x & 0xFFFF0000u);
-        v[2] = __uint_as_float(r.y << 16);
-        v[3] = __uint_as_float(r.y & 0xFFFF0000u);
-      } else {
-        const v4f r = *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(row) + e0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = r[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = clean(v[i]);
+  if constexpr (VEC) {   // E % 4 == 0; groups past the end load any of the row: no branch
+    const bool in = e0 < E;
+    const int at = in ? e0 : 0;
+    if constexpr (BF16) {
+      const uint2 r = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(row) + at);
+      v[0] = __uint_as_float(r.x << 16);
+      v[1] = __uint_as_float(r.x & 0xFFFF0000u);
+      v[2] = __uint_as_float(r.y << 16);
+      v[3] = __uint_as_float(r.y & 0xFFFF0000u);
     } else {
+      const v4f r = *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(row) + at);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = kNone;
+      for (int i = 0; i < 4; ++i) v[i] = r[i];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = in ? clean(v[i]) : kNone;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
