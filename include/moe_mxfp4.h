@@ -295,7 +295,8 @@ int moe_ffn_quantized(const moe_dims* dims, const uint8_t* x_q, const uint8_t* x
  * product (the router's logits, projections), the router's gate, and for tuning a
  * router its balance loss; with the gradients of all of them. The conventions at the
  * top hold; every pointer below must be 16-byte aligned (MOE_EINVAL otherwise), rows
- * are contiguous, and T or M is at most 2^21 (MOE_EUNSUPPORTED). Sums, norms and
+ * are contiguous, an output overlaps an input only where its entry says so, and T or M
+ * is at most 2^21 (MOE_EUNSUPPORTED). Sums, norms and
  * scores are formed in fp32 or better, outputs are rounded once. */
 enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 };
 

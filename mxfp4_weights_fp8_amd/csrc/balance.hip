@@ -114,10 +114,6 @@ __device__ __forceinline__ float balance_row(const BalanceArgs& a, int64_t t, in
   return dot;
 }
 
-__global__ __launch_bounds__(256) void k_fill_zero(int32_t* p, int64_t n) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
-}
-
 // Picks of tokens [first, end) into an LDS histogram.
 __device__ __forceinline__ void count_picks(const BalanceArgs& a, int64_t first, int64_t end, int32_t* hist) {
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
@@ -261,9 +257,8 @@ hipError_t launch_balance(const moe_gate_dims& d, int B, float alpha, const void
     });
     return hipGetLastError();
   }
-  const int64_t nc = (int64_t)B * d.E;
-  hipLaunchKernelGGL(k_fill_zero, dim3((unsigned)(ceil_div(nc, 256) < 1024 ? ceil_div(nc, 256) : 1024)), dim3(256), 0,
-                     s, counts, nc);
+  hipError_t err = launch_fill_zero(counts, (int64_t)B * d.E, s);
+  if (err != hipSuccess) return err;
   if (n > 0) {
     hipLaunchKernelGGL(k_balance_count, dim3((unsigned)ceil_div(d.T, kCountRows)), dim3(256), sizeof(int32_t) * d.E, s, a);
     by_experts(d.E, false, [&](auto lpr, auto nv) {

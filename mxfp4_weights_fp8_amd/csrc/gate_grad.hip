@@ -72,13 +72,13 @@ __global__ __launch_bounds__(kGateThreads) void k_gate_grad(GateGradArgs a) {
   if constexpr (SCORE == MOE_SCORE_SOFTMAX) pd = row_sum<LPR>(dc * s);
   else dc *= slope;
 
-  __builtin_amdgcn_wave_barrier();
+  wave_sync();
   float* flat = reinterpret_cast<float*>(spread);
   const int group = id >= 0 ? id >> 2 : 0;   // expert 4 group + i is spread[group / LPR][row's lane group % LPR][i]
   float* mine = flat + 4 * (group / LPR * kGateThreads + (threadIdx.x & ~(LPR - 1)) + (group & (LPR - 1))) + (id & 3);
   for (int k = 0; k < a.K; ++k) {
     if (lane == k && id >= 0) *mine += dc;
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
   }
   auto gradient = [&](int j) {
     v4f g = spread[j][threadIdx.x];

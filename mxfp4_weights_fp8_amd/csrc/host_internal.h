@@ -223,6 +223,7 @@ hipError_t launch_add_norm_grad(const uint16_t* dy, const uint16_t* h, const voi
                                 uint16_t* dx, float* dw, float* parts, int T, int H, float eps, hipStream_t s);
 // out[c] = sum over p of parts[p][c], c < n, in a fixed order.
 hipError_t launch_sum_parts(const float* parts, int n_parts, int n, float* out, hipStream_t s);
+hipError_t launch_fill_zero(int32_t* p, int64_t n, hipStream_t s);   // n >= 1
 // Dense product and its gradient (linear.h has what the two share).
 size_t linear_parts_bytes(int M, int N, int K);
 hipError_t launch_linear(const moe_linear_dims& d, const uint16_t* x, const uint16_t* w, const float* bias,

@@ -1,4 +1,5 @@
-// Reductions over 16 or 64 neighbouring lanes without LDS.
+// Reductions over 16 or 64 neighbouring lanes without LDS, and the ordering of LDS
+// accesses between the lanes of a wave.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -47,6 +48,14 @@ __device__ __forceinline__ float row_sum(float v) {
   return __int_as_float(row_reduce<LPR>(__float_as_int(v), [](int a, int b) {
     return __float_as_int(__int_as_float(a) + __int_as_float(b));
   }));
+}
+
+// LDS accesses of the wave's lanes before this are seen by all of its lanes after it: a
+// wave's LDS operations complete in order, so this only keeps the compiler from moving
+// them.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 }  // namespace moe

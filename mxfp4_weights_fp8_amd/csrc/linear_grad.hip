@@ -79,10 +79,9 @@ size_t linear_grad_ws_bytes(int M, int N, int K) { return grad_ws_layout(M, N, K
 
 hipError_t launch_linear_grad(const moe_linear_dims& d, const void* dy, const uint16_t* x, const uint16_t* w,
                               const float* z, uint16_t* dx, uint16_t* dw, float* db, void* ws, hipStream_t s) {
-  if (d.M == 0) {   // sums over no rows; dw as N K / 2 zero words
-    hipError_t err = dw ? launch_sum_parts(nullptr, 0, (int)((int64_t)d.N * d.K / 2), reinterpret_cast<float*>(dw), s)
-                        : hipSuccess;
-    return err == hipSuccess && db ? launch_sum_parts(nullptr, 0, d.N, db, s) : err;
+  if (d.M == 0) {   // sums over no rows
+    hipError_t err = dw ? launch_fill_zero(reinterpret_cast<int32_t*>(dw), (int64_t)d.N * d.K / 2, s) : hipSuccess;
+    return err == hipSuccess && db ? launch_fill_zero(reinterpret_cast<int32_t*>(db), d.N, s) : err;
   }
   GradWs g;
   grad_ws_layout(d.M, d.N, d.K, ws, &g);

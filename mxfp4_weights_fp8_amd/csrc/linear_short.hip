@@ -15,6 +15,7 @@
 // step g + kRing. The wait counts the loads issued after those of g + 1; stores that
 // are still on their way only make it wait longer. The epilogue loads nothing (no bias,
 // residual or activation): the wait for a load would be a wait for every copy.
+#include "lane_reduce.h"
 #include "linear.h"
 #include "linear_stage.h"
 
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
     for (int j = 0; j < FT; ++j) {
 #pragma unroll
       for (int i = 0; i < FW; ++i) *reinterpret_cast<v4f*>(out + c * kOutRow + 16 * i + 4 * q) = acc[i][j];
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       const int64_t mw = m0 + 64 * wave + 16 * j + q;
       const int n = t * kShortCols + 8 * c;
       const float* src = out + q * kOutRow + 8 * c;
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
       for (int u = 0; u < 4; ++u)
         finish_affine<false>(a, mw + 4 * u, n, *reinterpret_cast<const v4f*>(src + 4 * u * kOutRow),
                       *reinterpret_cast<const v4f*>(src + 4 * u * kOutRow + 4), Residual8<false, F32>{});
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
     }
 #pragma unroll
     for (int i = 0; i < FW; ++i)

@@ -350,6 +350,10 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_sum_parts(const float* __res
   }
 }
 
+__global__ __launch_bounds__(256) void k_fill_zero(int32_t* p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+
 }  // namespace
 
 hipError_t launch_add_norm(const uint16_t* x, const uint16_t* res, const void* w, bool w_f32, uint16_t* h,
@@ -373,6 +377,12 @@ hipError_t launch_add_norm_grad(const uint16_t* dy, const uint16_t* h, const voi
     by_kind(w_f32, past_cache(T, H), [&](auto f, auto nt) { launch_grad<decltype(f)::value, decltype(nt)::value>(a, n, s); });
   }
   return launch_sum_parts(parts, n, H, dw, s);
+}
+
+hipError_t launch_fill_zero(int32_t* p, int64_t n, hipStream_t s) {
+  const int64_t ctas = ceil_div(n, 256);
+  hipLaunchKernelGGL(k_fill_zero, dim3((unsigned)(ctas < 2048 ? ctas : 2048)), dim3(256), 0, s, p, n);
+  return hipGetLastError();
 }
 
 hipError_t launch_sum_parts(const float* parts, int n_parts, int n, float* out, hipStream_t s) {

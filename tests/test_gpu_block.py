@@ -554,6 +554,34 @@ def test_block_from_residual_to_experts(dev, T, Is):
     assert m["finite"] and m["max_rel"] <= 2e-2 and m["mean_rel"] <= 2e-3, m
 
 
+def test_padded_batch(dev):
+    """Rows behind the last token (n_valid): no picks, no part in the plan or the balance
+    loss, y zero; the others are what they are without padding."""
+    T, n = 40, 27
+    inp, ex = _block(dev, T)
+    w = inp.wl
+    W = moe.pack_weights(inp.weights)
+    nv = torch.tensor([n], dtype=torch.int32, device=dev)
+    off = torch.tensor([0, n], dtype=torch.int32, device=dev)
+
+    def run(rows, n_valid, seq):
+        x = inp.x[:rows].contiguous()
+        normed = moe.add_norm(x, ex["norm"], residual=ex["res"][:rows].contiguous())
+        logits = moe.linear(normed.y, ex["router"], dtype=F32)
+        ids, tw = moe.gate(logits, w.K, score="sigmoid", bias=ex["bias"], n_valid=n_valid)
+        p = moe.plan(ids, w.E, w.H, w.I)
+        y = moe.ffn_quantized(normed.x_q, normed.x_s, tw, p, W)
+        return ids, tw, p, y, moe.balance_loss(logits, ids, 0.1, score="sigmoid", seq_offsets=seq)
+    ids, tw, p, y, bal = run(T, nv, off)
+    ids1, tw1, p1, y1, bal1 = run(n, None, None)
+    torch.cuda.synchronize()
+    assert bool((ids[n:] == -1).all()) and bool((tw[n:] == 0).all()) and int(p.status) == (T - n) * w.K
+    assert bool((y[n:] == 0).all()) and bool((bal[2][n:] == 0).all())
+    assert torch.equal(ids[:n], ids1) and torch.equal(tw[:n], tw1)
+    assert torch.equal(y[:n].view(torch.int16), y1.view(torch.int16))
+    assert torch.equal(bal[1], bal1[1]) and torch.equal(bal[0], bal1[0]) and torch.equal(bal[2][:n], bal1[2])
+
+
 @pytest.mark.parametrize("T,Is,flags", [(7, 0, 0), (7, 128, 0), (300, 128, 0), (7, 0, moe.FLAG_DECODE_CHAIN),
                                         (7, 128, moe.FLAG_DECODE_CHAIN), (0, 0, 0)])
 def test_ffn_quantized_equals_ffn(dev, T, Is, flags):
