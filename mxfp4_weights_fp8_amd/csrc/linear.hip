@@ -79,8 +79,6 @@ __global__ __launch_bounds__(64 * kDotWaves) void k_linear_dot(LinearArgs a) {
 // At most 64 rows: bound by reading the weights. A workgroup owns 16 output columns and
 // one of a.splits shares of the contraction; its waves take every W-th step of 64 K,
 // straight from memory into registers, and add their sums through LDS in wave order.
-// Lane (c, q) reads bytes 32q .. 32q+31 of its row's 128-byte step: as K is summed, the
-// two operands only have to agree on which K a lane holds.
 constexpr int kSmallWaves = 16;
 
 template <int FT>
@@ -91,10 +89,10 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_linear_small(LinearArgs a)
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int n0 = blockIdx.x * 16, split = blockIdx.y;
   const int first = a.C / 64 * split / a.splits, steps = a.C / 64 * (split + 1) / a.splits;
-  const uint16_t* w = a.w + (int64_t)min(n0 + c, a.N - 1) * a.ws + q * 16;   // rows past the end: any valid row
+  const uint16_t* w = a.w + (int64_t)min(n0 + c, a.N - 1) * a.ws + q * 8;   // rows past the end: any valid row
   const uint16_t* x[FT];
 #pragma unroll
-  for (int f = 0; f < FT; ++f) x[f] = a.x + (int64_t)min(16 * f + c, a.M - 1) * a.xs + q * 16;
+  for (int f = 0; f < FT; ++f) x[f] = a.x + (int64_t)min(16 * f + c, a.M - 1) * a.xs + q * 8;
   v4f acc[FT] = {};
   for (int s = first + wave; s < steps; s += waves * kSmallDepth) {
     v4i wv[kSmallDepth][2], xv[kSmallDepth][FT][2];
@@ -104,9 +102,9 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_linear_small(LinearArgs a)
       if (st < steps) {   // wave-uniform
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          wv[d][h] = load16(w + st * 64 + 8 * h);
+          wv[d][h] = load16(w + st * 64 + 32 * h);
 #pragma unroll
-          for (int f = 0; f < FT; ++f) xv[d][f][h] = load16(x[f] + st * 64 + 8 * h);
+          for (int f = 0; f < FT; ++f) xv[d][f][h] = load16(x[f] + st * 64 + 32 * h);
         }
       }
     }
@@ -164,11 +162,16 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a) {
 // tile share a CU), prologue and epilogue `fixed` per round of tiles, and joining the
 // parts of a split product 4 us and its traffic at 4 TB/s. (8192^3: 256 x 256 tiles 851
 // us, 128 x 128 971; 8191 x 7168 x 2048: 310 and 266; 4096 x 2048 x 7168: 256 x 256 split
-// in two 112, 128 x 128 110, unsplit 256 x 256 168.)
+// in two 112, 128 x 128 110, unsplit 256 x 256 168; 16384 x 7168 x 384 without epilogue:
+// 256 x 256 129, 128 x 128 133, rows kept in registers 107.)
 LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain) {
-  if (M <= 64 && l == Layout::kRows) {
+  // Few rows. The vector units up to 1536 columns: 7 x 384 x 7168 8.2 us against 10.2 us
+  // by kSmall, 8 x 1536 x 4096 8.5 against 10.1, but 8 x 2048 x 7168 14.9 against 10.7. Above
+  // 16 rows kSmall while its workgroups' reads of x, M N K / 8 bytes, stay small: 64 x 4096 x
+  // 2048 11.8 us against 15.8 us in tiles, 64 x 7168 x 7168 75 against 30.
+  if (l == Layout::kRows && (M <= 16 || (M <= 64 && (int64_t)M * N * C <= 800000000))) {
     const int64_t tiles = ceil_div(N, 16), steps = C / 64;
-    if (M <= 8 && N <= 2048) return LinearPlan{Path::kDot, 0, 0, 1};
+    if (M <= 8 && N <= 1536) return LinearPlan{Path::kDot, 0, 0, 1};
     // fewer workgroups than CUs: split the contraction, at least 8 steps each
     int64_t splits = 256 / tiles;
     if (splits > steps / 8) splits = steps / 8;
@@ -182,7 +185,8 @@ LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain) {
   int64_t least = -1;
   for (const auto& t : kShapes) {
     const int64_t tiles = ceil_div(M, 32 * t.ft) * ceil_div(N, 32 * t.fw), slots = 256 * t.per_cu;
-    for (int64_t splits = 1; splits == 1 || (splits <= steps / 4 && tiles * splits <= 2 * slots); ++splits) {
+    for (int64_t splits = 1; splits == 1 || (splits <= steps / 4 && tiles * splits <= 2 * slots);
+         splits += splits < 4 ? 1 : splits / 4) {
       int64_t time = ceil_div(tiles * splits, slots) * (ceil_div(steps, splits) * t.step + t.fixed);
       if (splits > 1) time += 400 + splits * M * N * 8 / 40000;
       if (least < 0 || time < least) {
@@ -194,7 +198,7 @@ LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain) {
   if (C <= 384 && N % 8 == 0 && plain && l != Layout::kBothTrans) {   // C is a multiple of 128
     const int64_t n_tiles = ceil_div(N, 128), per = short_tiles_per_cta(M, N);
     const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(n_tiles, per), 256);
-    if (rounds * (500 + per * (steps * 45 + 70)) < least) return LinearPlan{Path::kShort, 0, 0, 1};
+    if (rounds * (500 + per * (steps * 100 + 150)) < least) return LinearPlan{Path::kShort, 0, 0, 1};
   }
   return best;
 }

@@ -195,7 +195,8 @@ def check_linear(dev, M, N, K, act="none", bias=False, res=False, dtype=BF16, z=
 @pytest.mark.parametrize("M,N,K", [(1, 1, 128), (1, 384, 7168), (7, 384, 7168), (16, 17, 256), (17, 16, 384), (33, 100, 1024),
                                    (64, 7, 2048), (3, 4097, 128), (64, 512, 8192), (48, 30, 128),
                                    (8, 769, 640), (5, 2048, 1152), (4, 767, 896), (2, 2049, 256), (40, 384, 7168),
-                                   (9, 33, 4096), (1, 770, 8192)])
+                                   (9, 33, 4096), (1, 770, 8192), (6, 1536, 256), (7, 1537, 1024),
+                                   (17, 8192, 7168), (64, 6001, 4096)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_linear_few_rows(dev, M, N, K, dtype):
     check_linear(dev, M, N, K, dtype=dtype, bias=N % 2 == 0, res=K < 1024, seed=M + N)
