@@ -162,8 +162,7 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a) {
 // tile share a CU), prologue and epilogue `fixed` per round of tiles, and joining the
 // parts of a split product 4 us and its traffic at 4 TB/s. (8192^3: 256 x 256 tiles 851
 // us, 128 x 128 971; 8191 x 7168 x 2048: 310 and 266; 4096 x 2048 x 7168: 256 x 256 split
-// in two 112, 128 x 128 110, unsplit 256 x 256 168; 16384 x 7168 x 384 without epilogue:
-// 256 x 256 129, 128 x 128 133, rows kept in registers 107.)
+// in two 112, 128 x 128 110, unsplit 256 x 256 168.)
 LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain) {
   // Few rows. The vector units up to 1536 columns: 7 x 384 x 7168 8.2 us against 10.2 us
   // by kSmall, 8 x 1536 x 4096 8.5 against 10.1, but 8 x 2048 x 7168 14.9 against 10.7. Above
@@ -195,11 +194,12 @@ LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain) {
       }
     }
   }
-  if (C <= 384 && N % 8 == 0 && plain && l != Layout::kBothTrans) {   // C is a multiple of 128
-    const int64_t n_tiles = ceil_div(N, 128), per = short_tiles_per_cta(M, N);
-    const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(n_tiles, per), 256);
-    if (rounds * (500 + per * (steps * 100 + 150)) < least) return LinearPlan{Path::kShort, 0, 0, 1};
-  }
+  // A contraction of up to 384 that needs no epilogue: rows kept in registers, once the
+  // result is large enough for a pipeline that starts once. In us, rows kept and tiles, at
+  // 384: 4096 x 7168 37 and 35, 8192 x 7168 59 and 67, 16384 x 7168 103 and 125, 32768 x 2048
+  // 61 and 74, 4096 x 2048 17 and 13; at 128: 8192 x 7168 34 and 43, 16384 x 7168 58 and 79.
+  if (C <= 384 && N % 8 == 0 && plain && l != Layout::kBothTrans && (int64_t)M * N >= 40000000)   // C is a multiple of 128
+    return LinearPlan{Path::kShort, 0, 0, 1};
   return best;
 }
 

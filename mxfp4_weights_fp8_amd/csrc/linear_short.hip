@@ -173,13 +173,9 @@ void run(const LinearArgs& a, bool w_trans, hipStream_t s) {
   const int total = m_tiles * (int)ceil_div(n_tiles, per);
   const dim3 grid((unsigned)(ceil_div(total, kXcds) * kXcds)), block(kShortThreads);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a, m_tiles, n_tiles, per, total); };
-  if (w_trans) {
-    if (a.out_f32) go(k_linear_short<KS, true, true>);
-    else go(k_linear_short<KS, true, false>);
-  } else {
-    if (a.out_f32) go(k_linear_short<KS, false, true>);
-    else go(k_linear_short<KS, false, false>);
-  }
+  if (w_trans) go(k_linear_short<KS, true, false>);   // an input's gradient, always bf16
+  else if (a.out_f32) go(k_linear_short<KS, false, true>);
+  else go(k_linear_short<KS, false, false>);
 }
 
 }  // namespace

@@ -217,7 +217,7 @@ def test_linear_large_tiles(dev, M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(1001, 8200, 128), (8203, 776, 256), (16390, 2504, 384), (70, 8, 128), (257, 120, 384),
-                                   (12003, 1000, 512), (129, 640, 2048)])
+                                   (5003, 8008, 128), (4999, 8072, 256), (12003, 1000, 512), (129, 640, 2048)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_linear_without_epilogue(dev, M, N, K, dtype):
     check_linear(dev, M, N, K, dtype=dtype, seed=N)
@@ -264,7 +264,8 @@ def test_linear_no_rows(dev):
     # every tile shape of both gradients, and runs of column tiles for a short contraction
     (128, 1000, 8192, "none", F32), (128, 12001, 1024, "none", BF16), (2048, 16500, 768, "none", BF16),
     (1000, 500, 8192, "relu", BF16), (12000, 500, 1024, "none", BF16), (16500, 2000, 768, "none", BF16),
-    (5003, 300, 2048, "silu", F32), (3001, 120, 4096, "none", BF16)])
+    (5003, 300, 2048, "silu", F32), (3001, 120, 4096, "none", BF16),
+    (5003, 100, 8064, "none", BF16), (5001, 200, 8064, "relu", BF16), (4997, 300, 8064, "none", BF16)])
 def test_linear_grad(dev, M, N, K, act, dtype):
     x, w = randn(M, K, seed=1, dtype=BF16), randn(N, K, seed=2, scale=1 / math.sqrt(K), dtype=BF16)
     dy = randn(M, N, seed=3, dtype=dtype)
