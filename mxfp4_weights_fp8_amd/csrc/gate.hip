@@ -277,11 +277,10 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
   // weight of the lane's pick, from its logit again
   const bool pick = pos < a.K;
   const float s = !pick || mine == kNoIndex ? 0.f : score_of<SCORE>(load_logit<BF16>(row, mine), top, sum);
-  float mul = a.scale;
-  if (a.renorm) mul = a.scale / (row_sum<LPR>(s) + 1e-20f);
+  const float sum_picked = a.renorm ? row_sum<LPR>(s) + 1e-20f : 1.f;
   if (pick) {
     ids[pos] = mine == kNoIndex ? -1 : mine;
-    w[pos] = s * mul;
+    w[pos] = s / sum_picked * a.scale;   // the quotient first: at most 1, whatever the scale
   }
 }
 

@@ -406,6 +406,16 @@ def test_gate_valid_counts(dev, n):
     check_gate(dev, randn(9, 30, seed=1), 4, f"n_valid={n}", "sigmoid", n_valid=n)
 
 
+def test_gate_large_scale(dev):
+    """Rows without any pick have weights of 0 whatever the scale; the others' stay finite."""
+    l = randn(5, 20, seed=1)
+    l[1] = -math.inf
+    l[3, 2:] = -math.inf
+    for score in SCORES:
+        for renorm in (False, True):
+            check_gate(dev, l, 4, f"scale 2^100 {score} renorm={renorm}", score, renorm=renorm, scale=2.0 ** 100)
+
+
 def check_gate_grad(dev, l, ids, dw, score, renorm, scale, add, what):
     ld, idd, dwd, addd = on(dev, l, ids, dw, add)
     dl = moe.gate_grad(ld, idd, dwd, score=score, renorm=renorm, scale=scale, add=addd)
