@@ -281,9 +281,10 @@ int moe_ffn_nvfp4(const moe_dims* dims, const uint16_t* x, const float* topk_wei
  * moe_quant_act): x_q [T, H] E4M3 codes and x_s [T, H/128] E8M0 scales in place of
  * x, everything else as moe_ffn, and bit for bit its result where the codes are
  * moe_quant_act's. No quantizer is launched; with a shared expert the codes are
- * expanded to bf16 once. dbg->x_q and dbg->x_s are not written.
+ * expanded to bf16 once. dbg->x_q and dbg->x_s are not written. x_s may be rows of a
+ * larger tensor: 4-byte aligned where H is a multiple of 512, any address otherwise.
  * Errors: as moe_ffn; MOE_EINVAL also with MOE_FLAG_A16 or MOE_FLAG_NVFP4 (bf16
- * activations). */
+ * activations) and for an x_q or x_s that is not aligned. */
 int moe_ffn_quantized(const moe_dims* dims, const uint8_t* x_q, const uint8_t* x_s, const float* topk_weights,
                       const int32_t* expert_offsets, const int32_t* sorted_pairs, const int32_t* pair_rows,
                       const void* plan_ws, const uint8_t* w13, const uint8_t* w13_s, const uint8_t* w2,
@@ -312,8 +313,9 @@ enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 };
  *   x_q, x_s   [T, H] E4M3 codes and [T, H/128] E8M0 scales of y (moe_ffn_quantized's
  *              operand; the rule of moe_quant_act, applied to y before its rounding to
  *              bf16), both NULL: not written
- * A row with infinities or NaN, or with squares that overflow fp32, gives
- * non-finite or zero outputs in that row alone.
+ * A row with infinities or NaN, with squares that overflow fp32, or with eps 0 and
+ * squares that all underflow (a row of zeros among them) gives non-finite or zero
+ * outputs in that row alone.
  * Errors: MOE_EINVAL (also x_q without x_s, or no output), MOE_EUNSUPPORTED, MOE_EHIP. */
 int moe_add_norm(int32_t T, int32_t H, float eps, const uint16_t* x, const uint16_t* residual, const void* weight,
                  int32_t weight_type, uint16_t* h, uint16_t* y, uint8_t* x_q, uint8_t* x_s, void* stream);

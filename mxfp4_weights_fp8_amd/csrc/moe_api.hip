@@ -397,6 +397,9 @@ int moe_ffn_quantized(const moe_dims* dims, const uint8_t* x_q, const uint8_t* x
   if (rc == MOE_OK && bf16_rows(*dims)) return MOE_EINVAL;   // bf16 activations: not quantized
   if (rc != MOE_OK || dims->T == 0) return rc;
   if (!x_s || !ws) return MOE_EINVAL;
+  // codes are loaded in 16 byte pieces; scales in dwords where rows are whole dwords, else in bytes
+  if (reinterpret_cast<uintptr_t>(x_q) % 16 || (dims->H % 512 == 0 && reinterpret_cast<uintptr_t>(x_s) % 4))
+    return MOE_EINVAL;
   if (ws_bytes < ffn_ws_layout(*dims, nullptr, nullptr)) return MOE_EWORKSPACE;
   return ffn_enqueue(*dims, nullptr, topk_weights, expert_offsets, sorted_pairs, pair_rows, plan_ws, w13, w13_s, w2,
                      w2_s, shared, y, dbg, ws, (hipStream_t)stream, nullptr, nullptr, x_q, x_s);

@@ -55,7 +55,7 @@ EI, EU, EW = moe.MOE_EINVAL, moe.MOE_EUNSUPPORTED, moe.MOE_EWORKSPACE
     (norm, dict(y=ODD), EI), (norm, dict(T=0, x=None), 0),
     (norm_grad, dict(H=100), EU), (norm_grad, dict(dy=None), EI), (norm_grad, dict(h=None), EI),
     (norm_grad, dict(dx=None), EI), (norm_grad, dict(dw=None), EI), (norm_grad, dict(ws=None), EI),
-    (norm_grad, dict(dh=ODD), EI), (norm_grad, dict(n=4 * 4 * 256 - 1), EW), (norm_grad, dict(T=0, w=None), EI),
+    (norm_grad, dict(dh=ODD), EI), (norm_grad, dict(n=4 * 256 - 1), EW), (norm_grad, dict(T=0, w=None), EI),
     (linear, dict(M=-1), EI), (linear, dict(N=0), EI), (linear, dict(K=0), EI), (linear, dict(K=192), EU),
     (linear, dict(act=5), EI), (linear, dict(act=-1), EI), (linear, dict(type=2), EI), (linear, dict(N=65537), EU),
     (linear, dict(K=65536 + 128), EU), (linear, dict(N=65536, K=32768), EU), (linear, dict(M=(1 << 21) + 1), EU),
@@ -98,6 +98,11 @@ def test_ffn_quantized_checks():
     assert call(d, ok, ws=None) == EI
     for i in range(11):
         assert call(d, ok[:i] + [None] + ok[i + 1:]) == EI, i
+    assert call(d, [ODD] + ok[1:]) == EI
+    d512 = moe.make_dims(4, 512, 512, 8, 2)
+    assert call(d512, [P, ctypes.c_void_p(0x1002)] + ok[2:]) == EI
+    assert call(d512, [P, ctypes.c_void_p(0x1004)] + ok[2:], n=16) == EW     # aligned enough: the next check fails
+    assert call(d, [P, ctypes.c_void_p(0x1001)] + ok[2:], n=16) == EW
     for flags in (moe.FLAG_A16, moe.FLAG_NVFP4):
         assert call(moe.make_dims(4, 256, 512, 8, 2, flags=flags), ok) == EI
     assert call(moe.make_dims(4, 200, 512, 8, 2), ok) == EU

@@ -520,6 +520,96 @@ def test_balance_loss_unordered_offsets_stay_in_bounds(dev):
     assert counts.shape == (5, 16) and dl.shape == (100, 16)
 
 
+
+# ------------------------------------------------------------ offsets past 32 bits
+
+
+@pytest.fixture
+def room(dev):
+    yield
+    torch.cuda.empty_cache()
+
+
+def tail_rows(dev, rows, cols, last, dtype=BF16, fill=0.0):
+    """[rows, cols] of `fill` whose last rows are `last`."""
+    t = torch.full((rows, cols), fill, dtype=dtype, device=dev)
+    t[rows - last.shape[0]:] = last.to(dev)
+    return t
+
+
+def test_add_norm_past_32_bits(dev, room):
+    T, H, n = 300007, 7168, 5                     # 2.15e9 elements
+    x, res, w = randn(n, H, seed=1, dtype=BF16), randn(n, H, seed=2, dtype=BF16), 1 + randn(H, seed=3, scale=0.2)
+    xd, rd, wd = tail_rows(dev, T, H, x, fill=1.0), tail_rows(dev, T, H, res, fill=1.0), w.to(dev)
+    say(f"[add_norm {T}x{H}]")
+    out = moe.add_norm(xd, wd, residual=rd)
+    check_normed(moe.Normed(*(t[-n:] for t in out)), x, w, res, 1e-6, "last rows")
+    check_normed(moe.Normed(*(t[:n] for t in out)), torch.ones(n, H, dtype=BF16), w, torch.ones(n, H, dtype=BF16), 1e-6, "first rows")
+    say(f"[add_norm_grad {T}x{H}]")
+    dy = tail_rows(dev, T, H, x)                  # zeros, so that dweight is the last rows' alone
+    dx, dw = moe.add_norm_grad(dy, rd, wd)
+    small, dw_small = moe.add_norm_grad(x.to(dev), res.to(dev), wd)
+    assert torch.equal(dx[-n:], small) and not bool(dx[:1000].any())
+    rdw = ob.add_norm_grad_ref(x, res, w, 1e-6, None)[1]
+    h64 = res.to(F64)
+    tol = (x.to(F64).abs() * h64.abs() / ((h64 * h64).mean(1, keepdim=True) + 1e-6).sqrt()).sum(0) * (n + NORM_TERMS + 16) * U
+    within(dw, rdw, tol, "dweight")
+    within(dw_small, rdw, tol, "dweight of the rows alone")
+
+
+def test_linear_past_32_bits(dev, room):
+    n = 70
+    # the rows of x, then the rows of y without and with an epilogue
+    for M, N, K, bias in ((262149, 16, 8192, False), (1048579, 2056, 128, False), (1048579, 2056, 128, True)):
+        x, w = randn(n, K, seed=1, dtype=BF16), randn(N, K, seed=2, scale=1 / math.sqrt(K), dtype=BF16)
+        b = randn(N, seed=3) if bias else None
+        say(f"[linear {M}x{N}x{K} bias={bias}]")
+        y = moe.linear(tail_rows(dev, M, K, x), *on(dev, w, b))
+        ref, z = ob.linear_ref(x, w, b)
+        within(y[-n:], ref, product_tol(x, w, K) + ref.abs() * (BF + 16 * U), "last rows")
+        within(y[:n], (torch.zeros(n, N) if b is None else b.expand(n, N)).to(F64), BF * (0 if b is None else b.abs().to(F64)), "first rows")
+        del y
+
+
+def test_linear_grad_past_32_bits(dev, room):
+    n = 70
+    for M, N, K in ((1048579, 2056, 128), (1048579, 16, 2176)):    # dy and dz; x and dx
+        x, w = randn(n, K, seed=1, dtype=BF16), randn(N, K, seed=2, scale=1 / math.sqrt(K), dtype=BF16)
+        dy = randn(n, N, seed=3, dtype=BF16)
+        say(f"[linear_grad {M}x{N}x{K}]")
+        dx, dw, db = moe.linear_grad(tail_rows(dev, M, N, dy), tail_rows(dev, M, K, x, fill=1.0), w.to(dev))
+        rdx, rdw, rdb, dz = ob.linear_grad_ref(dy, x, w, "none", None)
+        ax, aw = dz.abs() @ w.to(F64).abs(), dz.abs().t() @ x.to(F64).abs()
+        within(dx[-n:], rdx, rdx.abs() * BF + ax * (N / 32 + 64) * 2 * U, "dx")
+        assert not bool(dx[:1000].any())
+        within(dw, rdw, rdw.abs() * BF + aw * (n / 32 + 64) * 2 * U, "dw")
+        within(db, rdb, dz.abs().sum(0) * (n + 64) * U, "dbias")
+        del dx, dw, db
+
+
+def test_router_past_32_bits(dev, room):
+    T, E, K, n = 1048579, 2056, 8, 40
+    l, dw = randn(n, E, seed=1, scale=2.0), randn(n, K, seed=2)
+    ld = tail_rows(dev, T, E, l, dtype=F32)
+    say(f"[gate {T}x{E}]")
+    ids, w = moe.gate(ld, K)
+    rids, rw = ob.gate_ref(l, K, "softmax")
+    assert torch.equal(ids[-n:].cpu(), rids)
+    within(w[-n:], rw, rw * weight_tol(E), "weights")
+    assert bool((ids[:n] == torch.arange(K, device=dev)).all())    # equal logits: the lowest indices
+    say(f"[balance_loss {T}x{E}]")
+    off = torch.tensor([0, T - n, T], dtype=torch.int32, device=dev)
+    loss, counts, dl = moe.balance_loss(ld, ids, 1.0, seq_offsets=off)
+    _, rc, rd, mag = ob.balance_loss_ref(l, rids, 0.5, "softmax", None)
+    assert torch.equal(counts[1:].cpu(), rc) and int(counts[0, 0]) == T - n
+    tol = 6 * weight_tol(E)
+    within(dl[-n:], rd, mag * tol + 1e-30, "balance gradient")
+    say(f"[gate_grad {T}x{E}]")
+    add = dl[-n:].cpu()
+    moe.gate_grad(ld, ids, tail_rows(dev, T, K, dw, dtype=F32), add=dl, d_logits=dl)
+    rg, mag = ob.gate_grad_ref(l, rids, dw, "softmax", True, 1.0, add)
+    within(dl[-n:], rg, mag * 3 * weight_tol(E) + 1e-17, "gradient")
+
 # --------------------------------------------------------- together, graphs, streams
 
 def _block(dev, T, H=512, I=256, E=16, K=4, Is=0, seed=40):
@@ -606,6 +696,23 @@ def test_ffn_quantized_equals_ffn(dev, T, Is, flags):
     x_q, x_s = moe.quant_act(inp.x)
     ws = torch.full((moe.ffn_workspace_bytes(p.dims),), 0xFF, dtype=torch.uint8, device=dev)
     got = moe.ffn_quantized(x_q, x_s, inp.topk_weights, p, W, shared=inp.shared, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("T", [7, 300])
+@pytest.mark.parametrize("H", [384, 512])
+def test_ffn_quantized_on_rows_of_larger_tensors(dev, T, H):
+    """Codes and scales that start at a later row: scales at odd addresses where a row has
+    three of them."""
+    inp, _ = _block(dev, T, H=H)
+    w = inp.wl
+    W = moe.pack_weights(inp.weights)
+    p = moe.plan(inp.topk_ids, w.E, w.H, w.I)
+    want = moe.ffn(inp.x, inp.topk_weights, p, W)
+    x = torch.cat([inp.x[:1], inp.x])
+    x_q, x_s = moe.quant_act(x)
+    got = moe.ffn_quantized(x_q[1:], x_s[1:], inp.topk_weights, p, W)
     torch.cuda.synchronize()
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
