@@ -171,6 +171,11 @@ template <int POLICY = 0>
 __device__ __forceinline__ v4i buf_load16(rsrc_t r, int voff, int soff) {
   return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, POLICY));
 }
+// Bytes past the resource's size are not written.
+__device__ __forceinline__ void buf_store16(rsrc_t r, const v4i v, int voff) {
+  typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, voff, 0, 0);
+}
 // The same load with the nontemporal cache policy (the `nt` bit, cache-policy value
 // 2 on gfx950): for data read once per step, such as the decode weight streams
 // (measured on a stream of that shape: 6.0 -> 6.7 TB/s).

@@ -38,7 +38,7 @@ struct LinearPlan {
   Path path;
   int ft, fw, splits;
 };
-// plain: no bias, residual, activation or z.
+// plain: a bf16 result without bias, residual, activation or z.
 LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain);
 size_t linear_plan_parts(int M, int N, const LinearPlan& p);   // bytes of `parts`
 hipError_t launch_linear_plan(const LinearArgs& a, const LinearPlan& p, Layout l, hipStream_t s);
@@ -192,11 +192,11 @@ struct Residual8 {
   }
 };
 
-template <bool BIAS = true, bool RES, bool F32>
+template <bool RES, bool F32>
 __device__ __forceinline__ void finish_affine(const LinearArgs& a, int64_t m, int n, v4f lo, v4f hi,
                                               const Residual8<RES, F32>& res) {
   if (m >= a.M || n >= a.N) return;
-  if (BIAS && a.bias) {
+  if (a.bias) {
     lo += *reinterpret_cast<const v4f*>(a.bias + n);
     hi += *reinterpret_cast<const v4f*>(a.bias + n + 4);
   }

@@ -196,9 +196,9 @@ LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain) {
   }
   // A contraction of up to 384 that needs no epilogue: rows kept in registers, once the
   // result is large enough for a pipeline that starts once. In us, rows kept and tiles, at
-  // 384: 4096 x 7168 37 and 35, 8192 x 7168 59 and 67, 16384 x 7168 103 and 125, 32768 x 2048
-  // 61 and 74, 4096 x 2048 17 and 13; at 128: 8192 x 7168 34 and 43, 16384 x 7168 58 and 79.
-  if (C <= 384 && N % 8 == 0 && plain && l != Layout::kBothTrans && (int64_t)M * N >= 40000000)   // C is a multiple of 128
+  // 384: 16384 x 1024 25 and 21, 4096 x 7168 33 and 35, 8192 x 7168 52 and 63, 16384 x 7168
+  // 92 and 126, 32768 x 2048 56 and 70; at 128: 4096 x 7168 20 and 25, 16384 x 7168 49 and 76.
+  if (C <= 384 && N % 8 == 0 && plain && l != Layout::kBothTrans && (int64_t)M * N >= 20000000)   // C is a multiple of 128
     return LinearPlan{Path::kShort, 0, 0, 1};
   return best;
 }
@@ -256,7 +256,7 @@ hipError_t launch_linear(const moe_linear_dims& d, const uint16_t* x, const uint
                          const void* res, void* y, float* z, float* parts, hipStream_t s) {
   const LinearArgs a{x, w, d.K, d.K, bias, res, y, z, parts, d.M, d.N, d.K, d.K,
                      d.act, 1, d.type == MOE_TYPE_F32};
-  const bool plain = !bias && !res && !z && d.act == MOE_ACT_NONE;
+  const bool plain = !bias && !res && !z && d.act == MOE_ACT_NONE && d.type == MOE_TYPE_BF16;
   return launch_linear_plan(a, linear_plan(d.M, d.N, d.K, Layout::kRows, plain), Layout::kRows, s);
 }
 

@@ -7,14 +7,17 @@
 // a run of 128-column tiles. Only w goes through LDS: a ring of kRing one-step stages
 // (64 x 128) that runs on across the tiles, so that the next tile's columns arrive
 // during the epilogue. Per 256 x 128 outputs 96 KB are copied, against 4 x 192 KB for
-// the same outputs in 128 x 128 tiles (16384 x 7168 x 384: 152 us in those).
+// the same outputs in 128 x 128 tiles.
 //
 // Step g (tile g / KS, step g % KS): the MFMAs of its first half and the reads of its
 // second; wait for this wave's copies of step g + 1 and barrier, which frees g's stage;
-// the MFMAs of the second half, the reads of step g + 1's first half and the copies of
-// step g + kRing. The wait counts the loads issued after those of g + 1; stores that
-// are still on their way only make it wait longer. The epilogue loads nothing (no bias,
-// residual or activation): the wait for a load would be a wait for every copy.
+// the MFMAs of the second half, the reads of step g + 1's first half, the copies of
+// step g + kRing, and the stores of a share of the previous tile's results, which lie in
+// LDS as bf16. Stored all at once after their tile, they came from every CU at the same
+// time: 16384 x 7168 x 384 103 us, spread over the steps 92 us (without any stores 81).
+// The wait counts what was issued after the copies of g + 1, stores among them; loads
+// and stores leave the counter in the order of their issue. Nothing else is loaded (no
+// bias, residual or activation): the wait for a load would be a wait for every copy.
 #include "lane_reduce.h"
 #include "linear.h"
 #include "linear_stage.h"
@@ -24,7 +27,7 @@ namespace {
 
 constexpr int kShortThreads = 256;
 constexpr int kShortRows = 256, kShortCols = 128;
-constexpr int kRing = 7;
+constexpr int kRing = 5;
 constexpr int kXcds = 8;
 
 // acc += W X: acc and w in VGPRs, x in AGPRs. The compiler does not know that the
@@ -35,14 +38,16 @@ __device__ __forceinline__ void mma_x_agpr(v4f& acc, const v4i& w, const v4i& x)
 #endif
 }
 
-template <int KS, bool WT, bool F32>
+template <int KS, bool WT>
 __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a, int m_tiles, int n_tiles, int per_cta,
                                                                     int total) {
   constexpr int FT = 4, FW = 8;
   typedef Operand<kShortCols, WT> W;
   constexpr int kCopies = W::kCopies;
-  constexpr int kOutRow = kShortCols + 4;   // floats per staged row: 16 rows in distinct banks
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing * W::kBytes + 4 * 16 * kOutRow * 4];
+  constexpr int kOutRow = 2 * kShortCols + 16;   // bytes per staged row: 16 rows in distinct banks
+  constexpr int kStores = 16;                    // of a wave per tile, 4 rows each
+  constexpr int kLeastStores = kStores / KS;     // and step
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing * W::kBytes + 4 * 64 * kOutRow];
 
   // (column run, row tile), each XCD a contiguous share: its L2 holds few column runs
   const int run = (total + kXcds - 1) / kXcds;
@@ -107,22 +112,36 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
 #pragma unroll
   for (int i = 0; i < FW; ++i) w0[i] = rw.template read<0>(smem, i);
 
-  float* const out = reinterpret_cast<float*>(smem + kRing * W::kBytes + wave * 16 * kOutRow * 4);
+  // A tile's results wait in the wave's part of LDS as bf16 and are stored during the
+  // next tile's steps. Every wave issues every store, those of rows or columns past the
+  // end (and all of the first tile's) with an offset past the resource's size.
+  uint8_t* const out = smem + kRing * W::kBytes + wave * 64 * kOutRow;
+  const uint8_t* const out_read = out + q * kOutRow + 16 * c;
+  const int row_bytes = 2 * a.N;
+  const rsrc_t ry = make_rsrc(static_cast<const char*>(a.y) + (int64_t)m0 * row_bytes,
+                              (uint32_t)(min(kShortRows, a.M - m0) * row_bytes));   // at most 32 MB
+  constexpr int kOutside = 1 << 30;
+  int at = kOutside;   // this lane's offset in ry of the first store
+  auto store = [&](int u, const v4i v) { buf_store16(ry, v, at + 4 * u * row_bytes); };
   int buf = 0;   // stage of step g
   for (int t = t0; t < t1; ++t) {
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
+      constexpr int kMost = (kStores + KS - 1) / KS;
+      const int u0 = kStores * s / KS, u1 = kStores * (s + 1) / KS;
       const uint8_t* stage = smem + buf * W::kBytes;
       const int nbuf = buf + 1 == kRing ? 0 : buf + 1;
       const uint8_t* next = smem + nbuf * W::kBytes;
+      v4i done[kMost];
 #pragma unroll
       for (int i = 0; i < FW; ++i) {
         w1[i] = rw.template read<1>(stage, i);
+        if (i < u1 - u0) done[i] = *reinterpret_cast<const v4i*>(out_read + 4 * (u0 + i) * kOutRow);
 #pragma unroll
         for (int j = 0; j < FT; ++j) mma_x_agpr(acc[i][j], w0[i], x[j][s][0]);
         __builtin_amdgcn_sched_barrier(0);
       }
-      wait_vmcnt<(kRing - 2) * kCopies>();
+      wait_vmcnt<(kRing - 2) * (kCopies + kLeastStores)>();
       __syncthreads();
       __builtin_amdgcn_sched_barrier(0);
       const v4i_s r = next_rsrc();
@@ -130,6 +149,7 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
       for (int i = 0; i < FW; ++i) {
         w0[i] = rw.template read<0>(next, i);
         if (i % 2 == 0 && i / 2 < kCopies) ow.copy(r, smem + cbuf * W::kBytes, wave, i / 2);
+        if (i < u1 - u0) store(u0 + i, done[i]);
 #pragma unroll
         for (int j = 0; j < FT; ++j) mma_x_agpr(acc[i][j], w1[i], x[j][s][1]);
         __builtin_amdgcn_sched_barrier(0);
@@ -143,26 +163,22 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
     asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
 #endif
     __builtin_amdgcn_sched_barrier(0);
-    // results, 16 rows at a time through the wave's own LDS rows, 8 columns per lane
+    wave_sync();   // the tile before has been read
 #pragma unroll
-    for (int j = 0; j < FT; ++j) {
+    for (int j = 0; j < FT; ++j)
 #pragma unroll
-      for (int i = 0; i < FW; ++i) *reinterpret_cast<v4f*>(out + c * kOutRow + 16 * i + 4 * q) = acc[i][j];
-      wave_sync();
-      const int64_t mw = m0 + 64 * wave + 16 * j + q;
-      const int n = t * kShortCols + 8 * c;
-      const float* src = out + q * kOutRow + 8 * c;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        finish_affine<false>(a, mw + 4 * u, n, *reinterpret_cast<const v4f*>(src + 4 * u * kOutRow),
-                      *reinterpret_cast<const v4f*>(src + 4 * u * kOutRow + 4), Residual8<false, F32>{});
-      wave_sync();
-    }
-#pragma unroll
-    for (int i = 0; i < FW; ++i)
-#pragma unroll
-      for (int j = 0; j < FT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < FW; ++i) {
+        const v4f v = acc[i][j];
+        *reinterpret_cast<uint2*>(out + (16 * j + c) * kOutRow + 2 * (16 * i + 4 * q)) =
+            make_uint2(bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]));
+        acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      }
+    wave_sync();
+    const int n = t * kShortCols + 8 * c;
+    at = n < a.N ? (64 * wave + q) * row_bytes + 2 * n : kOutside;
   }
+#pragma unroll
+  for (int u = 0; u < kStores; ++u) store(u, *reinterpret_cast<const v4i*>(out_read + 4 * u * kOutRow));
   wait_vmcnt<0>();   // no copy may be in flight when the workgroup's LDS is given away
 }
 
@@ -173,9 +189,8 @@ void run(const LinearArgs& a, bool w_trans, hipStream_t s) {
   const int total = m_tiles * (int)ceil_div(n_tiles, per);
   const dim3 grid((unsigned)(ceil_div(total, kXcds) * kXcds)), block(kShortThreads);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a, m_tiles, n_tiles, per, total); };
-  if (w_trans) go(k_linear_short<KS, true, false>);   // an input's gradient, always bf16
-  else if (a.out_f32) go(k_linear_short<KS, false, true>);
-  else go(k_linear_short<KS, false, false>);
+  if (w_trans) go(k_linear_short<KS, true>);
+  else go(k_linear_short<KS, false>);
 }
 
 }  // namespace
