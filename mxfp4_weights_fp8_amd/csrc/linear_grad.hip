@@ -8,6 +8,8 @@
 // padded by zeros to a multiple of 128.
 #include "linear.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -17,32 +19,69 @@ struct DzArgs {
   uint16_t* dz;       // [M, Np], columns N .. Np - 1 zero
   float* db_parts;    // [ceil(M / 64), N]
   int M, N, Np, act;
-  bool dy_f32;
 };
 
-// dz of 64 rows x 64 columns, and its column sums (16 rows per wave, then the waves).
+// dz of 64 rows x 64 columns, and its column sums: a thread holds four columns of every
+// 16th row. Without activation every load is on its way at once (VEC: N a multiple of 4,
+// loads of four); with one, rows follow each other, as four slopes fill the registers.
+template <bool VEC, bool DY_F32, bool ACT>
 __global__ __launch_bounds__(256) void k_linear_dz(DzArgs a) {
-  __shared__ float sums[4][64];
-  const int m0 = blockIdx.x * 64;
-  const int c = threadIdx.x & 63, wave = threadIdx.x >> 6, n = blockIdx.y * 64 + c;
-  float sum = 0.f;
-  for (int r = wave; r < 64; r += 4) {
-    const int m = m0 + r;
-    if (m >= a.M) break;
-    float v = 0.f;
-    if (n < a.N) {
-      const int64_t at = (int64_t)m * a.N + n;
-      v = a.dy_f32 ? reinterpret_cast<const float*>(a.dy)[at]
-                   : bf16_to_float(reinterpret_cast<const uint16_t*>(a.dy)[at]);
-      if (a.act != MOE_ACT_NONE) v *= activate_slope(a.z[at], a.act);
+  __shared__ v4f sums[16][16];
+  const int group = threadIdx.x & 15, sub = threadIdx.x >> 4;
+  const int n = blockIdx.y * 64 + 4 * group;
+  const int64_t m0 = (int64_t)blockIdx.x * 64 + sub;
+  // columns past N are zeros
+  auto load = [&](const void* p, bool f32, int64_t m) {
+    v4f v{0.f, 0.f, 0.f, 0.f};
+    const int64_t at = m * a.N + n;
+    if constexpr (VEC) {
+      if (n >= a.N) return v;
+      if (f32) return *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(p) + at);
+      const uint2 r = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + at);
+      return v4f{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
+                 __uint_as_float(r.y & 0xFFFF0000u)};
     }
-    sum += v;
-    a.dz[(int64_t)m * a.Np + n] = (uint16_t)bf16_pack2(v, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.N)
+        v[i] = f32 ? reinterpret_cast<const float*>(p)[at + i] : bf16_to_float(reinterpret_cast<const uint16_t*>(p)[at + i]);
+    return v;
+  };
+  auto store = [&](int64_t m, const v4f v) {
+    *reinterpret_cast<uint2*>(a.dz + m * a.Np + n) = make_uint2(bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]));
+  };
+  v4f sum{0.f, 0.f, 0.f, 0.f};
+  if constexpr (ACT) {
+#pragma unroll 1
+    for (int64_t m = m0; m < m0 + 64 && m < a.M; m += 16) {
+      v4f dz = load(a.dy, DY_F32, m);
+      const v4f z = load(a.z, true, m);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (VEC || n + i < a.N) dz[i] *= activate_slope(z[i], a.act);
+      sum += dz;
+      store(m, dz);
+    }
+  } else {
+    constexpr int kTurns = 4;
+    v4f dz[kTurns];
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) dz[u] = load(a.dy, DY_F32, min(m0 + 16 * u, (int64_t)a.M - 1));
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u)
+      if (m0 + 16 * u < a.M) {
+        sum += dz[u];
+        store(m0 + 16 * u, dz[u]);
+      }
   }
-  sums[wave][c] = sum;
+  sums[sub][group] = sum;
   __syncthreads();
-  if (wave == 0 && n < a.N)
-    a.db_parts[(int64_t)blockIdx.x * a.N + n] = sums[0][c] + sums[1][c] + sums[2][c] + sums[3][c];
+  const int c = threadIdx.x;
+  if (c < 64 && blockIdx.y * 64 + c < a.N) {
+    float s = sums[0][c >> 2][c & 3];
+    for (int k = 1; k < 16; ++k) s += sums[k][c >> 2][c & 3];
+    a.db_parts[(int64_t)blockIdx.x * a.N + blockIdx.y * 64 + c] = s;
+  }
 }
 
 inline int pad128(int v) { return (v + 127) / 128 * 128; }
@@ -86,8 +125,18 @@ hipError_t launch_linear_grad(const moe_linear_dims& d, const void* dy, const ui
   GradWs g;
   grad_ws_layout(d.M, d.N, d.K, ws, &g);
   const int Np = pad128(d.N), m_blocks = (int)ceil_div(d.M, 64);
-  const DzArgs da{dy, z, g.dz, g.db_parts, d.M, d.N, Np, d.act, d.type == MOE_TYPE_F32};
-  hipLaunchKernelGGL(k_linear_dz, dim3(m_blocks, Np / 64), dim3(256), 0, s, da);
+  const DzArgs da{dy, z, g.dz, g.db_parts, d.M, d.N, Np, d.act};
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(m_blocks, Np / 64), dim3(256), 0, s, da); };
+  auto by_act = [&](auto vec, auto f32) {
+    if (d.act == MOE_ACT_NONE) go(k_linear_dz<decltype(vec)::value, decltype(f32)::value, false>);
+    else go(k_linear_dz<decltype(vec)::value, decltype(f32)::value, true>);
+  };
+  auto by_type = [&](auto vec) {
+    if (d.type == MOE_TYPE_F32) by_act(vec, std::true_type{});
+    else by_act(vec, std::false_type{});
+  };
+  if (d.N % 4 == 0) by_type(std::true_type{});
+  else by_type(std::false_type{});
   hipError_t err = hipGetLastError();
   if (err == hipSuccess && db) err = launch_sum_parts(g.db_parts, m_blocks, d.N, db, s);
   if (err == hipSuccess && dx) {   // [M, K] = dz [M, Np] . w [N, K], contracted over N

@@ -501,6 +501,8 @@ def test_balance_loss_masks_and_empty(dev, score):
     check_balance(dev, l, ids, 1.0, score, [0, 0, 0, 100, 100, 200, 200], "empty sequences")
     check_balance(dev, l, ids, 1.0, score, [50, 50], "no token in any")
     check_balance(dev, l, ids, 1.0, score, list(range(201)), "one token each")
+    check_balance(dev, l, ids, 1.0, score, list(range(0, 201, 2)), "two tokens each")
+    check_balance(dev, l, ids, 1.0, score, [7] * 150 + list(range(7, 180)), "more than 256 sequences")
     check_balance(dev, l, torch.full_like(ids, -1), 1.0, score, None, "every pick dropped")
 
 
