@@ -7,7 +7,9 @@
 // With a_be = alpha f_be / (B n_b) the loss is sum_t sum_e a_be p_te, so each token
 // adds its own dot product d_t = sum_e a_be p_te, the same sum its gradient needs:
 //   softmax: dl = p (a - d);   else dl = (a - d) s'(l) / sum s.
-// One pass over the logits, after the counts.
+// One pass over the logits, after the counts. 32768 x 384 top-8 in 17 sequences (102
+// MB): 29 us, of which the pass 20-21 (5 TB/s), the counts 5-7, the sum of the parts 4 (1024
+// numbers, latency) and clearing the counts 2.
 #include "router.h"
 
 namespace moe {

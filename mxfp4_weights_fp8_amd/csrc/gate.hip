@@ -17,6 +17,9 @@
 // lane's groups, a DPP reduction over the row's lanes, the lowest index that holds
 // it (group by group, then in the one group read back), and one group rewritten:
 // about 50 instructions instead of the 120 of scanning 24 keys in registers.
+//
+// 32768 x 384 top-8 with bias (52 MB): 25-27 us, bound by the vector units (scores of 24
+// experts per lane, then eight rounds); 7 x 384 5.2-5.9 us, latency.
 #include "router.h"
 
 namespace moe {

@@ -3,6 +3,7 @@
 // dc_j = scale (dw_j - sum_i dw_i s_i / S) / S with S = sum of the picked scores
 // + 1e-20 (renorm), or scale dw_j; ds = the dc of the picks, summed over equal ids;
 //   softmax: dl = p (ds - sum p ds);  else dl = ds s'(l).
+// 32768 x 384 top-8, softmax, with an added gradient (151 MB): 27-29 us, 5.4 TB/s.
 #include "router.h"
 
 namespace moe {
@@ -19,9 +20,9 @@ struct GateGradArgs {
   float scale;
 };
 
-// The picks' gradients are spread over the row through
-// LDS, one pick after another (so that equal ids add up in a fixed order): about 60
-// instructions, where comparing 24 experts per lane with 8 picks took 480.
+// The picks' gradients are spread over the row through LDS, one pick after another (so
+// that equal ids add up in a fixed order): about 60 instructions, where comparing 24
+// experts per lane with 8 picks took 480.
 template <int LPR, int NV, int SCORE, bool BF16, bool VEC>
 __global__ __launch_bounds__(kGateThreads) void k_gate_grad(GateGradArgs a) {
   __shared__ v4f spread[NV][kGateThreads];   // [j][row, lane]: experts 4 (j LPR + lane) ..  of a row

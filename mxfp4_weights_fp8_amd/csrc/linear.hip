@@ -24,7 +24,8 @@ __device__ __forceinline__ v4f mfma_bf16(const v4i a, const v4i b, v4f c) {
 // of a wave is in flight at once. A lane multiplies 8 of a 512-long chunk of K (wave w
 // takes chunks w, w + waves, ...) in fp32: R weights' and MT rows' 16 bytes give R MT
 // sums, added over the lanes, then over the waves in order.
-// 7 x 384 x 7168: 24 workgroups of 16 columns on the matrix cores took 12.3 us.
+// 7 x 384 x 7168: 6.0 us (0.9 TB/s, latency), 24 workgroups of 16 columns on the matrix
+// cores 12.3 us.
 constexpr int kDotWaves = 16;
 
 __device__ __forceinline__ void unpack8(const v4i raw, float (&v)[8]) {
@@ -79,6 +80,7 @@ __global__ __launch_bounds__(64 * kDotWaves) void k_linear_dot(LinearArgs a) {
 // At most 64 rows: bound by reading the weights. A workgroup owns 16 output columns and
 // one of a.splits shares of the contraction; its waves take every W-th step of 64 K,
 // straight from memory into registers, and add their sums through LDS in wave order.
+// 9 x 7168 x 7168 27 us, 3.8 TB/s; 64 x 384 x 7168 12.3 us per call, bound by the host.
 constexpr int kSmallWaves = 16;
 
 template <int FT>

@@ -5,7 +5,8 @@
 //
 // Both products contract over the rows of an operand; the tiled kernel reads such
 // operands transposed, as they lie. dz [M, N] goes to the workspace with its rows
-// padded by zeros to a multiple of 128.
+// padded by zeros to a multiple of 128. 16384 x 384 x 7168 (the router's): dz 8.7 us, 4.3
+// TB/s, dbias 5 us, dx 109-112 us, dw 107-112 us and 8 us for joining its three parts.
 #include "linear.h"
 
 #include <type_traits>
@@ -23,7 +24,8 @@ struct DzArgs {
 
 // dz of 64 rows x 64 columns, and its column sums: a thread holds four columns of every
 // 16th row. Without activation every load is on its way at once (VEC: N a multiple of 4,
-// loads of four); with one, rows follow each other, as four slopes fill the registers.
+// loads of four; one column per thread took 14.3 us of 16384 x 384); with one, rows follow
+// each other, as four slopes fill the registers.
 template <bool VEC, bool DY_F32, bool ACT>
 __global__ __launch_bounds__(256) void k_linear_dz(DzArgs a) {
   __shared__ v4f sums[16][16];

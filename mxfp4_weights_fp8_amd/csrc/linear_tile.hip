@@ -20,6 +20,11 @@
 // bytes of a row: with stages of 32 (64-byte pieces) the copies' issue took most of the
 // loop (32768 x 384 x 7168: 208 us).
 //
+// 32768 x 384 x 7168 to fp32 in 256 x 192 tiles 160 us, 1.13 PFLOP/s (one round of 256
+// workgroups); 8191 x 7168 x 2048 with residual in 128 x 128 tiles 265 us, 0.91 PFLOP/s;
+// 8192^3 851 us, 1.29 PFLOP/s. The library's product takes 187, 209 and 785 us. Without
+// its copies 8192^3 takes 720 us, its MFMAs alone 652 us: bound by the issue of the copies
+// and, where the contraction is short, by epilogues that all CUs reach together.
 #include "linear.h"
 #include "linear_stage.h"
 

@@ -8,7 +8,8 @@
 //
 // HBM-bound: a row is read once and kept in registers between the sum of squares
 // and the outputs. A lane's vector is 8 columns, so 16 lanes hold one 128-column
-// block and its amax is a 16-lane butterfly.
+// block and its amax is a 16-lane butterfly. 32768 x 7168 with residual and all outputs
+// (2.1 GB) 350-380 us, 5.6-6.0 TB/s; 7 x 7168 5 us, bound by the launch.
 #include "device_common.h"
 #include "host_internal.h"
 #include "lane_reduce.h"
@@ -184,6 +185,7 @@ void launch_fwd(const NormArgs& a, hipStream_t s) {
 // walk every gridDim * kRows-th row, the next row's values on their way while a row is
 // reduced, and keep their part of dw in registers; the parts of a workgroup are added
 // through LDS, go to the workspace as [gridDim, H], and k_sum_parts adds them in order.
+// 4099 x 7168 (235 MB) 51-53 us, 4.5 TB/s, and 5 us for the parts.
 struct NormGradArgs {
   const uint16_t* dy;
   const uint16_t* h;

@@ -31,6 +31,8 @@ Modules:
   brute    -- an independent per-token, per-expert loop version with its own
               codecs (fractions / brute-force nearest search, math.fsum), used only
               to pin ``moe`` on tiny inputs.
+  block    -- the operators in front of the FFN (residual add + norm, dense product,
+              gate, balance loss) and their gradients, in float64.
   compare  -- the parity metrics and the SwiGLU-code comparison rule.
 
 Parity status of each function is stated in its docstring; every function here
