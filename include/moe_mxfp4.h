@@ -423,7 +423,7 @@ int moe_gate_grad(const moe_gate_dims* dims, const void* logits, const int32_t* 
  *                results are unspecified, but nothing outside the buffers is touched.)
  *   loss [1] fp32 out, counts [B, E] int32 out
  *   d_logits [T, E] fp32 out: the gradient of the loss; rows in no sequence are zero
- *   ws  at least moe_balance_loss_workspace_bytes bytes
+ *   ws  at least moe_balance_loss_workspace_bytes bytes (0 for small batches: ws may be NULL)
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED (B * E of 2^31 or more), MOE_EWORKSPACE, MOE_EHIP. */
 size_t moe_balance_loss_workspace_bytes(const moe_gate_dims* dims, int32_t B);
 int moe_balance_loss(const moe_gate_dims* dims, int32_t B, float alpha, const void* logits, const int32_t* topk_ids,

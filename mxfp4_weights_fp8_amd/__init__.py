@@ -447,6 +447,15 @@ def _tensor(t, dtype, shape, dev, name):
     return t.data_ptr()
 
 
+def _new(rows, cols, dtype, dev):
+    """An uninitialised [rows, cols] tensor (empty_strided takes 1.3 us, empty 2.2 us)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=dev)
+
+
+def _vector(n, dtype, dev):
+    return torch.empty_strided((n,), (1,), dtype=dtype, device=dev)
+
+
 def _first(t, dims, name):
     """Checks that the argument that sets sizes and device is a cuda tensor of `dims` dimensions."""
     if t.dim() != dims or not t.is_cuda:
@@ -462,7 +471,7 @@ def _one_of(table, key, name):
 
 def _workspace(nbytes, dev, ws):
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        return _vector(nbytes, torch.uint8, dev) if nbytes else None
     if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"ws: expected contiguous uint8 on {dev}, got {ws.dtype} on {ws.device}")
     return ws
@@ -509,11 +518,15 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
         q = s = None
     else:
         if q is None:
-            q = torch.empty(shape, dtype=torch.uint8, device=dev)
+            q = _new(T, H, torch.uint8, dev)
+            qp = q.data_ptr()
+        else:
+            qp = _tensor(q, torch.uint8, shape, dev, "out.x_q")
         if s is None:
-            s = torch.empty((T, H // 128), dtype=torch.uint8, device=dev)
-        qp = _tensor(q, torch.uint8, shape, dev, "out.x_q")
-        sp = _tensor(s, torch.uint8, (T, H // 128), dev, "out.x_s")
+            s = _new(T, H // 128, torch.uint8, dev)
+            sp = s.data_ptr()
+        else:
+            sp = _tensor(s, torch.uint8, (T, H // 128), dev, "out.x_s")
     _enqueue("moe_add_norm", dev, T, H, eps, xp, rp, wp, wt, hp, yp, qp, sp)
     return Normed(h, y, q, s)
 
@@ -531,7 +544,7 @@ def add_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: 
     wt = _one_of(TYPES, weight.dtype, "weight type")
     if dx is None:
         dx = torch.empty_like(h)
-    dw = torch.empty(H, dtype=torch.float32, device=dev)
+    dw = _vector(H, torch.float32, dev)
     ws = _workspace(lib().moe_add_norm_grad_workspace_bytes(T, H), dev, ws)
     _enqueue("moe_add_norm_grad", dev, T, H, eps, _tensor(dy, torch.bfloat16, shape, dev, "dy"),
              _tensor(h, torch.bfloat16, shape, dev, "h"), _tensor(weight, weight.dtype, (H,), dev, "weight"), wt,
@@ -559,7 +572,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     N = w.shape[0]
     d = LinearDims(M, N, K, _one_of(ACTS, act, "act"), _one_of(TYPES, dtype, "dtype"))
     if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=dev)
+        y = _new(M, N, dtype, dev)
     ws = _workspace(lib().moe_linear_workspace_bytes(d), dev, ws)
     _enqueue("moe_linear", dev, d, _tensor(x, torch.bfloat16, (M, K), dev, "x"),
              _tensor(w, torch.bfloat16, (N, K), dev, "w"), _tensor(bias, torch.float32, (N,), dev, "bias"),
@@ -581,7 +594,7 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str = "
     d = LinearDims(M, N, K, _one_of(ACTS, act, "act"), _one_of(TYPES, dy.dtype, "dy type"))
     dx = torch.empty_like(x) if need[0] else None
     dw = torch.empty_like(w) if need[1] else None
-    db = torch.empty(N, dtype=torch.float32, device=dev) if need[2] else None
+    db = _vector(N, torch.float32, dev) if need[2] else None
     ws = _workspace(lib().moe_linear_grad_workspace_bytes(d), dev, ws)
     _enqueue("moe_linear_grad", dev, d, _tensor(dy, dy.dtype, (M, N), dev, "dy"),
              _tensor(x, torch.bfloat16, (M, K), dev, "x"), _tensor(w, torch.bfloat16, (N, K), dev, "w"),
@@ -609,9 +622,9 @@ def gate(logits: torch.Tensor, K: int, score: str = "softmax", bias: Optional[to
     d = _gate_dims(logits, K, score, renorm, scale)
     shape = (T, K)
     if topk_ids is None:
-        topk_ids = torch.empty(shape, dtype=torch.int32, device=dev)
+        topk_ids = _new(T, K, torch.int32, dev)
     if topk_weights is None:
-        topk_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+        topk_weights = _new(T, K, torch.float32, dev)
     _enqueue("moe_gate", dev, d, _tensor(logits, logits.dtype, (T, E), dev, "logits"),
              _tensor(bias, torch.float32, (E,), dev, "bias"), _tensor(n_valid, torch.int32, (1,), dev, "n_valid"),
              _tensor(topk_ids, torch.int32, shape, dev, "topk_ids"),
@@ -632,7 +645,7 @@ def gate_grad(logits: torch.Tensor, topk_ids: torch.Tensor, d_weights: torch.Ten
     K = topk_ids.shape[1]
     d = _gate_dims(logits, K, score, renorm, scale)
     if d_logits is None:
-        d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        d_logits = _new(T, E, torch.float32, dev)
     _enqueue("moe_gate_grad", dev, d, _tensor(logits, logits.dtype, (T, E), dev, "logits"),
              _tensor(topk_ids, torch.int32, (T, K), dev, "topk_ids"),
              _tensor(d_weights, torch.float32, (T, K), dev, "d_weights"),
@@ -656,9 +669,9 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, alpha: float, sco
         _first(seq_offsets, 1, "seq_offsets")
     B = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
     d = _gate_dims(logits, K, score, False, 1.0)
-    loss = torch.empty(1, dtype=torch.float32, device=dev)
-    counts = torch.empty((max(B, 0), E), dtype=torch.int32, device=dev)
-    d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+    loss = _vector(1, torch.float32, dev)
+    counts = _new(max(B, 0), E, torch.int32, dev)
+    d_logits = _new(T, E, torch.float32, dev)
     ws = _workspace(lib().moe_balance_loss_workspace_bytes(d, B), dev, ws)
     _enqueue("moe_balance_loss", dev, d, B, alpha, _tensor(logits, logits.dtype, (T, E), dev, "logits"),
              _tensor(topk_ids, torch.int32, (T, K), dev, "topk_ids"),

@@ -268,16 +268,18 @@ __global__ __launch_bounds__(kOneThreads) void k_balance_one(BalanceArgs a) {
 }
 
 // One workgroup where it needs at most 8 rounds of 64 tokens and 4 sequences (256 x 64
-// top-6: 6 us, 13 us per call, bound by the host; the four launches below 22 us per call).
+// top-6: 6 us, 11 us per call, bound by the host; the four launches below 22 us per call).
 inline bool one_workgroup(const moe_gate_dims& d, int B) { return d.T <= 512 && d.E <= 512 && B <= 4; }
 
 }  // namespace
 
-int balance_parts(const moe_gate_dims& d) { return (int)ceil_div(d.T, kBalanceRows); }
+int balance_parts(const moe_gate_dims& d, int B) {
+  return one_workgroup(d, B) ? 0 : (int)ceil_div(d.T, kBalanceRows);
+}
 
 hipError_t launch_balance(const moe_gate_dims& d, int B, float alpha, const void* logits, const int32_t* ids,
                           const int32_t* off, float* loss, int32_t* counts, float* dl, double* parts, hipStream_t s) {
-  const int n = balance_parts(d);
+  const int n = balance_parts(d, B);
   const BalanceArgs a{logits, ids, off, counts, dl, parts, loss, d.T, d.E, d.K, B, alpha};
   const bool bf = d.logits_type == MOE_TYPE_BF16, vec = d.E % 4 == 0;
   if (one_workgroup(d, B)) {

@@ -125,7 +125,7 @@ int moe_gate_grad(const moe_gate_dims* dims, const void* logits, const int32_t* 
 
 size_t moe_balance_loss_workspace_bytes(const moe_gate_dims* dims, int32_t B) {
   if (check_gate(dims) != MOE_OK || B < 1) return 0;
-  return sizeof(double) * (size_t)balance_parts(*dims);
+  return sizeof(double) * (size_t)balance_parts(*dims, B);
 }
 
 int moe_balance_loss(const moe_gate_dims* dims, int32_t B, float alpha, const void* logits, const int32_t* topk_ids,
@@ -135,9 +135,10 @@ int moe_balance_loss(const moe_gate_dims* dims, int32_t B, float alpha, const vo
   if (rc != MOE_OK) return rc;
   if (B < 1 || !finite(alpha) || (!seq_offsets && B != 1)) return MOE_EINVAL;
   if ((int64_t)B * dims->E >= (int64_t)1 << 31) return MOE_EUNSUPPORTED;
-  if (!loss || !counts || (dims->T > 0 && (!logits || !topk_ids || !d_logits || !ws))) return MOE_EINVAL;
+  const size_t need = sizeof(double) * (size_t)balance_parts(*dims, B);
+  if (!loss || !counts || (dims->T > 0 && (!logits || !topk_ids || !d_logits)) || (need && !ws)) return MOE_EINVAL;
   if (!all_aligned(logits, topk_ids, seq_offsets, loss, counts, d_logits, ws)) return MOE_EINVAL;
-  if (ws_bytes < moe_balance_loss_workspace_bytes(dims, B)) return MOE_EWORKSPACE;
+  if (ws_bytes < need) return MOE_EWORKSPACE;
   return hip_status(launch_balance(*dims, B, alpha, logits, topk_ids, seq_offsets, loss, counts, d_logits,
                                    static_cast<double*>(ws), (hipStream_t)stream));
 }

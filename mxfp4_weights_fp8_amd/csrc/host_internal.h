@@ -236,7 +236,7 @@ hipError_t launch_gate(const moe_gate_dims& d, const void* logits, const float* 
                        int32_t* ids, float* w, hipStream_t s);
 hipError_t launch_gate_grad(const moe_gate_dims& d, const void* logits, const int32_t* ids, const float* dw,
                             const float* add, float* dl, hipStream_t s);
-int balance_parts(const moe_gate_dims& d);   // doubles of its workspace
+int balance_parts(const moe_gate_dims& d, int B);   // doubles of its workspace
 hipError_t launch_balance(const moe_gate_dims& d, int B, float alpha, const void* logits, const int32_t* ids,
                           const int32_t* off, float* loss, int32_t* counts, float* dl, double* parts, hipStream_t s);
 

@@ -74,7 +74,7 @@ EI, EU, EW = moe.MOE_EINVAL, moe.MOE_EUNSUPPORTED, moe.MOE_EWORKSPACE
     (balance, dict(B=0), EI), (balance, dict(alpha=NAN), EI), (balance, dict(B=2, off=None), EI),
     (balance, dict(B=1 << 30), EU), (balance, dict(l=None), EI), (balance, dict(ids=None), EI),
     (balance, dict(loss=None), EI), (balance, dict(c=None), EI), (balance, dict(dl=None), EI),
-    (balance, dict(ws=None), EI), (balance, dict(n=0), EW), (balance, dict(off=ODD), EI), (balance, dict(K=9), EI),
+    (balance, dict(T=513, ws=None), EI), (balance, dict(T=513, n=0), EW), (balance, dict(B=5, n=0), EW), (balance, dict(off=ODD), EI), (balance, dict(K=9), EI),
 ])
 def test_calls_are_refused_on_the_host(call, kw, code):
     assert call(**kw) == code
