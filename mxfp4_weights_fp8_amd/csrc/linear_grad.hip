@@ -127,7 +127,8 @@ hipError_t launch_linear_grad(const moe_linear_dims& d, const void* dy, const ui
   GradWs g;
   grad_ws_layout(d.M, d.N, d.K, ws, &g);
   const int Np = pad128(d.N), m_blocks = (int)ceil_div(d.M, 64);
-  const DzArgs da{dy, z, g.dz, g.db_parts, d.M, d.N, Np, d.act};
+  const bool one = m_blocks == 1 && db;   // the only part is the result: one launch less
+  const DzArgs da{dy, z, g.dz, one ? db : g.db_parts, d.M, d.N, Np, d.act};
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(m_blocks, Np / 64), dim3(256), 0, s, da); };
   auto by_act = [&](auto vec, auto f32) {
     if (d.act == MOE_ACT_NONE) go(k_linear_dz<decltype(vec)::value, decltype(f32)::value, false>);
@@ -140,7 +141,7 @@ hipError_t launch_linear_grad(const moe_linear_dims& d, const void* dy, const ui
   if (d.N % 4 == 0) by_type(std::true_type{});
   else by_type(std::false_type{});
   hipError_t err = hipGetLastError();
-  if (err == hipSuccess && db) err = launch_sum_parts(g.db_parts, m_blocks, d.N, db, s);
+  if (err == hipSuccess && db && !one) err = launch_sum_parts(g.db_parts, m_blocks, d.N, db, s);
   if (err == hipSuccess && dx) {   // [M, K] = dz [M, Np] . w [N, K], contracted over N
     const LinearArgs a{g.dz, w, Np, d.K, nullptr, nullptr, dx, nullptr, g.parts, d.M, d.K, Np, d.N,
                        MOE_ACT_NONE, 1, false};

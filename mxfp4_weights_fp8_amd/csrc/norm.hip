@@ -375,10 +375,10 @@ hipError_t launch_add_norm_grad(const uint16_t* dy, const uint16_t* h, const voi
                                 uint16_t* dx, float* dw, float* parts, int T, int H, float eps, hipStream_t s) {
   const int n = norm_grad_parts(T, H);
   if (n > 0) {
-    const NormGradArgs a{dy, h, w, dh, dx, parts, T, H, eps};
+    const NormGradArgs a{dy, h, w, dh, dx, n == 1 ? dw : parts, T, H, eps};   // one part is the result
     by_kind(w_f32, past_cache(T, H), [&](auto f, auto nt) { launch_grad<decltype(f)::value, decltype(nt)::value>(a, n, s); });
   }
-  return launch_sum_parts(parts, n, H, dw, s);
+  return n == 1 ? hipGetLastError() : launch_sum_parts(parts, n, H, dw, s);
 }
 
 hipError_t launch_fill_zero(int32_t* p, int64_t n, hipStream_t s) {
