@@ -358,8 +358,9 @@ int moe_linear(const moe_linear_dims* dims, const uint16_t* x, const uint16_t* w
                const void* residual, void* y, float* z, void* ws, size_t ws_bytes, void* stream);
 
 /* Gradient of moe_linear: dz = dy * act'(z); dx = dz w, dw = dz^T x, dbias = sum over
- * rows of dz (the residual's gradient is dy). The products take dz rounded to bf16,
- * dbias sums it in fp32.
+ * rows of dz (the residual's gradient is dy). The products take dz to within 2^-15 of it
+ * (as two bf16 values; one, exact, where dy is bf16 and act none or relu, which halves
+ * their work), dbias sums it in fp32.
  *   dy [M, N] of `type`, x and w as in moe_linear, z [M, N] fp32 from moe_linear
  *   (not read with MOE_ACT_NONE)
  *   dx [M, K] bf16 out, dw [N, K] bf16 out, dbias [N] fp32 out; any may be NULL

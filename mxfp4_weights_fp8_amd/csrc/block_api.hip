@@ -89,7 +89,7 @@ int moe_linear(const moe_linear_dims* dims, const uint16_t* x, const uint16_t* w
 
 size_t moe_linear_grad_workspace_bytes(const moe_linear_dims* dims) {
   if (check_linear(dims) != MOE_OK || dims->M == 0) return 0;
-  return linear_grad_ws_bytes(dims->M, dims->N, dims->K);
+  return linear_grad_ws_bytes(*dims);
 }
 
 int moe_linear_grad(const moe_linear_dims* dims, const void* dy, const uint16_t* x, const uint16_t* w, const float* z,
@@ -99,7 +99,7 @@ int moe_linear_grad(const moe_linear_dims* dims, const void* dy, const uint16_t*
   if (!all_aligned(dy, x, w, z, dx, dw, dbias, ws)) return MOE_EINVAL;
   if (dims->M > 0) {
     if (!dy || (dw && !x) || (dx && !w) || (dims->act != MOE_ACT_NONE && !z) || !ws) return MOE_EINVAL;
-    if (ws_bytes < linear_grad_ws_bytes(dims->M, dims->N, dims->K)) return MOE_EWORKSPACE;
+    if (ws_bytes < linear_grad_ws_bytes(*dims)) return MOE_EWORKSPACE;
   }
   return hip_status(launch_linear_grad(*dims, dy, x, w, z, dx, dw, dbias, ws, (hipStream_t)stream));
 }

@@ -228,7 +228,7 @@ hipError_t launch_fill_zero(int32_t* p, int64_t n, hipStream_t s);   // n >= 1
 size_t linear_parts_bytes(int M, int N, int K);
 hipError_t launch_linear(const moe_linear_dims& d, const uint16_t* x, const uint16_t* w, const float* bias,
                          const void* res, void* y, float* z, float* parts, hipStream_t s);
-size_t linear_grad_ws_bytes(int M, int N, int K);
+size_t linear_grad_ws_bytes(const moe_linear_dims& d);
 hipError_t launch_linear_grad(const moe_linear_dims& d, const void* dy, const uint16_t* x, const uint16_t* w,
                               const float* z, uint16_t* dx, uint16_t* dw, float* db, void* ws, hipStream_t s);
 // The router's gate, its gradient and the balance loss.

@@ -12,11 +12,13 @@ namespace moe {
 // y[m, n] = act(sum_c X[m, c] W[n, c] + bias[n]) + residual[m, n]. An operand lies in
 // memory either as [rows, C] with the contraction along memory (C a multiple of 128),
 // or as [C, rows], which the tiled kernel reads transposed. Strides are in elements,
-// multiples of 8.
+// multiples of 8. X may be the sum of two bf16 values per element, its low parts x_low
+// elements behind the high ones: both products go into the same accumulators.
 struct LinearArgs {
   const uint16_t* x;
   const uint16_t* w;
   int64_t xs, ws;         // elements from one memory row of x (w) to the next
+  int x_low;              // 0: x is one bf16 value per element
   const float* bias;      // [N], optional
   const void* res;        // [M, N] of the output's type, optional; may be y
   void* y;                // [M, N] bf16 or fp32
@@ -38,11 +40,12 @@ struct LinearPlan {
   Path path;
   int ft, fw, splits;
 };
-// plain: a bf16 result without bias, residual, activation or z.
-LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain);
+// plain: a bf16 result without bias, residual, activation or z. two: x in two parts (the
+// gradients' layouts alone).
+LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain, bool two = false);
 size_t linear_plan_parts(int M, int N, const LinearPlan& p);   // bytes of `parts`
 hipError_t launch_linear_plan(const LinearArgs& a, const LinearPlan& p, Layout l, hipStream_t s);
-int short_tiles_per_cta(int M, int N);
+int short_tiles_per_cta(int M, int N, bool two);
 void launch_short(const LinearArgs& a, Layout l, hipStream_t s);
 void launch_tiles(const LinearArgs& a, const LinearPlan& p, Layout l, hipStream_t s);
 

@@ -165,7 +165,7 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a) {
 // parts of a split product 4 us and its traffic at 4 TB/s. (8192^3: 256 x 256 tiles 851
 // us, 128 x 128 971; 8191 x 7168 x 2048: 310 and 266; 4096 x 2048 x 7168: 256 x 256 split
 // in two 112, 128 x 128 110, unsplit 256 x 256 168.)
-LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain) {
+LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain, bool two) {
   // Few rows. The vector units up to 1536 columns: 7 x 384 x 7168 8.2 us against 10.2 us
   // by kSmall, 8 x 1536 x 4096 8.5 against 10.1, but 8 x 2048 x 7168 14.9 against 10.7. Above
   // 16 rows kSmall while its workgroups' reads of x, M N K / 8 bytes, stay small: 64 x 4096 x
@@ -181,7 +181,7 @@ LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain) {
   static const struct {
     int ft, fw, per_cu, step, fixed;
   } kShapes[] = {{8, 8, 1, 170, 2200}, {8, 6, 1, 145, 1500}, {6, 8, 1, 145, 1500}, {4, 4, 2, 98, 800}};
-  const int64_t steps = ceil_div(C, 64);
+  const int64_t steps = ceil_div(C, 64) * (two ? 2 : 1);
   LinearPlan best{Path::kTiles, 0, 0, 1};
   int64_t least = -1;
   for (const auto& t : kShapes) {
@@ -200,6 +200,8 @@ LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain) {
   // result is large enough for a pipeline that starts once. In us, rows kept and tiles, at
   // 384: 16384 x 1024 25 and 21, 4096 x 7168 33 and 35, 8192 x 7168 52 and 63, 16384 x 7168
   // 92 and 126, 32768 x 2048 56 and 70; at 128: 4096 x 7168 20 and 25, 16384 x 7168 49 and 76.
+  // With x in two parts (and the kernel that makes them) at 384: 8192 x 2048 48 and 46, 4096 x
+  // 7168 64 and 66, 16384 x 7168 199 and 230; at 128: 8192 x 2048 28 and 27, 4096 x 7168 34 and 38.
   if (C <= 384 && N % 8 == 0 && plain && l != Layout::kBothTrans && (int64_t)M * N >= 20000000)   // C is a multiple of 128
     return LinearPlan{Path::kShort, 0, 0, 1};
   return best;
@@ -256,7 +258,7 @@ hipError_t launch_linear_plan(const LinearArgs& in, const LinearPlan& p, Layout 
 
 hipError_t launch_linear(const moe_linear_dims& d, const uint16_t* x, const uint16_t* w, const float* bias,
                          const void* res, void* y, float* z, float* parts, hipStream_t s) {
-  const LinearArgs a{x, w, d.K, d.K, bias, res, y, z, parts, d.M, d.N, d.K, d.K,
+  const LinearArgs a{x, w, d.K, d.K, 0, bias, res, y, z, parts, d.M, d.N, d.K, d.K,
                      d.act, 1, d.type == MOE_TYPE_F32};
   const bool plain = !bias && !res && !z && d.act == MOE_ACT_NONE && d.type == MOE_TYPE_BF16;
   return launch_linear_plan(a, linear_plan(d.M, d.N, d.K, Layout::kRows, plain), Layout::kRows, s);

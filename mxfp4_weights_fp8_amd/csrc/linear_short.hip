@@ -2,9 +2,9 @@
 // input, contracted over its experts): bound by writing the result, and with square
 // tiles by the copies into LDS.
 //
-// A workgroup keeps 256 rows of x in registers, 64 per wave and the whole contraction
-// (at C = 384 192 registers, in the AGPR file as the MFMAs' second operand), and walks
-// a run of 128-column tiles. Only w goes through LDS: a ring of kRing one-step stages
+// A workgroup keeps 256 rows of x in registers (128 of an x in two parts), 64 (32) per wave
+// and the whole contraction (at C = 384 192 registers, in the AGPR file as the MFMAs'
+// second operand), and walks a run of 128-column tiles. Only w goes through LDS: a ring of kRing one-step stages
 // (64 x 128) that runs on across the tiles, so that the next tile's columns arrive
 // during the epilogue. Per 256 x 128 outputs 96 KB are copied, against 4 x 192 KB for
 // the same outputs in 128 x 128 tiles.
@@ -26,7 +26,8 @@ namespace moe {
 namespace {
 
 constexpr int kShortThreads = 256;
-constexpr int kShortRows = 256, kShortCols = 128;
+constexpr int kShortCols = 128;
+constexpr int short_rows(bool two) { return two ? 128 : 256; }
 constexpr int kRing = 5;
 constexpr int kXcds = 8;
 
@@ -38,16 +39,18 @@ __device__ __forceinline__ void mma_x_agpr(v4f& acc, const v4i& w, const v4i& x)
 #endif
 }
 
-template <int KS, bool WT>
+// TWO: x in two parts; a fragment of w meets the high and the low part of half the rows.
+template <int KS, bool WT, bool TWO>
 __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a, int m_tiles, int n_tiles, int per_cta,
                                                                     int total) {
-  constexpr int FT = 4, FW = 8;
+  constexpr int P = TWO ? 2 : 1, FT = 4 / P, FW = 8;
+  constexpr int kShortRows = short_rows(TWO), kWaveRows = 16 * FT;
   typedef Operand<kShortCols, WT> W;
   constexpr int kCopies = W::kCopies;
   constexpr int kOutRow = 2 * kShortCols + 16;   // bytes per staged row: 16 rows in distinct banks
-  constexpr int kStores = 16;                    // of a wave per tile, 4 rows each
+  constexpr int kStores = kWaveRows / 4;         // of a wave per tile, 4 rows each
   constexpr int kLeastStores = kStores / KS;     // and step
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing * W::kBytes + 4 * 64 * kOutRow];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing * W::kBytes + 4 * kWaveRows * kOutRow];
 
   // (column run, row tile), each XCD a contiguous share: its L2 holds few column runs
   const int run = (total + kXcds - 1) / kXcds;
@@ -66,7 +69,7 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
   const int steps = (t1 - t0) * KS;
   int ct = t0, cs = 0, cbuf = 0, issued = 0;   // the copies' tile, step and stage
   ow.place(a.w, a.ws, ct * kShortCols, a.N, a.w_rows);
-  auto next_rsrc = [&]() { return ow.rsrc(cs, issued < steps ? KS : 0); };
+  auto next_rsrc = [&]() { return ow.rsrc(cs, issued < steps); };
   auto advance = [&]() {
     ++issued;
     cbuf = cbuf + 1 == kRing ? 0 : cbuf + 1;
@@ -85,21 +88,25 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
   }
   // x: lane (c, q) holds contraction 64 s + 32 h + 8q .. + 7 of rows 16 j + c; rows past
   // the end repeat the last one and are not stored
-  v4i x[FT][KS][2];
+  v4i x[FT][P][KS][2];
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
-    const uint16_t* row = a.x + (int64_t)min(m0 + 64 * wave + 16 * j + c, a.M - 1) * a.xs + 8 * q;
+    const uint16_t* row = a.x + (int64_t)min(m0 + kWaveRows * wave + 16 * j + c, a.M - 1) * a.xs + 8 * q;
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) x[j][s][h] = load16(row + 64 * s + 32 * h);
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[j][p][s][h] = load16(row + p * a.x_low + 64 * s + 32 * h);
   }
 #pragma unroll
   for (int j = 0; j < FT; ++j)
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) asm volatile("; in an AGPR from here" : "+a"(x[j][s][h]));
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) asm volatile("; in an AGPR from here" : "+a"(x[j][p][s][h]));
   wait_vmcnt<0>();
   __syncthreads();
 
@@ -115,7 +122,7 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
   // A tile's results wait in the wave's part of LDS as bf16 and are stored during the
   // next tile's steps. Every wave issues every store, those of rows or columns past the
   // end (and all of the first tile's) with an offset past the resource's size.
-  uint8_t* const out = smem + kRing * W::kBytes + wave * 64 * kOutRow;
+  uint8_t* const out = smem + kRing * W::kBytes + wave * kWaveRows * kOutRow;
   const uint8_t* const out_read = out + q * kOutRow + 16 * c;
   const int row_bytes = 2 * a.N;
   const rsrc_t ry = make_rsrc(static_cast<const char*>(a.y) + (int64_t)m0 * row_bytes,
@@ -138,7 +145,9 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
         w1[i] = rw.template read<1>(stage, i);
         if (i < u1 - u0) done[i] = *reinterpret_cast<const v4i*>(out_read + 4 * (u0 + i) * kOutRow);
 #pragma unroll
-        for (int j = 0; j < FT; ++j) mma_x_agpr(acc[i][j], w0[i], x[j][s][0]);
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int j = 0; j < FT; ++j) mma_x_agpr(acc[i][j], w0[i], x[j][p][s][0]);
         __builtin_amdgcn_sched_barrier(0);
       }
       wait_vmcnt<(kRing - 2) * (kCopies + kLeastStores)>();
@@ -151,7 +160,9 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
         if (i % 2 == 0 && i / 2 < kCopies) ow.copy(r, smem + cbuf * W::kBytes, wave, i / 2);
         if (i < u1 - u0) store(u0 + i, done[i]);
 #pragma unroll
-        for (int j = 0; j < FT; ++j) mma_x_agpr(acc[i][j], w1[i], x[j][s][1]);
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int j = 0; j < FT; ++j) mma_x_agpr(acc[i][j], w1[i], x[j][p][s][1]);
         __builtin_amdgcn_sched_barrier(0);
       }
       advance();
@@ -175,7 +186,7 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
       }
     wave_sync();
     const int n = t * kShortCols + 8 * c;
-    at = n < a.N ? (64 * wave + q) * row_bytes + 2 * n : kOutside;
+    at = n < a.N ? (kWaveRows * wave + q) * row_bytes + 2 * n : kOutside;
   }
 #pragma unroll
   for (int u = 0; u < kStores; ++u) store(u, *reinterpret_cast<const v4i*>(out_read + 4 * u * kOutRow));
@@ -184,20 +195,22 @@ __global__ __launch_bounds__(kShortThreads, 1) void k_linear_short(LinearArgs a,
 
 template <int KS>
 void run(const LinearArgs& a, bool w_trans, hipStream_t s) {
-  const int m_tiles = (int)ceil_div(a.M, kShortRows), n_tiles = (int)ceil_div(a.N, kShortCols);
-  const int per = short_tiles_per_cta(a.M, a.N);
+  const bool two = a.x_low != 0;   // only with w transposed
+  const int m_tiles = (int)ceil_div(a.M, short_rows(two)), n_tiles = (int)ceil_div(a.N, kShortCols);
+  const int per = short_tiles_per_cta(a.M, a.N, two);
   const int total = m_tiles * (int)ceil_div(n_tiles, per);
   const dim3 grid((unsigned)(ceil_div(total, kXcds) * kXcds)), block(kShortThreads);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a, m_tiles, n_tiles, per, total); };
-  if (w_trans) go(k_linear_short<KS, true>);
-  else go(k_linear_short<KS, false>);
+  if (two) go(k_linear_short<KS, true, true>);
+  else if (w_trans) go(k_linear_short<KS, true, false>);
+  else go(k_linear_short<KS, false, false>);
 }
 
 }  // namespace
 
 // Column tiles per workgroup: as many as leave one workgroup per CU.
-int short_tiles_per_cta(int M, int N) {
-  const int64_t m_tiles = ceil_div(M, kShortRows), n_tiles = ceil_div(N, kShortCols);
+int short_tiles_per_cta(int M, int N, bool two) {
+  const int64_t m_tiles = ceil_div(M, short_rows(two)), n_tiles = ceil_div(N, kShortCols);
   int64_t runs = 256 / m_tiles;
   runs = runs < 1 ? 1 : runs > n_tiles ? n_tiles : runs;
   return (int)ceil_div(n_tiles, runs);

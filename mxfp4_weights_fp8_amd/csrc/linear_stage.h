@@ -69,12 +69,13 @@ struct Operand {
       }
     }
   }
-  // the buffer resource of step s; size 0 from `end` on
-  __device__ v4i_s rsrc(int s, int end) const {
-    int64_t bytes = left - s * step;
+  // the buffer resource of step s, `shift` bytes behind it; size 0 unless it is `wanted`
+  __device__ v4i_s rsrc(int s, bool wanted, int shift = 0) const {
+    const int64_t at = s * step + shift;
+    int64_t bytes = left - at;
     const int64_t most = (int64_t)(TRANS ? 64 : ROWS) * row_bytes;   // keeps the size in 32 bits
     bytes = bytes < 0 ? 0 : bytes > most ? most : bytes;
-    return rsrc4(base + s * step, s < end ? (uint32_t)bytes : 0u);
+    return rsrc4(base + at, wanted ? (uint32_t)bytes : 0u);
   }
   __device__ void copy(v4i_s r, uint8_t* stage, int wave, int i) const {
     dma16(r, lds_addr(stage + (kCopies * wave + i) * 1024), voff[i], 0);

@@ -43,7 +43,9 @@ __device__ __forceinline__ void mma_agpr(v4f& acc, const v4i& a, const v4i& b) {
 #endif
 }
 
-template <int FT, int FW, bool XT, bool WT>
+// TWO: x in two parts. The steps of the contraction run twice, over x's high parts and
+// then over its low ones, with the same w.
+template <int FT, int FW, bool XT, bool WT, bool TWO>
 __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, int m_tiles, int n_tiles) {
   constexpr int kRows = 32 * FT, kCols = 32 * FW;
   constexpr int kXStages = 3, kWStages = 2;
@@ -72,7 +74,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & 1, wn = wave >> 1;
   // this split's steps, dealt as evenly as they go
-  const int steps = (a.C + 63) / 64;
+  const int part_steps = (a.C + 63) / 64, steps = TWO ? 2 * part_steps : part_steps;
   const int s0 = (int)((int64_t)steps * split / a.splits), s1 = (int)((int64_t)steps * (split + 1) / a.splits);
 
   X ox;
@@ -97,11 +99,16 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
     v4i x[FT];
   };
   Ops ops[2];
+  auto low = [&](int s) { return TWO && s >= part_steps; };
+  auto rsrc_x = [&](int s) {
+    return ox.rsrc(low(s) ? s - part_steps : s, s < s1, low(s) ? 2 * a.x_low : 0);
+  };
+  auto rsrc_w = [&](int s) { return ow.rsrc(low(s) ? s - part_steps : s, s < s1); };
   auto copy_x = [&](v4i_s r, int buf, int i) { ox.copy(r, smem + buf * X::kBytes, wave, i); };
   auto copy_w = [&](v4i_s r, int buf, int i) { ow.copy(r, smem_w + buf * W::kBytes, wave, i); };
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    const v4i_s rw0 = ow.rsrc(s0 + b, s1), rx0 = ox.rsrc(s0 + b, s1);
+    const v4i_s rw0 = rsrc_w(s0 + b), rx0 = rsrc_x(s0 + b);
 #pragma unroll
     for (int i = 0; i < W::kCopies; ++i) copy_w(rw0, b, i);
 #pragma unroll
@@ -117,7 +124,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
   int xb = 0, wb = 0;   // stages of step s
   for (int s = s0; s < s1; ++s) {
     const int xb1 = xb + 1 == kXStages ? 0 : xb + 1, xb2 = xb1 + 1 == kXStages ? 0 : xb1 + 1;
-    const v4i_s rx2 = ox.rsrc(s + 2, s1), rw2 = ow.rsrc(s + 2, s1);
+    const v4i_s rx2 = rsrc_x(s + 2), rw2 = rsrc_w(s + 2);
     const uint8_t *px = smem + xb * X::kBytes, *pw = smem_w + wb * W::kBytes;
 #pragma unroll
     for (int p = 0; p < FW; ++p) {   // half A
@@ -210,28 +217,33 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_linear_tile(LinearArgs a, i
   }
 }
 
-template <int FT, int FW, bool XT, bool WT>
+template <int FT, int FW, bool XT, bool WT, bool TWO>
 void run(const LinearArgs& a, hipStream_t s) {
   const int m_tiles = (int)ceil_div(a.M, 32 * FT), n_tiles = (int)ceil_div(a.N, 32 * FW);
   const int64_t total = (int64_t)m_tiles * n_tiles * a.splits;
-  hipLaunchKernelGGL((k_linear_tile<FT, FW, XT, WT>), dim3((unsigned)(ceil_div(total, kXcds) * kXcds)),
+  hipLaunchKernelGGL((k_linear_tile<FT, FW, XT, WT, TWO>), dim3((unsigned)(ceil_div(total, kXcds) * kXcds)),
                      dim3(kTileThreads), 0, s, a, m_tiles, n_tiles);
 }
 
-template <bool XT, bool WT>
+template <bool XT, bool WT, bool TWO>
 void by_tile(const LinearArgs& a, const LinearPlan& p, hipStream_t s) {
-  if (p.ft == 8 && p.fw == 8) run<8, 8, XT, WT>(a, s);
-  else if (p.ft == 8) run<8, 6, XT, WT>(a, s);
-  else if (p.ft == 6) run<6, 8, XT, WT>(a, s);
-  else run<4, 4, XT, WT>(a, s);
+  if (p.ft == 8 && p.fw == 8) run<8, 8, XT, WT, TWO>(a, s);
+  else if (p.ft == 8) run<8, 6, XT, WT, TWO>(a, s);
+  else if (p.ft == 6) run<6, 8, XT, WT, TWO>(a, s);
+  else run<4, 4, XT, WT, TWO>(a, s);
+}
+template <bool XT>   // a gradient's layout: w transposed, x in one or two parts
+void by_parts(const LinearArgs& a, const LinearPlan& p, hipStream_t s) {
+  if (a.x_low) by_tile<XT, true, true>(a, p, s);
+  else by_tile<XT, true, false>(a, p, s);
 }
 
 }  // namespace
 
 void launch_tiles(const LinearArgs& a, const LinearPlan& p, Layout l, hipStream_t s) {
-  if (l == Layout::kRows) by_tile<false, false>(a, p, s);
-  else if (l == Layout::kWTrans) by_tile<false, true>(a, p, s);
-  else by_tile<true, true>(a, p, s);
+  if (l == Layout::kRows) by_tile<false, false, false>(a, p, s);
+  else if (l == Layout::kWTrans) by_parts<false>(a, p, s);
+  else by_parts<true>(a, p, s);
 }
 
 }  // namespace moe

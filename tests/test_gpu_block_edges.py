@@ -1,0 +1,63 @@
+"""GPU tests of the operators in front of the FFN at their edges: gradients whose dz is no
+bf16 value, against the bound that the outputs' own rounding leaves. Tolerances as in
+test_gpu_block.py."""
+
+import math
+
+import pytest
+import torch
+
+import mxfp4_weights_fp8_amd as moe
+from gpu_helpers import say
+from oracle import block as ob
+from test_gpu_block import BF, BF16, F32, F64, U, dev, on, randn, within  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------- gradients of the product
+
+@pytest.mark.parametrize("M,N,K,act,dtype", [
+    (1, 1, 128, "none", F32), (7, 384, 256, "none", F32), (65, 130, 128, "sigmoid", BF16), (129, 70, 384, "silu", BF16),
+    (300, 384, 512, "relu", F32), (1000, 33, 256, "gelu", F32), (4100, 40, 256, "none", F32), (63, 1000, 128, "gelu", BF16),
+    (200, 129, 640, "relu", BF16), (200, 129, 640, "none", BF16),
+    # the tile shapes, the contraction split and not
+    (128, 1000, 8192, "none", F32), (128, 12001, 1024, "none", F32), (2048, 16500, 768, "none", F32),
+    (1000, 500, 8192, "silu", BF16), (12000, 500, 1024, "none", F32), (16500, 2000, 768, "none", F32),
+    # short contractions over 128, 256 and 384 columns of dz
+    (5003, 100, 8064, "none", F32), (5001, 200, 8064, "silu", BF16), (4997, 300, 8064, "none", F32), (20001, 384, 1152, "none", F32)])
+def test_linear_grad_keeps_dz(dev, M, N, K, act, dtype):
+    """dx and dw are off by their own rounding and by 2^-15 of dz (a bf16 dz would add 2^-8
+    of it), whatever dy's type and the activation."""
+    x, w = randn(M, K, seed=1, dtype=BF16), randn(N, K, seed=2, scale=1 / math.sqrt(K), dtype=BF16)
+    dy = randn(M, N, seed=3, dtype=dtype)
+    z = None if act == "none" else randn(M, N, seed=4, scale=1.5)
+    say(f"[linear_grad {M}x{N}x{K} {act} {dtype}]")
+    dx, dw, _ = moe.linear_grad(*on(dev, dy, x, w), act=act, z=None if z is None else z.to(dev))
+    torch.cuda.synchronize()
+    rdx, rdw, _, dz = ob.linear_grad_ref(dy, x, w, act, z)
+    op = 2.0 ** -15 + (0 if act == "none" else 32 * U)       # the operand's two parts, its slope
+    ax, aw = dz.abs() @ w.to(F64).abs(), dz.abs().t() @ x.to(F64).abs()
+    within(dx, rdx, rdx.abs() * BF + ax * (op + (2 * N / 32 + 64) * 2 * U), "dx")
+    within(dw, rdw, rdw.abs() * BF + aw * (op + (2 * M / 32 + 64) * 2 * U), "dw")
+
+
+def test_linear_grad_of_infinities_and_far_values(dev):
+    """An infinite dy reaches its own row of dx and its own row of dw, as an infinity (its
+    low part is 0); values near fp32's largest stay finite in both parts."""
+    M, N, K = 70, 40, 128
+    x, w = randn(M, K, seed=1, dtype=BF16).abs() + 1, randn(N, K, seed=2, dtype=BF16).abs() + 1
+    dy = randn(M, N, seed=3)
+    dy[3, 5], dy[9, 7] = math.inf, -math.inf
+    dy[20] = 0
+    dy[20, 11] = 3.3999e38                       # above bf16's largest value
+    w[11] = 2.0 ** -10
+    x[20] = 2.0 ** -10
+    dx, dw, _ = (t.cpu() for t in moe.linear_grad(*on(dev, dy, x, w)))
+    assert bool((dx[3] == math.inf).all()) and bool((dx[9] == -math.inf).all())
+    assert bool((dw[5] == math.inf).all()) and bool((dw[7] == -math.inf).all())
+    rows = [m for m in range(M) if m not in (3, 9)]
+    cols = [n for n in range(N) if n not in (5, 7)]
+    assert bool(torch.isfinite(dx[rows]).all()) and bool(torch.isfinite(dw[cols]).all())
+    rdx = ob.linear_grad_ref(dy[rows], x[rows], w)[0]
+    within(dx[rows], rdx, rdx.abs() * BF + (dy[rows].abs().to(F64) @ w.to(F64)) * 2.0 ** -14, "dx")
