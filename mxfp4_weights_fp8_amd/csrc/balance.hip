@@ -226,11 +226,15 @@ __global__ __launch_bounds__(256) void k_balance_sum(const double* __restrict__ 
 }
 
 // Small batches of few sequences in one launch of one workgroup: sequence by sequence,
-// the histogram, then its tokens.
-constexpr int kOneThreads = 1024;
+// the histogram, then its tokens. With many experts half the threads, as 16 waves leave
+// each 128 registers and a row's scores and slopes then go to scratch (64 x 512 sigmoid 17.4
+// us on 1024 threads, 9.8 on 512; 256 x 384 softmax, which fits, 15.8 and 18.2).
+constexpr int one_threads(int nv, int score) {
+  return nv <= 4 || (nv <= 6 && score == MOE_SCORE_SOFTMAX) ? 1024 : 512;
+}
 template <int LPR, int NV, int SCORE, bool BF16, bool VEC>
-__global__ __launch_bounds__(kOneThreads) void k_balance_one(BalanceArgs a) {
-  constexpr int kRows = kOneThreads / LPR;
+__global__ __launch_bounds__(one_threads(NV, SCORE)) void k_balance_one(BalanceArgs a) {
+  constexpr int kOneThreads = one_threads(NV, SCORE), kRows = kOneThreads / LPR;
   __shared__ __attribute__((aligned(16))) int32_t hist[4 * LPR * NV];   // E at most
   __shared__ double red[kRows];
   const int lane = threadIdx.x & (LPR - 1), sub = threadIdx.x / LPR;
@@ -267,9 +271,23 @@ __global__ __launch_bounds__(kOneThreads) void k_balance_one(BalanceArgs a) {
   }
 }
 
-// One workgroup where it needs at most 8 rounds of 64 tokens and 4 sequences (256 x 64
-// top-6: 6 us, 11 us per call, bound by the host; the four launches below 22 us per call).
-inline bool one_workgroup(const moe_gate_dims& d, int B) { return d.T <= 512 && d.E <= 512 && B <= 4; }
+// One workgroup while its work is small: its rounds over the tokens, one more for each
+// further sequence, times the groups of experts that a lane scores, times what a score
+// costs. Per call in us (the four launches below take 20-21, bound by the host; in a
+// captured graph 9-19), one workgroup at
+//   cost up to 48  11, bound by the host
+//   64 to 96       512 x 128 softmax 13 and sigmoid 16, 256 x 256 13 and 15, 128 x 512 13
+//                  and 16, 256 x 384 softmax 16, sqrtsoftplus 256 x 128 16 and
+//                  64 x 512 18
+//   from 128 on    512 x 256 softmax 22 and sigmoid 26, 512 x 128 sqrtsoftplus 29
+inline bool one_workgroup(const moe_gate_dims& d, int B) {
+  if (d.T > 512 || d.E > 512 || B > 4) return false;
+  int groups = 0;
+  by_few_experts(d.E, [&](auto nv) { groups = decltype(nv)::value; });
+  const int rows = one_threads(groups, d.score) / 16;
+  const int score = d.score == MOE_SCORE_SOFTMAX ? 2 : d.score == MOE_SCORE_SIGMOID ? 3 : 6;
+  return (ceil_div(d.T, rows) + B - 1) * (rows / 32) * groups * score <= 96;
+}
 
 }  // namespace
 
@@ -288,7 +306,7 @@ hipError_t launch_balance(const moe_gate_dims& d, int B, float alpha, const void
         by_layout(bf, vec, [&](auto bf16, auto v) {
           hipLaunchKernelGGL((k_balance_one<16, decltype(nv)::value, decltype(score)::value, decltype(bf16)::value != 0,
                                             decltype(v)::value != 0>),
-                             dim3(1), dim3(kOneThreads), 0, s, a);
+                             dim3(1), dim3(one_threads(decltype(nv)::value, decltype(score)::value)), 0, s, a);
         });
       });
     });

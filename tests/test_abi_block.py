@@ -127,3 +127,12 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
               lambda: moe.add_norm(x[0], x[0])):
         with pytest.raises(ValueError):
             f()
+
+
+def test_balance_loss_leaves_one_workgroup_by_work():
+    """No workspace: one workgroup does everything. Tokens times experts (times two for
+    sqrtsoftplus) decide, not the two of them apart."""
+    def need(T, E, B=1, score=0):
+        return moe.lib().moe_balance_loss_workspace_bytes(moe.GateDims(T, E, 4, score, 0, 1, 1.0), B)
+    assert all(need(*a) == 0 for a in ((512, 64), (256, 256), (64, 512), (7, 384, 1, 2), (64, 64, 4, 1), (64, 384, 4), (0, 512)))
+    assert all(need(*a) > 0 for a in ((512, 512), (512, 384, 1, 1), (256, 384, 1, 1), (512, 128, 1, 2), (128, 384, 1, 2), (512, 128, 4, 1)))

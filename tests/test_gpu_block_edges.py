@@ -10,7 +10,7 @@ import torch
 import mxfp4_weights_fp8_amd as moe
 from gpu_helpers import say
 from oracle import block as ob
-from test_gpu_block import BF, BF16, F32, F64, U, dev, on, randn, within  # noqa: F401
+from test_gpu_block import BF, BF16, F32, F64, SCORES, U, check_balance, dev, on, randn, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,18 @@ def test_linear_grad_of_infinities_and_far_values(dev):
     assert bool(torch.isfinite(dx[rows]).all()) and bool(torch.isfinite(dw[cols]).all())
     rdx = ob.linear_grad_ref(dy[rows], x[rows], w)[0]
     within(dx[rows], rdx, rdx.abs() * BF + (dy[rows].abs().to(F64) @ w.to(F64)) * 2.0 ** -14, "dx")
+
+
+# --------------------------------------------------------------------------- balance loss
+
+@pytest.mark.parametrize("T,E", [(64, 384), (40, 512), (33, 300), (128, 512), (129, 512), (256, 256), (512, 100), (512, 256),
+                                 (300, 385)])
+@pytest.mark.parametrize("score", SCORES)
+def test_balance_loss_of_small_batches(dev, T, E, score):
+    """On both sides of the choice between one workgroup and four launches."""
+    l = randn(T, E, seed=T + E, scale=1.5)
+    ids = torch.randint(-1, E + 1, (T, 6), generator=torch.Generator().manual_seed(7), dtype=torch.int32)
+    say(f"[balance {T}x{E} {score}]")
+    check_balance(dev, l, ids, 0.3, score, None, "one sequence")
+    check_balance(dev, l.to(BF16), ids, 0.3, score, [1, T // 3, T // 3, T - 5], "sequences, bf16")
+    check_balance(dev, l, ids, 0.3, score, [0, T // 4, T // 3, T // 2, T - 1], "four sequences")
