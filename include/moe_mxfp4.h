@@ -417,7 +417,8 @@ int moe_gate_grad(const moe_gate_dims* dims, const void* logits, const int32_t* 
  *   sequence; f_be = E c_be / (K n_b)
  *   loss = alpha / B * sum over b, e of f_be P_be          (an empty sequence adds 0)
  * The counts are constants of the gradient. scale and renorm are not used.
- *   logits       [T, E]; a row without any unmasked expert has p = 0
+ *   logits       [T, E]; a row without any unmasked expert has p = 0, and so has one whose
+ *                logits are all below -690 (sigmoid, sqrtsoftplus)
  *   topk_ids     [T, K]; ids outside [0, E) are not counted
  *   seq_offsets  [B + 1] int32 on the device, ascending within [0, T]; NULL with B == 1:
  *                all tokens are one sequence. (With offsets that are not ascending the

@@ -88,10 +88,54 @@ __device__ __forceinline__ void load_row(const BalanceArgs& a, int64_t t, int la
   for (int j = 0; j < NV; ++j) load_logits4<BF16, VEC>(row, 4 * (j * LPR + lane), a.E, l[j]);
 }
 
-// One token of logits s: writes its gradient, returns its part of the loss.
-template <int LPR, int NV, int SCORE, bool BF16, bool VEC>
+// The counts of a sequence, and what makes them coefficients.
+struct Sequence {
+  const int32_t* counts;
+  float factor;
+};
+
+// A row whose scores come to less than kTinySum has every logit below -40 or so, where
+// sigmoid(l) is e^l and sqrt(softplus(l)) e^(l/2) to fp32, so that scores and slopes may be
+// taken relative to the largest logit's: their common factor, which fp32 cannot hold below
+// 2^-126, leaves p and the gradient alone. Below kLowestLogit a row counts as empty. Such
+// rows are rare: they are read again, an expert at a time, so that the others keep their
+// registers (32768 x 384 takes as long as without them).
+constexpr float kTinySum = 8.67361738e-19f;   // 2^-60
+constexpr float kLowestLogit = -690.f;
+template <int LPR, int SCORE, bool BF16>
+__device__ __forceinline__ float tiny_row(const BalanceArgs& a, int64_t t, int lane, const Sequence& q) {
+  constexpr float kPower = SCORE == MOE_SCORE_SIGMOID ? 1.f : 0.5f;   // slope = kPower * score
+  const char* row = reinterpret_cast<const char*>(a.logits) + t * a.E * (BF16 ? 2 : 4);
+  float top = kNone;
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += LPR) top = fmaxf(top, load_logit<BF16>(row, e));
+  top = row_max<LPR>(top);
+  auto score = [&](int e) {
+    const float l = load_logit<BF16>(row, e);
+    return top < kLowestLogit || l == kNone ? 0.f : exp_f(kPower * (l - top));
+  };
+  float sum = 0.f, dot = 0.f;
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += LPR) {
+    const float s = score(e);
+    sum += s;
+    dot += s * (q.factor * (float)q.counts[e]);
+  }
+  sum = row_sum<LPR>(sum);
+  dot = row_sum<LPR>(dot);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  dot *= inv;
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += LPR)
+    a.dl[t * a.E + e] = kPower * score(e) * ((q.factor * (float)q.counts[e] - dot) * inv);
+  return dot;
+}
+
+// One token of logits s: writes its gradient, returns its part of the loss. coef: factor
+// times the counts of its sequence, which `sequence` gives again where it is asked.
+template <int LPR, int NV, int SCORE, bool BF16, bool VEC, typename F>
 __device__ __forceinline__ float balance_row(const BalanceArgs& a, int64_t t, int lane, const float (&coef)[NV][4],
-                                             float (&s)[NV][4]) {
+                                             F sequence, float (&s)[NV][4]) {
   float* dl = a.dl + t * a.E;
   float k[NV][4];   // what multiplies (a - d) / sum in the gradient; s becomes the scores
   float top = kNone;
@@ -115,6 +159,8 @@ __device__ __forceinline__ float balance_row(const BalanceArgs& a, int64_t t, in
     }
   sum = row_sum<LPR>(sum);
   dot = row_sum<LPR>(dot);
+  if constexpr (SCORE != MOE_SCORE_SOFTMAX)
+    if (sum < kTinySum) return tiny_row<LPR, SCORE, BF16>(a, t, lane, sequence());   // all lanes of the row
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   dot *= inv;
 #pragma unroll
@@ -187,24 +233,27 @@ __global__ __launch_bounds__(kGateThreads) void k_balance(BalanceArgs a) {
   constexpr int kRows = kGateThreads / LPR;   // rows in flight
   __shared__ double red[kRows];
   const int lane = threadIdx.x & (LPR - 1), sub = threadIdx.x / LPR;
-  const int64_t first = (int64_t)blockIdx.x * kBalanceRows;
-  const int64_t end = first + kBalanceRows < a.T ? first + kBalanceRows : a.T;
+  const int first = blockIdx.x * kBalanceRows, end = min(first + kBalanceRows, (int)a.T);   // T is at most 2^21
   double mine = 0.0;
-  int64_t stop = -1;   // end of the sequence whose coefficients are held
+  int stop = -1;   // end of the sequence whose coefficients are held
   float coef[NV][4];
-  for (int64_t t = first + sub; t < end; t += kRows) {
+  for (int t = first + sub; t < end; t += kRows) {
     float l[NV][4];
     load_row<LPR, NV, BF16, VEC>(a, t, lane, l);
     if (t >= stop) {
       const int b = find_seq<LPR>(a, t, lane);
       if (b < 0) {   // in front of the first sequence or behind the last
-        for (int e = lane; e < a.E; e += LPR) a.dl[t * a.E + e] = 0.f;
+        for (int e = lane; e < a.E; e += LPR) a.dl[(int64_t)t * a.E + e] = 0.f;
         continue;
       }
-      stop = a.off ? a.off[b + 1] : a.T;
+      stop = a.off ? a.off[b + 1] : (int)a.T;
       load_coef<LPR, NV, VEC>(a.counts + (int64_t)b * a.E, a.E, seq_factor(a, b), lane, coef);
     }
-    mine += (double)balance_row<LPR, NV, SCORE, BF16, VEC>(a, t, lane, coef, l);
+    auto sequence = [&]() {
+      const int b = find_seq<LPR>(a, t, lane);
+      return Sequence{a.counts + (int64_t)b * a.E, seq_factor(a, b)};
+    };
+    mine += (double)balance_row<LPR, NV, SCORE, BF16, VEC>(a, t, lane, coef, sequence, l);
   }
   if (lane == 0) red[sub] = mine;
   __syncthreads();
@@ -252,11 +301,13 @@ __global__ __launch_bounds__(one_threads(NV, SCORE)) void k_balance_one(BalanceA
     for (int e = threadIdx.x; e < a.E; e += kOneThreads) a.counts[(int64_t)b * a.E + e] = hist[e];
     if (hi > lo) {   // the same for everybody
       float coef[NV][4];
-      load_coef<LPR, NV, VEC>(hist, a.E, seq_factor(a, b), lane, coef);
+      const float factor = seq_factor(a, b);
+      load_coef<LPR, NV, VEC>(hist, a.E, factor, lane, coef);
+      auto sequence = [&]() { return Sequence{hist, factor}; };
       for (int64_t t = lo + sub; t < hi; t += kRows) {
         float l[NV][4];
         load_row<LPR, NV, BF16, VEC>(a, t, lane, l);
-        mine += (double)balance_row<LPR, NV, SCORE, BF16, VEC>(a, t, lane, coef, l);
+        mine += (double)balance_row<LPR, NV, SCORE, BF16, VEC>(a, t, lane, coef, sequence, l);
       }
     }
     __syncthreads();   // the histogram is read before the next sequence clears it

@@ -76,3 +76,21 @@ def test_balance_loss_of_small_batches(dev, T, E, score):
     check_balance(dev, l, ids, 0.3, score, None, "one sequence")
     check_balance(dev, l.to(BF16), ids, 0.3, score, [1, T // 3, T // 3, T - 5], "sequences, bf16")
     check_balance(dev, l, ids, 0.3, score, [0, T // 4, T // 3, T // 2, T - 1], "four sequences")
+
+
+@pytest.mark.parametrize("T,E", [(40, 64), (600, 384), (30, 450), (9, 1000), (5, 4096)])
+@pytest.mark.parametrize("score", ["sigmoid", "sqrtsoftplus"])
+def test_balance_loss_of_rows_with_tiny_scores(dev, T, E, score):
+    """Rows whose scores fp32 cannot hold have their probabilities and gradient all the same,
+    down to logits of -690."""
+    l = randn(T, E, seed=T, scale=1.5)
+    for i, shift in enumerate((-30.0, -39.0, -42.0, -60.0, -88.0, -100.0, -175.0, -300.0, -680.0)):
+        l[i::11] += shift
+    l[2::11, 1::3] = -math.inf
+    ids = torch.randint(0, E, (T, 6), generator=torch.Generator().manual_seed(7), dtype=torch.int32)
+    say(f"[balance {T}x{E} {score}]")
+    for logits in (l, l.to(BF16)):
+        check_balance(dev, logits, ids, 0.3, score, None, "tiny scores")
+    l[:] = -800.0                                  # below the documented end: no probabilities
+    loss, _, dl = moe.balance_loss(*on(dev, l, ids), 0.3, score=score)
+    assert float(loss) == 0 and not bool(dl.any())
