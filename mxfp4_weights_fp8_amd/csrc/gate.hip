@@ -5,12 +5,14 @@
 //
 // Order of the picks. Every score rises with its logit, so without a bias the
 // logits themselves are compared, which is exact. With one, keys s + b are formed in
-// fp32 with the hardware's fast functions, each off by at most half of `slack`. All
-// experts whose key is within `slack` of the K-th best one are taken as candidates
-// (a true pick cannot be further away), and where two neighbours in their order are
-// within it too, the candidates are ranked again by fp64 keys: one fp64 score per
-// lane. Where there are more candidates than lanes (many equal keys) the whole row
-// is selected in fp64. Equal keys go to the lowest index.
+// fp32 with the hardware's fast functions. A key is off by what its score is, at most half
+// of `slack`, and by its own rounding; the size of a bias enters by that rounding alone, so
+// that an expert held back by a bias of -1e9 makes nobody else's key uncertain. All
+// experts whose key may still reach the K-th best one are taken as candidates, and where
+// two neighbours in their order cannot be told apart either, the candidates are ranked again
+// by fp64 keys: one fp64 score per lane. Where there are more candidates than lanes (many
+// equal keys) the whole row is selected in fp64, in ten to twenty times the time. Equal
+// keys go to the lowest index.
 //
 // Selection. The keys, as integers of the same order, lie in LDS in the lane's groups
 // of four, each group's maximum in a register. A round is the maximum over the
@@ -18,8 +20,9 @@
 // it (group by group, then in the one group read back), and one group rewritten:
 // about 50 instructions instead of the 120 of scanning 24 keys in registers.
 //
-// 32768 x 384 top-8 with bias (52 MB): 25-27 us, bound by the vector units (scores of 24
-// experts per lane, then eight rounds); 7 x 384 5.2-5.9 us, latency.
+// 32768 x 384 top-8 with bias (52 MB): 23-27 us, bound by the vector units (scores of 24
+// experts per lane, then eight rounds), the same with experts at biases of -1e9 (286-598 us
+// when their size went into everybody's bound); 7 x 384 5.2-5.9 us, latency.
 #include "router.h"
 
 namespace moe {
@@ -38,11 +41,11 @@ __device__ __forceinline__ float from_key(int k) { return __int_as_float(k ^ ((k
 // Scores from the hardware's exp2, log2, rcp and sqrt (1 ulp each): the product
 // l log2(e) is off by 2^-24 of itself, at most 127 * 2^-24 where e^l is not out of
 // range, so e^l is off by at most 6e-6 of itself, and what follows by no more:
-// kSlack (score + |bias|) is twice a key's error. One exception: 1 + e^l of
-// sqrt(softplus) is rounded to 2^-24, which moves a score s below kLowScore by up to
-// 2^-25 / s, or s itself where that is less: by up to 2.5e-4 (kLowSlack is twice
-// that).
-constexpr float kSlack = 1.5e-5f, kLowScore = 0.1f, kLowSlack = 5e-4f;
+// kSlack score is twice a score's error. One exception: 1 + e^l of sqrt(softplus) is
+// rounded to 2^-24, which moves a score s below kLowScore by up to 2^-25 / s, or s itself
+// where that is less: by up to 2.5e-4 (kLowSlack is twice that). kRounding |key| is twice
+// the rounding of the sum with the bias.
+constexpr float kSlack = 1.5e-5f, kLowScore = 0.1f, kLowSlack = 5e-4f, kRounding = 0x1p-23f;
 template <int SCORE>
 __device__ __forceinline__ float score_fast(float l) {
   if constexpr (SCORE == MOE_SCORE_SIGMOID)
@@ -120,7 +123,8 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
   if constexpr (SCORE == MOE_SCORE_SOFTMAX) softmax();
 
   int best_of[NV];       // largest key of each group
-  float bias_size = 0.f;  // largest |bias| of the row's unmasked experts
+  float score_size = 0.f;     // the row's largest score
+  float bias_top = -INFINITY;   // the largest bias (sqrt(softplus) alone asks)
   if (a.bias) {
     const float inv_sum = 1.f / sum;
 #pragma unroll
@@ -141,21 +145,16 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
         float s;
         if constexpr (SCORE == MOE_SCORE_SOFTMAX) s = l[j][i] * inv_sum;
         else s = score_fast<SCORE>(l[j][i]);
+        score_size = fmaxf(score_size, s);   // 0 or less where masked
         k[i] = to_key(masked ? kNone : s + bias[i]);
       }
       groups[j][threadIdx.x] = k;
       best_of[j] = max(max(k[0], k[1]), max(k[2], k[3]));
-      bias_size = fmaxf(fmaxf(bias_size, fmaxf(fabsf(bias[0]), fabsf(bias[1]))), fmaxf(fabsf(bias[2]), fabsf(bias[3])));
+      if constexpr (SCORE == MOE_SCORE_SQRTSOFTPLUS)
+        bias_top = fmaxf(fmaxf(bias_top, fmaxf(bias[0], bias[1])), fmaxf(bias[2], bias[3]));
     }
-    bias_size = row_max<LPR>(bias_size);
-    if (bias_size == INFINITY) {   // experts masked by their bias: the largest of the others
-      bias_size = 0.f;
-      for (int e = lane; e < a.E; e += LPR) {
-        const float b = a.bias[e];
-        bias_size = b == kNone || !(b == b) ? bias_size : fmaxf(bias_size, fabsf(b));
-      }
-      bias_size = row_max<LPR>(bias_size);
-    }
+    score_size = row_max<LPR>(score_size);
+    if constexpr (SCORE == MOE_SCORE_SQRTSOFTPLUS) bias_top = row_max<LPR>(bias_top);
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -207,21 +206,19 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
     }
   } else {
     bool more = true;
-    // the key before, the smallest step between keys, the errors' bound (from the best
-    // key: no score is above it by more than bias_size), and what a candidate needs
-    // once there are K
-    float before = INFINITY, step = INFINITY, slack = 0.f, least = kNone;
+    // the key before, the smallest step between keys less their roundings, the bound of
+    // two scores' errors, and what a candidate needs once there are K
+    float before = INFINITY, step = INFINITY, slack = kSlack * score_size + 1e-18f, least = kNone;
     for (int j = 0; j < LPR && __any(more); ++j) {
       const int best = row_best();
       const float f = from_key(best);
       more = more && best != kNoKey && !(f < least);
       if (!more) continue;   // the same in all lanes of the row
-      if (j == 0) slack = kSlack * (fabsf(f) + 2.f * bias_size) + 1e-18f;
       if (j == a.K - 1) {
-        if (SCORE == MOE_SCORE_SQRTSOFTPLUS && !(f > kLowScore + kLowSlack + bias_size + slack)) slack += kLowSlack;
-        least = f - slack;
+        if (SCORE == MOE_SCORE_SQRTSOFTPLUS && !(f > kLowScore + kLowSlack + bias_top + slack)) slack += kLowSlack;
+        least = f - slack - 2.f * kRounding * fabsf(f);
       }
-      step = fminf(step, before - f);
+      step = fminf(step, before - f - kRounding * (fabsf(before) + fabsf(f)));   // behind infinity NaN, which is passed over
       before = f;
       const int index = take(best);
       mine = j == lane ? index : mine;

@@ -3,6 +3,7 @@ bf16 value, against the bound that the outputs' own rounding leaves. Tolerances 
 test_gpu_block.py."""
 
 import math
+import time
 
 import pytest
 import torch
@@ -10,7 +11,7 @@ import torch
 import mxfp4_weights_fp8_amd as moe
 from gpu_helpers import say
 from oracle import block as ob
-from test_gpu_block import BF, BF16, F32, F64, SCORES, U, check_balance, dev, on, randn, within  # noqa: F401
+from test_gpu_block import BF, BF16, F32, F64, SCORES, U, check_balance, check_gate, dev, on, randn, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -94,3 +95,56 @@ def test_balance_loss_of_rows_with_tiny_scores(dev, T, E, score):
     l[:] = -800.0                                  # below the documented end: no probabilities
     loss, _, dl = moe.balance_loss(*on(dev, l, ids), 0.3, score=score)
     assert float(loss) == 0 and not bool(dl.any())
+
+
+# ----------------------------------------------------------------------------------- gate
+
+FAR_BIASES = [1e3, -1e3, -1e4, -1e9, 1e9, -3e38, 3e38, -math.inf, math.inf, math.nan]
+
+
+@pytest.mark.parametrize("T,E,K", [(20, 384, 8), (33, 37, 5), (9, 600, 17), (4, 2100, 64)])
+@pytest.mark.parametrize("score", SCORES)
+def test_gate_with_far_biases(dev, T, E, K, score):
+    """Experts forced in or held back by biases of any size leave the others' choice exact,
+    near ties of the others among them."""
+    l = randn(T, E, seed=E, scale=2.0)
+    l[:, 1::4] = l[:, 0::4][:, : l[:, 1::4].shape[1]] + 1e-7       # pairs that fp32 scores cannot tell apart
+    l[3, E // 2:] = -math.inf
+    say(f"[gate {T}x{E} top-{K} {score}]")
+    for far in FAR_BIASES:
+        b = randn(E, seed=3, scale=0.1)
+        b[0::4] = 0.0
+        b[1::4] = 0.0
+        b[7] = far
+        check_gate(dev, l, K, f"one bias of {far}", score, bias=b)
+        b[2::3] = far
+        check_gate(dev, l, K, f"a third of the biases {far}", score, bias=b)
+        b[: E - 3] = far                                           # fewer than K left where they are held back
+        check_gate(dev, l, K, f"most biases {far}", score, bias=b)
+
+
+@pytest.mark.parametrize("score", SCORES)
+def test_gate_is_not_slowed_by_far_biases(dev, score):
+    """One expert held back or forced in by a finite bias leaves the fast path to the rows
+    (ranking every row in 64 bits takes ten to twenty times as long)."""
+    l = randn(8192, 384, seed=1).to(dev)
+
+    def us(far):
+        b = randn(384, seed=2, scale=0.1)
+        if far:
+            b[17] = far
+        bd = b.to(dev)
+        best = math.inf
+        for _ in range(5):
+            torch.cuda.synchronize()
+            t = time.perf_counter()
+            for _ in range(40):
+                moe.gate(l, 8, score=score, bias=bd)
+            torch.cuda.synchronize()
+            best = min(best, (time.perf_counter() - t) / 40 * 1e6)
+        return best
+    plain = us(None)
+    for far in (-1e4, -1e9, 1e9, torch.finfo(F32).min):
+        t = us(far)
+        say(f"[gate {score}] bias {far}: {t:.1f} us against {plain:.1f}")
+        assert t < 3 * plain
