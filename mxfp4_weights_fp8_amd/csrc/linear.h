@@ -83,9 +83,9 @@ __device__ __forceinline__ float activate_slope(float z, int act) {
       return p * (1.f + z * (1.f - p));
     }
     case MOE_ACT_GELU: return 0.5f * erfcf(z * -0.707106781f) + z * expf(-0.5f * z * z) * 0.398942280f;
-    case MOE_ACT_SIGMOID: {
-      const float p = sigmoid_f(z);
-      return p * (1.f - p);
+    case MOE_ACT_SIGMOID: {   // p (1 - p) without the difference, which cancels for z > 0
+      const float e = expf(-fabsf(z)), r = 1.f / (1.f + e);
+      return e * r * r;
     }
     default: return 1.f;
   }

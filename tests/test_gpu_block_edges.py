@@ -64,6 +64,19 @@ def test_linear_grad_of_infinities_and_far_values(dev):
     within(dx[rows], rdx, rdx.abs() * BF + (dy[rows].abs().to(F64) @ w.to(F64)) * 2.0 ** -14, "dx")
 
 
+def test_sigmoid_slope_keeps_its_digits(dev):
+    """One row of dy = 1: dbias is the slope itself, e^-|z| / (1 + e^-|z|)^2, to a few roundings
+    at either end."""
+    z = torch.linspace(-60, 60, 1201).view(1, -1)
+    N = z.shape[1]
+    x, w = torch.ones(1, 128, dtype=BF16), torch.ones(N, 128, dtype=BF16)
+    e = torch.exp(-z.to(F64).abs())
+    want = (e / (1 + e) ** 2)[0]
+    for dtype in (BF16, F32):
+        _, _, db = moe.linear_grad(*on(dev, torch.ones(1, N, dtype=dtype), x, w), act="sigmoid", z=z.to(dev))
+        within(db, want, want * 16 * U, "slope")
+
+
 # --------------------------------------------------------------------------- balance loss
 
 @pytest.mark.parametrize("T,E", [(64, 384), (40, 512), (33, 300), (128, 512), (129, 512), (256, 256), (512, 100), (512, 256),
