@@ -478,7 +478,7 @@ def _workspace(nbytes, dev, ws):
 
 
 class Normed(NamedTuple):
-    h: torch.Tensor                  # [T, H] bf16 residual stream (x itself without a residual)
+    h: torch.Tensor                  # [T, H] bf16 residual stream (x itself without a residual and without out.h)
     y: Optional[torch.Tensor]        # [T, H] bf16
     x_q: Optional[torch.Tensor]      # [T, H] uint8 E4M3 codes of y
     x_s: Optional[torch.Tensor]      # [T, H/128] uint8 E8M0 scales
@@ -489,8 +489,9 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     """moe_add_norm on the current stream: h = x + residual, y = RMS norm of h times
     weight, and y's E4M3 codes and E8M0 scales for ffn_quantized. x, residual: bf16
     [T, H]; weight: bf16 or float32 [H]. bf16 / fp8 choose which forms of y are written
-    (None in the other's place). out: tensors to write (None members are allocated);
-    out.h may be the residual, out.y may be x."""
+    (None in the other's place). out: tensors to write (None members are allocated;
+    without a residual h is x itself unless out.h is given, which then receives a copy);
+    out.h may be the residual or x, out.y may be x."""
     dev = _first(x, 2, "x")
     shape = x.shape
     T, H = shape
@@ -500,13 +501,15 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     wp = _tensor(weight, weight.dtype, (H,), dev, "weight")
     h, y, q, s = out if out is not None else (None, None, None, None)
     hp = yp = qp = sp = None
-    if residual is None:
+    if h is not None:
+        hp = _tensor(h, torch.bfloat16, shape, dev, "out.h")
+        if residual is None and hp == xp:
+            hp = None        # x is there already
+    elif residual is None:
         h = x
-    elif h is None:
+    else:
         h = torch.empty_like(x)
         hp = h.data_ptr()
-    else:
-        hp = _tensor(h, torch.bfloat16, shape, dev, "out.h")
     if not bf16:
         y = None
     elif y is None:

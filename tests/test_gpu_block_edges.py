@@ -16,6 +16,26 @@ from test_gpu_block import BF, BF16, F32, F64, SCORES, U, check_balance, check_g
 pytestmark = pytest.mark.gpu
 
 
+# ------------------------------------------------------------------------------- add_norm
+
+@pytest.mark.parametrize("T,H", [(1, 128), (7, 7168), (300, 640)])
+def test_add_norm_writes_out_h_without_a_residual(dev, T, H):
+    """A buffer given for h receives x, also where h would be x itself, and is checked."""
+    x, w = randn(T, H, seed=T, dtype=BF16).to(dev), (1 + randn(H, seed=2, scale=0.2)).to(dev)
+    want = moe.add_norm(x, w)
+    h = torch.full_like(x, math.nan)
+    got = moe.add_norm(x, w, out=moe.Normed(h, None, None, None))
+    assert got.h is h and torch.equal(h, x)
+    assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:]))
+    only = moe.add_norm(x, w, bf16=False, fp8=False, out=moe.Normed(h.fill_(math.nan), None, None, None))
+    assert torch.equal(only.h, x) and only[1:] == (None, None, None)
+    same = moe.add_norm(x, w, out=moe.Normed(x, None, None, None))
+    assert same.h is x and torch.equal(same.y, want.y)
+    for bad in (h[:, : H - 1], h.float(), h.cpu()):
+        with pytest.raises(ValueError):
+            moe.add_norm(x, w, out=moe.Normed(bad, None, None, None))
+
+
 # ------------------------------------------------------------- gradients of the product
 
 @pytest.mark.parametrize("M,N,K,act,dtype", [
