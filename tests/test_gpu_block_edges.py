@@ -130,6 +130,47 @@ def test_balance_loss_of_rows_with_tiny_scores(dev, T, E, score):
     assert float(loss) == 0 and not bool(dl.any())
 
 
+def guarded(nbytes, dev):
+    """(device address of nbytes between guards, check): check fails where a guard byte
+    changed."""
+    room = torch.full((nbytes + 8192,), 0xA5, dtype=torch.uint8, device=dev)
+    start = 4096 + (-(room.data_ptr() + 4096)) % 256
+
+    def check(what):
+        assert bool((room[:start] == 0xA5).all()) and bool((room[start + nbytes:] == 0xA5).all()), what
+    return room.data_ptr() + start, check
+
+
+@pytest.mark.parametrize("T,E,B", [(100, 16, 3), (100, 30, 5), (100, 16, 300), (1000, 24, 2), (1000, 384, 40), (700, 600, 400)])
+@pytest.mark.parametrize("score", [0, 1, 2])
+def test_balance_loss_of_unordered_offsets_writes_its_buffers_only(dev, T, E, B, score):
+    """Every way to find a token's sequence, in one workgroup and in four launches, with
+    offsets that run up and down and past both ends: the values are unspecified, what lies
+    around the outputs and the workspace stays."""
+    g = torch.Generator().manual_seed(B)
+    l, ids = randn(T, E, seed=1).to(dev), torch.randint(-3, E + 3, (T, 4), generator=g, dtype=torch.int32).to(dev)
+    far = torch.tensor([2 ** 31 - 1, -2 ** 31, T + 1, -1], dtype=torch.int64)
+    d = moe.GateDims(T, E, 4, score, 0, 1, 1.0)
+    nbytes = moe.lib().moe_balance_loss_workspace_bytes(d, B)
+    for turn in range(4):
+        off = torch.randint(-50, T + 50, (B + 1,), generator=g)
+        if turn % 2:
+            at = torch.randint(0, B + 1, (3,), generator=g)
+            off[at] = far[torch.randint(0, 4, (3,), generator=g)]
+        if turn == 3:
+            off = off.flip(0).sort(descending=True).values
+        off = off.clamp(-2 ** 31, 2 ** 31 - 1).to(torch.int32).to(dev)
+        say(f"[balance unordered {T}x{E} B={B} score {score} turn {turn}]")
+        bufs = [guarded(n, dev) for n in (4, 4 * B * E, 4 * T * E, nbytes)]
+        torch.cuda.synchronize()
+        rc = moe.lib().moe_balance_loss(d, B, 1.0, l.data_ptr(), ids.data_ptr(), off.data_ptr(), bufs[0][0], bufs[1][0],
+                                        bufs[2][0], bufs[3][0] if nbytes else None, nbytes, None)
+        torch.cuda.synchronize()
+        assert rc == moe.MOE_OK
+        for (_, check), name in zip(bufs, ("loss", "counts", "d_logits", "ws")):
+            check(name)
+
+
 # ----------------------------------------------------------------------------------- gate
 
 FAR_BIASES = [1e3, -1e3, -1e4, -1e9, 1e9, -3e38, 3e38, -math.inf, math.inf, math.nan]
