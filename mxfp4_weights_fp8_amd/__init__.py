@@ -433,6 +433,10 @@ def _enqueue(name: str, dev: torch.device, *args):
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, _raw_stream(index))
+    if rc == MOE_EINVAL:     # name what no check of shapes and types shows
+        odd = [hex(a) for a in args if isinstance(a, int) and a >> 32 > 0 and a % 16]
+        if odd:
+            raise MoEError(rc, f"{name}: tensors start at 16-byte aligned addresses, {', '.join(odd)} is not one")
     if rc != MOE_OK:
         raise MoEError(rc, name)
 
@@ -617,7 +621,8 @@ def gate(logits: torch.Tensor, K: int, score: str = "softmax", bias: Optional[to
          topk_ids: Optional[torch.Tensor] = None, topk_weights: Optional[torch.Tensor] = None):
     """moe_gate on the current stream. logits: float32 or bf16 [T, E]; score: a key of
     SCORES; bias: optional float32 [E], added to the scores for the choice alone;
-    n_valid: optional int32 [1] on the device, rows from there on are padding. Returns
+    n_valid: optional int32 [1] on the device (16-byte aligned, as every tensor here: not any
+    element of a larger one), rows from there on are padding. Returns
     (topk_ids int32 [T, K], topk_weights float32 [T, K]), ready for plan and ffn; picks
     that do not exist have id -1 and weight 0."""
     dev = _first(logits, 2, "logits")

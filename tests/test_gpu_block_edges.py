@@ -222,3 +222,19 @@ def test_gate_is_not_slowed_by_far_biases(dev, score):
         t = us(far)
         say(f"[gate {score}] bias {far}: {t:.1f} us against {plain:.1f}")
         assert t < 3 * plain
+
+
+def test_unaligned_scalars_are_refused_by_name(dev):
+    """One counter out of several starts at any multiple of 4 bytes: the error says so."""
+    l, counters = randn(4, 8, seed=1).to(dev), torch.tensor([0, 4, 0, 0, 4], dtype=torch.int32, device=dev)
+    with pytest.raises(moe.MoEError, match="16-byte aligned") as e:
+        moe.gate(l, 2, n_valid=counters[1:2])
+    assert hex(counters[1:2].data_ptr()) in str(e.value)
+    ids, _ = moe.gate(l, 2, n_valid=counters[4:5])
+    with pytest.raises(moe.MoEError, match="16-byte aligned"):
+        moe.balance_loss(l, ids, 1.0, seq_offsets=counters[:2].clone().repeat(2)[2:])
+    with pytest.raises(moe.MoEError, match="16-byte aligned"):
+        moe.gate(l, 2, topk_weights=torch.empty(9, device=dev)[1:].view(4, 2))
+    with pytest.raises(moe.MoEError) as e:
+        moe.balance_loss(l, ids, math.nan)
+    assert "aligned" not in str(e.value)
