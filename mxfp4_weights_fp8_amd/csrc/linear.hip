@@ -159,6 +159,9 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a) {
 
 }  // namespace
 
+// Rows that k_linear_dot is built for.
+inline int dot_rows(int M) { return M == 1 ? 1 : M <= 4 ? 4 : 8; }
+
 // Tile shape and splits of the contraction: the least estimated time. Measured with
 // every CU busy, in 10 ns: a step of 64 takes `step` (two workgroups of the smallest
 // tile share a CU), prologue and epilogue `fixed` per round of tiles, and joining the
@@ -166,13 +169,18 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a) {
 // us, 128 x 128 971; 8191 x 7168 x 2048: 310 and 266; 4096 x 2048 x 7168: 256 x 256 split
 // in two 112, 128 x 128 110, unsplit 256 x 256 168.)
 LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain, bool two) {
-  // Few rows. The vector units up to 1536 columns: 7 x 384 x 7168 8.2 us against 10.2 us
-  // by kSmall, 8 x 1536 x 4096 8.5 against 10.1, but 8 x 2048 x 7168 14.9 against 10.7. Above
-  // 16 rows kSmall while its workgroups' reads of x, M N K / 8 bytes, stay small: 64 x 4096 x
+  // Few rows. The vector units (rows in ones, fours or eights) while their products take less
+  // time than what kSmall pays for its parts. In us, kDot and kSmall: at 384 columns 8 x 512
+  // 3.6 and 3.5, 8 x 1024 3.7 and 5.4, 8 x 7168 5.6 and 8.1, 8 x 16384 7.8 and 10.3; 8 rows x 1024 x
+  // 7168 8.8 and 9.5, x 1536 x 4096 7.5 and 8.3, x 2048 x 4096 8.9 and 8.7, x 1536 x 7168 13.4
+  // and 10.6; 4 x 384 x 256 3.0 and 2.8, 4 x 384 x 512 2.9 and 3.3, 4 x 1536 x 7168 8.0 and 10.0, 4 x
+  // 2048 x 7168 10.8 and 10.7; 1 x 384 x 128 2.4 and 2.5, 1 x 2048 x 16384 11.9 and 17.0. From 2560
+  // columns on kSmall needs no parts (8 x 2560 x 2048 6.4 and 5.9). Above 16 rows kSmall while its workgroups' reads of x, M N K / 8 bytes, stay small: 64 x 4096 x
   // 2048 11.8 us against 15.8 us in tiles, 64 x 7168 x 7168 75 against 30.
   if (l == Layout::kRows && (M <= 16 || (M <= 64 && (int64_t)M * N * C <= 800000000))) {
     const int64_t tiles = ceil_div(N, 16), steps = C / 64;
-    if (M <= 8 && N <= 1536) return LinearPlan{Path::kDot, 0, 0, 1};
+    const int64_t rows = dot_rows(M);
+    if (M <= 8 && N <= 2048 && C >= 128 * rows && rows * N * C <= 60000000) return LinearPlan{Path::kDot, 0, 0, 1};
     // fewer workgroups than CUs: split the contraction, at least 8 steps each
     int64_t splits = 256 / tiles;
     if (splits > steps / 8) splits = steps / 8;
@@ -224,15 +232,13 @@ hipError_t launch_linear_plan(const LinearArgs& in, const LinearPlan& p, Layout 
     const int64_t chunks = ceil_div(a.C, 512);
     const dim3 block(64 * (unsigned)(chunks < kDotWaves ? chunks : kDotWaves));
     auto run = [&](auto kernel, int r) { hipLaunchKernelGGL(kernel, dim3((unsigned)ceil_div(a.N, r)), block, 0, s, a); };
-    if (a.N <= 768) {   // 192 workgroups for 384 columns
-      if (a.M == 1) run(k_linear_dot<1, 2>, 2);
-      else if (a.M <= 4) run(k_linear_dot<4, 2>, 2);
-      else run(k_linear_dot<8, 2>, 2);
-    } else {
-      if (a.M == 1) run(k_linear_dot<1, 4>, 4);
-      else if (a.M <= 4) run(k_linear_dot<4, 4>, 4);
-      else run(k_linear_dot<8, 4>, 4);
-    }
+    // Two columns per workgroup; four where two would come to more than 256 workgroups of
+    // long rows (8 x 768 x 7168 8.1 us against 9.4, 8 x 768 x 4096 5.8 against 5.6).
+    const int rows = dot_rows(a.M);
+    if (rows == 1) run(k_linear_dot<1, 2>, 2);
+    else if (rows == 4) run(k_linear_dot<4, 2>, 2);
+    else if (a.N <= 512 || a.C <= 4096) run(k_linear_dot<8, 2>, 2);
+    else run(k_linear_dot<8, 4>, 4);
     return hipGetLastError();
   }
   if (p.path == Path::kSmall) {

@@ -11,7 +11,7 @@ import torch
 import mxfp4_weights_fp8_amd as moe
 from gpu_helpers import say
 from oracle import block as ob
-from test_gpu_block import BF, BF16, F32, F64, SCORES, U, check_balance, check_gate, dev, on, randn, within  # noqa: F401
+from test_gpu_block import BF, BF16, F32, F64, SCORES, U, check_balance, check_gate, check_linear, dev, on, randn, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -82,6 +82,13 @@ def test_linear_grad_of_infinities_and_far_values(dev):
     assert bool(torch.isfinite(dx[rows]).all()) and bool(torch.isfinite(dw[cols]).all())
     rdx = ob.linear_grad_ref(dy[rows], x[rows], w)[0]
     within(dx[rows], rdx, rdx.abs() * BF + (dy[rows].abs().to(F64) @ w.to(F64)) * 2.0 ** -14, "dx")
+
+
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 8])
+@pytest.mark.parametrize("N,K", [(384, 128), (17, 512), (385, 1024), (769, 7168), (512, 7168), (1024, 4096), (2048, 3584),
+                                 (2047, 1024), (2049, 1024), (3, 65536), (1500, 8192)])
+def test_linear_of_few_rows_on_both_sides_of_the_choice(dev, M, N, K):
+    check_linear(dev, M, N, K, dtype=F32 if N % 2 else BF16, bias=K < 4096, res=N == 385, seed=M + N)
 
 
 def test_sigmoid_slope_keeps_its_digits(dev):
