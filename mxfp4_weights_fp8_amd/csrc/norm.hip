@@ -9,7 +9,7 @@
 // HBM-bound: a row is read once and kept in registers between the sum of squares
 // and the outputs. A lane's vector is 8 columns, so 16 lanes hold one 128-column
 // block and its amax is a 16-lane butterfly. 32768 x 7168 with residual and all outputs
-// (2.1 GB) 350-380 us, 5.6-6.0 TB/s; 7 x 7168 5 us, bound by the launch.
+// (2.1 GB) 380 us, 5.6 TB/s; 7 x 7168 5 us, bound by the launch.
 #include "device_common.h"
 #include "host_internal.h"
 #include "lane_reduce.h"
@@ -83,9 +83,13 @@ __device__ __forceinline__ void sum_over_row(float (&s)[N], float* red) {
   }
 }
 
-// Loads and stores of the row tensors. NT: nontemporal, for tensors that do not fit the
-// 256 MB last-level cache anyway (32768 x 7168: 336 us against 387 us; 4096 x 7168, whose
-// outputs stay cached for the next kernel: 49 against 47 us).
+// Loads and stores of the row tensors. NT: nontemporal, for tensors that the 256 MB
+// last-level cache does not hold from one kernel to the next. add_norm nontemporal and
+// cached, in us, three sets of tensors in turn, and in brackets with the router's product
+// behind it: at H 7168 8 M elements 16 and 13 (40 and 37), 16 M 31 and 36 (59 and 61), 32 M 55
+// and 61 (98 and 105), 64 M 101 and 114 (180 and 189), 235 M 382 and 390; at H 1024 8 M 14 and
+// 12 (31 and 27), 16 M 26 and 31 (49 and 50), 64 M 90 and 104 (167 and 180). Its gradient:
+// 8 M 26 and 20, 16 M 36 and 35, 32 M 61 and 62, 64 M 106 and 112; at H 1024 16 M 33 and 35.
 template <bool NT>
 __device__ __forceinline__ v4i load_row(const uint16_t* p) {
   return NT ? load16_nt(p) : load16(p);
@@ -95,7 +99,7 @@ __device__ __forceinline__ void store_row(uint16_t* p, const v4i v) {
   if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(p));
   else *reinterpret_cast<v4i*>(p) = v;
 }
-inline bool past_cache(int T, int H) { return (int64_t)T * H > 50000000; }
+inline bool past_cache(int T, int H) { return (int64_t)T * H > 16000000; }
 
 struct NormArgs {
   const uint16_t* x;
