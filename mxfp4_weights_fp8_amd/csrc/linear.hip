@@ -169,14 +169,15 @@ inline int dot_rows(int M) { return M == 1 ? 1 : M <= 4 ? 4 : 8; }
 // us, 128 x 128 971; 8191 x 7168 x 2048: 310 and 266; 4096 x 2048 x 7168: 256 x 256 split
 // in two 112, 128 x 128 110, unsplit 256 x 256 168.)
 LinearPlan linear_plan(int M, int N, int C, Layout l, bool plain, bool two) {
-  // Few rows. The vector units (rows in ones, fours or eights) while their products take less
-  // time than what kSmall pays for its parts. In us, kDot and kSmall: at 384 columns 8 x 512
-  // 3.6 and 3.5, 8 x 1024 3.7 and 5.4, 8 x 7168 5.6 and 8.1, 8 x 16384 7.8 and 10.3; 8 rows x 1024 x
-  // 7168 8.8 and 9.5, x 1536 x 4096 7.5 and 8.3, x 2048 x 4096 8.9 and 8.7, x 1536 x 7168 13.4
-  // and 10.6; 4 x 384 x 256 3.0 and 2.8, 4 x 384 x 512 2.9 and 3.3, 4 x 1536 x 7168 8.0 and 10.0, 4 x
-  // 2048 x 7168 10.8 and 10.7; 1 x 384 x 128 2.4 and 2.5, 1 x 2048 x 16384 11.9 and 17.0. From 2560
-  // columns on kSmall needs no parts (8 x 2560 x 2048 6.4 and 5.9). Above 16 rows kSmall while its workgroups' reads of x, M N K / 8 bytes, stay small: 64 x 4096 x
-  // 2048 11.8 us against 15.8 us in tiles, 64 x 7168 x 7168 75 against 30.
+  // Few rows. The vector units (rows in ones, fours or eights) while their products take
+  // less time than what kSmall pays for its parts. In us, kDot and kSmall: at 384 columns
+  // 8 x 512 3.6 and 3.5, 8 x 1024 3.7 and 5.4, 8 x 7168 5.6 and 8.1, 8 x 16384 7.8 and 10.3; 8
+  // rows x 1024 x 7168 8.8 and 9.5, x 1536 x 4096 7.5 and 8.3, x 2048 x 4096 8.9 and 8.7, x
+  // 1536 x 7168 13.4 and 10.6; 4 x 384 x 256 3.0 and 2.8, 4 x 384 x 512 2.9 and 3.3, 4 x 1536
+  // x 7168 8.0 and 10.0, 4 x 2048 x 7168 10.8 and 10.7; 1 x 384 x 128 2.4 and 2.5, 1 x 2048 x
+  // 16384 11.9 and 17.0. From 2560 columns on kSmall needs no parts (8 x 2560 x 2048 6.4 and
+  // 5.9). Above 16 rows kSmall while its workgroups' reads of x, M N K / 8 bytes, stay small:
+  // 64 x 4096 x 2048 11.8 us against 15.8 us in tiles, 64 x 7168 x 7168 75 against 30.
   if (l == Layout::kRows && (M <= 16 || (M <= 64 && (int64_t)M * N * C <= 800000000))) {
     const int64_t tiles = ceil_div(N, 16), steps = C / 64;
     const int64_t rows = dot_rows(M);

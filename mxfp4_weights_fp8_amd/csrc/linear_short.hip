@@ -4,10 +4,10 @@
 //
 // A workgroup keeps 256 rows of x in registers (128 of an x in two parts), 64 (32) per wave
 // and the whole contraction (at C = 384 192 registers, in the AGPR file as the MFMAs'
-// second operand), and walks a run of 128-column tiles. Only w goes through LDS: a ring of kRing one-step stages
-// (64 x 128) that runs on across the tiles, so that the next tile's columns arrive
-// during the epilogue. Per 256 x 128 outputs 96 KB are copied, against 4 x 192 KB for
-// the same outputs in 128 x 128 tiles.
+// second operand), and walks a run of 128-column tiles. Only w goes through LDS: a ring
+// of kRing one-step stages (64 x 128) that runs on across the tiles, so that the next
+// tile's columns arrive during the epilogue. Per 256 x 128 outputs 96 KB are copied,
+// against 4 x 192 KB for the same outputs in 128 x 128 tiles.
 //
 // Step g (tile g / KS, step g % KS): the MFMAs of its first half and the reads of its
 // second; wait for this wave's copies of step g + 1 and barrier, which frees g's stage;

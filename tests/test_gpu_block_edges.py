@@ -11,7 +11,7 @@ import torch
 import mxfp4_weights_fp8_amd as moe
 from gpu_helpers import say
 from oracle import block as ob
-from test_gpu_block import BF, BF16, F32, F64, SCORES, U, check_balance, check_gate, check_linear, dev, on, randn, within  # noqa: F401
+from test_gpu_block import BF, BF16, F32, F64, SCORES, U, check_balance, check_gate, check_linear, dev, on, randn, room, tail_rows, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -82,6 +82,20 @@ def test_linear_grad_of_infinities_and_far_values(dev):
     assert bool(torch.isfinite(dx[rows]).all()) and bool(torch.isfinite(dw[cols]).all())
     rdx = ob.linear_grad_ref(dy[rows], x[rows], w)[0]
     within(dx[rows], rdx, rdx.abs() * BF + (dy[rows].abs().to(F64) @ w.to(F64)) * 2.0 ** -14, "dx")
+
+
+def test_linear_grad_in_two_parts_past_32_bits(dev, room):
+    """dz's high and low parts at offsets past 2^32 bytes, read along its rows and transposed."""
+    M, N, K, n = 1048579, 2056, 128, 70
+    x, w, dy = randn(n, K, seed=1, dtype=BF16), randn(N, K, seed=2, scale=0.1, dtype=BF16), randn(n, N, seed=3)
+    say(f"[linear_grad {M}x{N}x{K} float32]")
+    dx, dw, db = moe.linear_grad(tail_rows(dev, M, N, dy, dtype=F32), tail_rows(dev, M, K, x, fill=1.0), w.to(dev))
+    rdx, rdw, rdb, dz = ob.linear_grad_ref(dy, x, w)
+    ax, aw = dz.abs() @ w.to(F64).abs(), dz.abs().t() @ x.to(F64).abs()
+    within(dx[-n:], rdx, rdx.abs() * BF + ax * (2.0 ** -15 + (2 * N / 32 + 64) * 2 * U), "dx")
+    assert not bool(dx[:1000].any())
+    within(dw, rdw, rdw.abs() * BF + aw * (2.0 ** -15 + (2 * n / 32 + 64) * 2 * U), "dw")
+    within(db, rdb, dz.abs().sum(0) * (n + 64) * U, "dbias")
 
 
 @pytest.mark.parametrize("M", [1, 2, 4, 5, 8])
