@@ -89,7 +89,8 @@ __device__ __forceinline__ void sum_over_row(float (&s)[N], float* red) {
 // behind it: at H 7168 8 M elements 16 and 13 (40 and 37), 16 M 31 and 36 (59 and 61), 32 M 55
 // and 61 (98 and 105), 64 M 101 and 114 (180 and 189), 235 M 382 and 390; at H 1024 8 M 14 and
 // 12 (31 and 27), 16 M 26 and 31 (49 and 50), 64 M 90 and 104 (167 and 180). Its gradient:
-// 8 M 26 and 20, 16 M 36 and 35, 32 M 61 and 62, 64 M 106 and 112; at H 1024 16 M 33 and 35.
+// 8 M 26 and 20, 16 M 36 and 35, 29 M 58 and 56, 32 M 61 and 62, 64 M 106 and 112; at H 1024
+// 16 M 33 and 35, 32 M 53 and 58.
 template <bool NT>
 __device__ __forceinline__ v4i load_row(const uint16_t* p) {
   return NT ? load16_nt(p) : load16(p);
@@ -99,7 +100,7 @@ __device__ __forceinline__ void store_row(uint16_t* p, const v4i v) {
   if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(p));
   else *reinterpret_cast<v4i*>(p) = v;
 }
-inline bool past_cache(int T, int H) { return (int64_t)T * H > 16000000; }
+constexpr int64_t kCached = 16000000, kCachedGrad = 32000000;   // elements of a row tensor
 
 struct NormArgs {
   const uint16_t* x;
@@ -365,7 +366,7 @@ __global__ __launch_bounds__(256) void k_fill_zero(int32_t* p, int64_t n) {
 hipError_t launch_add_norm(const uint16_t* x, const uint16_t* res, const void* w, bool w_f32, uint16_t* h,
                            uint16_t* y, uint8_t* x_q, uint8_t* x_s, int T, int H, float eps, hipStream_t s) {
   const NormArgs a{x, res, w, h, y, x_q, x_s, T, H, eps};
-  by_kind(w_f32, past_cache(T, H), [&](auto f, auto nt) { launch_fwd<decltype(f)::value, decltype(nt)::value>(a, s); });
+  by_kind(w_f32, (int64_t)T * H > kCached, [&](auto f, auto nt) { launch_fwd<decltype(f)::value, decltype(nt)::value>(a, s); });
   return hipGetLastError();
 }
 
@@ -380,7 +381,8 @@ hipError_t launch_add_norm_grad(const uint16_t* dy, const uint16_t* h, const voi
   const int n = norm_grad_parts(T, H);
   if (n > 0) {
     const NormGradArgs a{dy, h, w, dh, dx, n == 1 ? dw : parts, T, H, eps};   // one part is the result
-    by_kind(w_f32, past_cache(T, H), [&](auto f, auto nt) { launch_grad<decltype(f)::value, decltype(nt)::value>(a, n, s); });
+    by_kind(w_f32, (int64_t)T * H > kCachedGrad,
+            [&](auto f, auto nt) { launch_grad<decltype(f)::value, decltype(nt)::value>(a, n, s); });
   }
   return n == 1 ? hipGetLastError() : launch_sum_parts(parts, n, H, dw, s);
 }

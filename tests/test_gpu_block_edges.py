@@ -11,7 +11,7 @@ import torch
 import mxfp4_weights_fp8_amd as moe
 from gpu_helpers import say
 from oracle import block as ob
-from test_gpu_block import BF, BF16, F32, F64, SCORES, U, check_balance, check_gate, check_linear, dev, on, randn, room, tail_rows, within  # noqa: F401
+from test_gpu_block import BF, BF16, F32, F64, SCORES, U, check_balance, check_gate, check_linear, check_normed, dev, on, randn, room, tail_rows, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -34,6 +34,23 @@ def test_add_norm_writes_out_h_without_a_residual(dev, T, H):
     for bad in (h[:, : H - 1], h.float(), h.cpu()):
         with pytest.raises(ValueError):
             moe.add_norm(x, w, out=moe.Normed(bad, None, None, None))
+
+
+@pytest.mark.parametrize("T,H", [(127000, 128), (9001, 1920), (2300, 7168), (979, 16384)])
+def test_add_norm_past_the_cache(dev, T, H):
+    """Tensors that are loaded and stored nontemporally, at every kind of row; the last rows
+    and the whole in place."""
+    x, res = randn(T, H, seed=1, dtype=BF16), randn(T, H, seed=2, scale=3.0, dtype=BF16)
+    w = 1 + randn(H, seed=5, scale=0.3)
+    xd, rd, wd = on(dev, x, res, w)
+    say(f"[add_norm {T}x{H}]")
+    out = moe.add_norm(xd, wd, residual=rd, eps=1e-5)
+    for part in (slice(0, 40), slice(T - 40, T)):
+        check_normed(moe.Normed(*(t[part] for t in out)), x[part], w, res[part], 1e-5, "rows")
+    alone = moe.add_norm(xd[: T // 2], wd, residual=rd[: T // 2], eps=1e-5)     # half the rows: cached
+    assert all(torch.equal(a, b[: T // 2]) for a, b in zip(alone, out))
+    moe.add_norm(xd, wd, rd, 1e-5, out=moe.Normed(rd, xd, None, None))
+    assert torch.equal(rd, out.h) and torch.equal(xd, out.y)
 
 
 # ------------------------------------------------------------- gradients of the product
