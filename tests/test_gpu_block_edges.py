@@ -62,6 +62,8 @@ def test_add_norm_past_the_cache(dev, T, H):
     # the tile shapes, the contraction split and not
     (128, 1000, 8192, "none", F32), (128, 12001, 1024, "none", F32), (2048, 16500, 768, "none", F32),
     (1000, 500, 8192, "silu", BF16), (12000, 500, 1024, "none", F32), (16500, 2000, 768, "none", F32),
+    # the most columns, the longest rows
+    (3, 65536, 128, "none", F32), (70, 65529, 256, "silu", BF16), (5, 20, 65536, "none", F32),
     # short contractions over 128, 256 and 384 columns of dz
     (5003, 100, 8064, "none", F32), (5001, 200, 8064, "silu", BF16), (4997, 300, 8064, "none", F32), (20001, 384, 1152, "none", F32)])
 def test_linear_grad_keeps_dz(dev, M, N, K, act, dtype):
@@ -163,6 +165,7 @@ def test_balance_loss_of_rows_with_tiny_scores(dev, T, E, score):
     say(f"[balance {T}x{E} {score}]")
     for logits in (l, l.to(BF16)):
         check_balance(dev, logits, ids, 0.3, score, None, "tiny scores")
+        check_balance(dev, logits, ids, 0.3, score, [1, T // 3, T // 3, T - 1], "tiny scores, sequences")
     l[:] = -800.0                                  # below the documented end: no probabilities
     loss, _, dl = moe.balance_loss(*on(dev, l, ids), 0.3, score=score)
     assert float(loss) == 0 and not bool(dl.any())
