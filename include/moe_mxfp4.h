@@ -432,6 +432,115 @@ int moe_balance_loss(const moe_gate_dims* dims, int32_t B, float alpha, const vo
                      const int32_t* seq_offsets, float* loss, int32_t* counts, float* d_logits, void* ws,
                      size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------
+ * Training the experts: tokens laid out by expert and brought back, the experts'
+ * products with bf16 weights, the gated activation between them with its input saved in
+ * 8 bits, and the gradients of all of them. The route is moe_plan's: rows are its
+ * positions in sorted_pairs, expert e has rows [expert_offsets[e], expert_offsets[e + 1]),
+ * and pair p = t K + j has row pair_rows[p], or none (-1: dropped). Rows from
+ * expert_offsets[E] on belong to nobody: they are not read, and left as they were where
+ * rows are written. The conventions of the section above hold (16-byte aligned pointers,
+ * contiguous rows, T at most 2^21); T K and the rows are at most 2^27. Buffers overlap
+ * only where an entry says so. */
+
+/* rows[pair_rows[t K + j]] = x[t] for every pick that was not dropped.
+ *   T, H, K    T >= 0; H a multiple of 8 (of 128 with x_s), at most 16384; K 1..64
+ *   x          [T, H] bf16, or with x_s E4M3 codes (moe_add_norm's or moe_quant_act's, kept
+ *              from the forward pass in place of the bf16 tensor)
+ *   x_s        [T, H/128] E8M0 scales of the codes, NULL: x is bf16
+ *   rows       [T K, H] bf16 out (the codes' values are exact in bf16)
+ * Its gradient is moe_return_rows without weights.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP. */
+int moe_sort_rows(int32_t T, int32_t H, int32_t K, const void* x, const uint8_t* x_s, const int32_t* pair_rows,
+                  uint16_t* rows, void* stream);
+
+/* The values of saved codes, x[t] = E4M3(x_q[t]) * scale, as bf16 [T, H] (moe_linear_grad's
+ * x, from what moe_add_norm wrote). H a multiple of 128. Exact, but for magnitudes outside
+ * bf16's range: 2^128 (what codes of values from 1.9375 * 2^127 on stand for) is infinite.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP. */
+int moe_restore_act(int32_t T, int32_t H, const uint8_t* x_q, const uint8_t* x_s, uint16_t* x, void* stream);
+
+/* y[t] = sum over the picks j that were not dropped, in order, of weights[t, j] *
+ * rows[pair_rows[t K + j]], plus add[t]; summed in fp32.
+ *   T, H, K    as in moe_sort_rows (H a multiple of 8)
+ *   rows       [T K, H] bf16
+ *   weights    [T, K] fp32, NULL: 1
+ *   add        [T, H] of y's type, NULL: none; may be y
+ *   y          [T, H] of `type` (MOE_TYPE_*) out; a token without picks gets add, or 0
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP. */
+int moe_return_rows(int32_t T, int32_t H, int32_t K, const uint16_t* rows, const int32_t* pair_rows,
+                    const float* weights, const void* add, int32_t type, void* y, void* stream);
+
+/* Gradient of moe_return_rows (add's is dy):
+ *   dy         [T, H] of `type`
+ *   rows       [T K, H] bf16 as in the call (not read without d_weights)
+ *   weights    as in the call
+ *   d_rows     [T K, H] bf16 out: weights[t, j] * dy[t]; may be rows; NULL: not computed
+ *   d_weights  [T, K] fp32 out: the dot product of dy[t] with the pick's row, 0 for a
+ *              dropped pick (moe_gate_grad's d_weights); NULL: not computed
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP. */
+int moe_return_rows_grad(int32_t T, int32_t H, int32_t K, const void* dy, int32_t type, const uint16_t* rows,
+                         const int32_t* pair_rows, const float* weights, uint16_t* d_rows, float* d_weights,
+                         void* stream);
+
+/* The experts' products, y[r] = w[e] x[r] for the rows r of expert e.
+ *   P rows (>= 0), N outputs and K inputs (multiples of 128, at most 65536, N * K below
+ *   2^31), E experts (1..4096)
+ *   type  of y (moe_expert_linear) or of dw (moe_expert_linear_grad): MOE_TYPE_* */
+typedef struct moe_expert_dims {
+  int32_t P, N, K, E;
+  int32_t type;
+} moe_expert_dims;
+
+/*   x [P, K] bf16, w [E, N, K] bf16, expert_offsets [E + 1] int32 on the device, ascending
+ *     within [0, P] (else the results are unspecified, but nothing outside the buffers is
+ *     touched)
+ *   y [P, N] of `type` out
+ *   ws  at least moe_expert_linear_workspace_bytes bytes (0 for few rows: ws may be NULL)
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP. */
+size_t moe_expert_linear_workspace_bytes(const moe_expert_dims* dims);
+int moe_expert_linear(const moe_expert_dims* dims, const uint16_t* x, const uint16_t* w, const int32_t* expert_offsets,
+                      void* y, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient: dx[r] = w[e]^T dy[r]; dw[e] = sum over the rows r of e of dy[r] x[r]^T, 0
+ * for an expert without rows.
+ *   dy [P, N] bf16, x (not read without dw) and w (not read without dx) as in the call
+ *   dx [P, K] bf16 out, dw [E, N, K] of `type` out; either may be NULL (not computed)
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP. */
+size_t moe_expert_linear_grad_workspace_bytes(const moe_expert_dims* dims);
+int moe_expert_linear_grad(const moe_expert_dims* dims, const uint16_t* dy, const uint16_t* x, const uint16_t* w,
+                           const int32_t* expert_offsets, uint16_t* dx, void* dw, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* The gated activation between an expert's products: z[r] = (g, u), two halves of I
+ * columns; h = act(g) u.
+ *   R rows (>= 0), I a multiple of 128, at most 16384; act one of MOE_ACT_* (silu is the
+ *   FFN's); E experts (0..4096): with E > 0 the rows from expert_offsets[E] on belong to
+ *   nobody, with E == 0 all R count (expert_offsets is not read) */
+typedef struct moe_glu_dims {
+  int32_t R, I, E;
+  int32_t act;
+} moe_glu_dims;
+
+/*   z [R, 2I] bf16, h [R, I] bf16 out
+ *   z_q, z_s  [R, 2I] E4M3 codes and [R, 2I/128] E8M0 scales of z out (the rule of
+ *             moe_quant_act), all that the gradient needs of z; both NULL: not written.
+ *             A block of 128 columns with an infinity or NaN gets unspecified codes.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP. */
+int moe_glu(const moe_glu_dims* dims, const uint16_t* z, const int32_t* expert_offsets, uint16_t* h, uint8_t* z_q,
+            uint8_t* z_s, void* stream);
+
+/* Its gradient, at the values that the codes stand for, or at z itself:
+ *   dz = (dh u act'(g), dh act(g))
+ *   dh        [R, I] bf16
+ *   z         [R, 2I] bf16, or NULL with z_q and z_s from moe_glu (one of the two)
+ *   dz        [R, 2I] bf16 out; may be z
+ *   h         [R, I] bf16 out: act(g) u at the same values, for the second product's dw;
+ *             may be dh; NULL: not written
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP. */
+int moe_glu_grad(const moe_glu_dims* dims, const uint16_t* dh, const uint16_t* z, const uint8_t* z_q,
+                 const uint8_t* z_s, const int32_t* expert_offsets, uint16_t* dz, uint16_t* h, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* moe_status_string(int code);
 

@@ -21,6 +21,17 @@ In front of the FFN, each with its gradient as an explicit call:
     gate(logits, K)                       -> topk_ids, topk_weights    (moe_gate)
     gate_grad(logits, topk_ids, d_weights) -> d_logits                 (moe_gate_grad)
     balance_loss(logits, topk_ids, alpha) -> loss, counts, d_logits    (moe_balance_loss)
+
+Training the experts (bf16 weights), along a plan:
+
+    sort_rows(x, p)                       -> rows by expert            (moe_sort_rows)
+    expert_linear(rows, w, p)             -> y                         (moe_expert_linear)
+    glu(z)                                -> h, z_q, z_s               (moe_glu: z saved in 8 bits)
+    return_rows(rows, p, weights)         -> y by token                (moe_return_rows)
+    return_rows_grad(dy, rows, p, weights) -> d_rows, d_weights        (moe_return_rows_grad)
+    glu_grad(dh, z_q, z_s)                -> dz, h                     (moe_glu_grad)
+    expert_linear_grad(dy, rows, w, p)    -> dx, dw                    (moe_expert_linear_grad)
+    sort_rows(x_q, p, scales=x_s), restore_act(x_q, x_s)               (rows, tokens from add_norm's codes)
 """
 
 from __future__ import annotations
@@ -84,6 +95,15 @@ class GateDims(ctypes.Structure):
                 ("renorm", ctypes.c_int32), ("logits_type", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class ExpertDims(ctypes.Structure):
+    _fields_ = [("P", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("type", ctypes.c_int32)]
+
+
+class GluDims(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("I", ctypes.c_int32), ("E", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
 #: MOE_TYPE_*, MOE_ACT_* and MOE_SCORE_* by what the functions below take
 TYPES = {torch.bfloat16: 0, torch.float32: 1}
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}
@@ -123,6 +143,20 @@ _SIGNATURES = {
     "moe_balance_loss_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(GateDims), ctypes.c_int32]),
     "moe_balance_loss": (ctypes.c_int, [ctypes.POINTER(GateDims), ctypes.c_int32, ctypes.c_float] +
                          [ctypes.c_void_p] * 7 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_sort_rows": (ctypes.c_int, [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 5),
+    "moe_restore_act": (ctypes.c_int, [ctypes.c_int32] * 2 + [ctypes.c_void_p] * 4),
+    "moe_return_rows": (ctypes.c_int, [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 4 + [ctypes.c_int32] +
+                        [ctypes.c_void_p] * 2),
+    "moe_return_rows_grad": (ctypes.c_int, [ctypes.c_int32] * 3 + [ctypes.c_void_p, ctypes.c_int32] +
+                             [ctypes.c_void_p] * 6),
+    "moe_expert_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(ExpertDims)]),
+    "moe_expert_linear": (ctypes.c_int, [ctypes.POINTER(ExpertDims)] + [ctypes.c_void_p] * 5 +
+                          [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_expert_linear_grad_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(ExpertDims)]),
+    "moe_expert_linear_grad": (ctypes.c_int, [ctypes.POINTER(ExpertDims)] + [ctypes.c_void_p] * 7 +
+                               [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_glu": (ctypes.c_int, [ctypes.POINTER(GluDims)] + [ctypes.c_void_p] * 6),
+    "moe_glu_grad": (ctypes.c_int, [ctypes.POINTER(GluDims)] + [ctypes.c_void_p] * 8),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 
@@ -686,3 +720,202 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, alpha: float, sco
              _tensor(seq_offsets, torch.int32, (B + 1,), dev, "seq_offsets"), loss.data_ptr(), counts.data_ptr(),
              d_logits.data_ptr(), *_ws_args(ws))
     return loss, counts, d_logits
+
+
+# ------------------------------------------------------------------ training the experts
+
+BF16 = torch.bfloat16
+
+
+def _pairs(p: Plan, dev):
+    """(T, K, address of pair_rows) of a plan."""
+    d = p.dims
+    T, K = d.T, d.K
+    return T, K, _tensor(p.pair_rows, torch.int32, (max(T * K, 1),), dev, "pair_rows")
+
+
+def _offsets(p: Plan, dev):
+    """(rows, experts, address of expert_offsets) of a plan."""
+    d = p.dims
+    return d.T * d.K, d.E, _tensor(p.expert_offsets, torch.int32, (d.E + 1,), dev, "expert_offsets")
+
+
+def sort_rows(x: torch.Tensor, p: Plan, scales: Optional[torch.Tensor] = None,
+              rows: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_sort_rows on the current stream: the rows of the plan's experts, bf16 [T K, H].
+    x: bf16 [T, H], or with scales (uint8 [T, H/128]) uint8 E4M3 codes as add_norm or
+    quant_act gave them. rows: optional tensor to write. Rows behind the last expert's are
+    left as they were (uninitialised in a new tensor). Its gradient is return_rows."""
+    dev = _first(x, 2, "x")
+    T, K, pr = _pairs(p, dev)
+    H = x.shape[1]
+    if rows is None:
+        rows = _new(T * K, H, BF16, dev)
+    _enqueue("moe_sort_rows", dev, T, H, K, _tensor(x, BF16 if scales is None else torch.uint8, (T, H), dev, "x"),
+             _tensor(scales, torch.uint8, (T, H // 128), dev, "scales"), pr, _tensor(rows, BF16, (T * K, H), dev, "rows"))
+    return rows
+
+
+def restore_act(x_q: torch.Tensor, x_s: torch.Tensor) -> torch.Tensor:
+    """moe_restore_act on the current stream: bf16 [T, H] values of E4M3 codes x_q uint8
+    [T, H] and E8M0 scales x_s uint8 [T, H/128], as add_norm or quant_act gave them."""
+    dev = _first(x_q, 2, "x_q")
+    T, H = x_q.shape
+    x = _new(T, H, BF16, dev)
+    _enqueue("moe_restore_act", dev, T, H, _tensor(x_q, torch.uint8, (T, H), dev, "x_q"),
+             _tensor(x_s, torch.uint8, (T, H // 128), dev, "x_s"), x.data_ptr())
+    return x
+
+
+def return_rows(rows: torch.Tensor, p: Plan, weights: Optional[torch.Tensor] = None,
+                add: Optional[torch.Tensor] = None, dtype: torch.dtype = BF16,
+                y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_return_rows on the current stream: [T, H] of dtype (torch.bfloat16 or
+    torch.float32), the sum over a token's picks of weights float32 [T, K] (default: 1)
+    times their rows (bf16 [T K, H] in the plan's order), plus add ([T, H] of dtype). y:
+    optional tensor to write (may be add)."""
+    dev = _first(rows, 2, "rows")
+    T, K, pr = _pairs(p, dev)
+    H = rows.shape[1]
+    t = _one_of(TYPES, dtype, "dtype")
+    if y is None:
+        y = _new(T, H, dtype, dev)
+    _enqueue("moe_return_rows", dev, T, H, K, _tensor(rows, BF16, (T * K, H), dev, "rows"), pr,
+             _tensor(weights, torch.float32, (T, K), dev, "weights"), _tensor(add, dtype, (T, H), dev, "add"), t,
+             _tensor(y, dtype, (T, H), dev, "y"))
+    return y
+
+
+def return_rows_grad(dy: torch.Tensor, rows: Optional[torch.Tensor], p: Plan, weights: Optional[torch.Tensor] = None,
+                     need=(True, True), d_rows: Optional[torch.Tensor] = None):
+    """moe_return_rows_grad on the current stream. dy: bf16 or float32 [T, H]; rows and
+    weights as in return_rows (rows may be None where d_weights is not needed). Returns
+    (d_rows bf16 [T K, H], d_weights float32 [T, K], gate_grad's), None where not needed.
+    d_rows: optional tensor to write (may be rows); rows behind the last expert's are left
+    as they were."""
+    dev = _first(dy, 2, "dy")
+    T, K, pr = _pairs(p, dev)
+    H = dy.shape[1]
+    t = _one_of(TYPES, dy.dtype, "dy type")
+    if not need[0]:
+        d_rows = None
+    elif d_rows is None:
+        d_rows = _new(T * K, H, BF16, dev)
+    dw = _new(T, K, torch.float32, dev) if need[1] else None
+    _enqueue("moe_return_rows_grad", dev, T, H, K, _tensor(dy, dy.dtype, (T, H), dev, "dy"), t,
+             _tensor(rows, BF16, (T * K, H), dev, "rows"), pr,
+             _tensor(weights, torch.float32, (T, K), dev, "weights"),
+             _tensor(d_rows, BF16, (T * K, H), dev, "d_rows"), dw.data_ptr() if need[1] else None)
+    return d_rows, dw
+
+
+def expert_linear(x: torch.Tensor, w: torch.Tensor, p: Plan, dtype: torch.dtype = BF16,
+                  y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_expert_linear on the current stream: y[r] = w[e] x[r] for the plan's rows r of
+    expert e. x: bf16 [T K, K'] (sort_rows's); w: bf16 [E, N, K']; y: [T K, N] of dtype
+    (torch.bfloat16 or torch.float32), optionally a tensor to write; rows behind the last
+    expert's are left as they were (uninitialised in a new tensor)."""
+    dev = _first(x, 2, "x")
+    _first(w, 3, "w")
+    P, E, off = _offsets(p, dev)
+    N, K = w.shape[1:]
+    d = ExpertDims(P, N, K, E, _one_of(TYPES, dtype, "dtype"))
+    if y is None:
+        y = _new(P, N, dtype, dev)
+    ws = _workspace(lib().moe_expert_linear_workspace_bytes(d), dev, ws)
+    _enqueue("moe_expert_linear", dev, d, _tensor(x, BF16, (P, K), dev, "x"), _tensor(w, BF16, (E, N, K), dev, "w"),
+             off, _tensor(y, dtype, (P, N), dev, "y"), *_ws_args(ws))
+    return y
+
+
+def expert_linear_grad(dy: torch.Tensor, x: Optional[torch.Tensor], w: Optional[torch.Tensor], p: Plan,
+                       need=(True, True), dtype: torch.dtype = BF16, dx: Optional[torch.Tensor] = None,
+                       dw: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """moe_expert_linear_grad on the current stream. dy: bf16 [T K, N]; x, w as in
+    expert_linear (x may be None where dw is not needed, w where dx is not). Returns (dx
+    bf16 [T K, K'], dw [E, N, K'] of dtype, zero for an expert without rows), None where
+    not needed; dx, dw: optional tensors to write (rows of dx behind the last expert's are
+    left as they were)."""
+    dev = _first(dy, 2, "dy")
+    P, E, off = _offsets(p, dev)
+    N = dy.shape[1]
+    if w is not None:
+        _first(w, 3, "w")
+    elif x is None or need[0]:
+        raise ValueError("w: needed for dx, and one of x and w for the sizes")
+    else:
+        _first(x, 2, "x")
+    K = w.shape[2] if w is not None else x.shape[1]
+    d = ExpertDims(P, N, K, E, _one_of(TYPES, dtype, "dtype"))
+    if not need[0]:
+        dx = None
+    elif dx is None:
+        dx = _new(P, K, BF16, dev)
+    if not need[1]:
+        dw = None
+    elif dw is None:
+        dw = torch.empty_strided((E, N, K), (N * K, K, 1), dtype=dtype, device=dev)
+    ws = _workspace(lib().moe_expert_linear_grad_workspace_bytes(d), dev, ws)
+    _enqueue("moe_expert_linear_grad", dev, d, _tensor(dy, BF16, (P, N), dev, "dy"), _tensor(x, BF16, (P, K), dev, "x"),
+             _tensor(w, BF16, (E, N, K), dev, "w"), off, _tensor(dx, BF16, (P, K), dev, "dx"),
+             _tensor(dw, dtype, (E, N, K), dev, "dw"), *_ws_args(ws))
+    return dx, dw
+
+
+def _glu_dims(R, I, act, p, dev):
+    if p is None:
+        return GluDims(R, I, 0, _one_of(ACTS, act, "act")), None
+    P, E, off = _offsets(p, dev)
+    if P != R:
+        raise ValueError(f"a plan of {P} rows for {R}")
+    return GluDims(R, I, E, _one_of(ACTS, act, "act")), off
+
+
+def glu(z: torch.Tensor, act: str = "silu", save: bool = True, p: Optional[Plan] = None, out=None):
+    """moe_glu on the current stream: (h, z_q, z_s) with h = act(g) u bf16 [R, I] of z = (g,
+    u) bf16 [R, 2I], and z's E4M3 codes uint8 [R, 2I] and E8M0 scales uint8 [R, 2I/128] to
+    keep for glu_grad in place of z (None without save). p: rows behind the plan's last
+    expert's are left as they were (default: every row counts). out: (h, z_q, z_s) tensors
+    to write, None members are allocated."""
+    dev = _first(z, 2, "z")
+    R, I = z.shape[0], z.shape[1] // 2
+    if z.shape[1] % 2:
+        raise ValueError(f"z: two halves, got {z.shape[1]} columns")
+    d, off = _glu_dims(R, I, act, p, dev)
+    h, q, s = out if out is not None else (None, None, None)
+    if h is None:
+        h = _new(R, I, BF16, dev)
+    if not save:
+        q = s = None
+    else:
+        if q is None:
+            q = _new(R, 2 * I, torch.uint8, dev)
+        if s is None:
+            s = _new(R, 2 * I // 128, torch.uint8, dev)
+    _enqueue("moe_glu", dev, d, _tensor(z, BF16, (R, 2 * I), dev, "z"), off, _tensor(h, BF16, (R, I), dev, "out h"),
+             _tensor(q, torch.uint8, (R, 2 * I), dev, "out z_q"), _tensor(s, torch.uint8, (R, 2 * I // 128), dev, "out z_s"))
+    return h, q, s
+
+
+def glu_grad(dh: torch.Tensor, z: torch.Tensor, scales: Optional[torch.Tensor] = None, act: str = "silu",
+             p: Optional[Plan] = None, need_h: bool = True, out=None):
+    """moe_glu_grad on the current stream: (dz bf16 [R, 2I], h bf16 [R, I] or None) from dh
+    bf16 [R, I] and z: glu's codes uint8 [R, 2I] with their scales, or bf16 z itself. h is
+    act(g) u at the same values, for the second product's dw. p as in glu. out: (dz, h)
+    tensors to write (dz may be a bf16 z, h may be dh), None members are allocated."""
+    dev = _first(dh, 2, "dh")
+    R, I = dh.shape
+    d, off = _glu_dims(R, I, act, p, dev)
+    dz, h = out if out is not None else (None, None)
+    if dz is None:
+        dz = _new(R, 2 * I, BF16, dev)
+    if not need_h:
+        h = None
+    elif h is None:
+        h = _new(R, I, BF16, dev)
+    zp = _tensor(z, BF16 if scales is None else torch.uint8, (R, 2 * I), dev, "z")
+    sp = _tensor(scales, torch.uint8, (R, 2 * I // 128), dev, "scales")
+    _enqueue("moe_glu_grad", dev, d, _tensor(dh, BF16, (R, I), dev, "dh"), None if scales is not None else zp,
+             zp if scales is not None else None, sp, off, _tensor(dz, BF16, (R, 2 * I), dev, "out dz"),
+             _tensor(h, BF16, (R, I), dev, "out h"))
+    return dz, h

@@ -1,0 +1,277 @@
+// The experts' products on rows grouped by expert, and their gradients, in bf16 with fp32
+// sums:  y[r] = W[e] x[r],  dx[r] = W[e]^T dy[r],  dW[e] = sum over e's rows of dy[r] x[r]^T
+// for the rows r in [offsets[e], offsets[e + 1]). The offsets live on the device, so
+// grids are sized by bounds and workgroups look up what is theirs.
+//
+// Few rows per expert (a decode step): bound by streaming the weights of the experts that
+// have rows, on k_expert_few. More rows: tiles (experts_tile.hip), along a list that one
+// workgroup writes first.
+#include "experts.h"
+#include "linear.h"
+#include "lane_reduce.h"
+
+namespace moe {
+namespace {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ v4f mfma_bf16(const v4i a, const v4i b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------ few rows
+// Unit u of the experts' rows in units of at most kFewRows; rows 0 past the last one. A
+// wave looks it up: each lane counts the units of E / 64 neighbouring experts, a scan
+// over the lanes finds the lane, a second one the expert.
+constexpr int kFewRows = 64;
+struct Unit {
+  int expert, row0, rows;
+};
+__device__ __forceinline__ int scan_add(int v, int lane) {   // inclusive, over a wave
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    v += lane >= d ? o : 0;
+  }
+  return v;
+}
+__device__ __forceinline__ Unit find_unit(const int32_t* off, int E, int P, int u) {
+  const int lane = threadIdx.x & 63, per = (E + 63) / 64;
+  auto units = [&](const RowRange r) { return (r.hi - r.lo + kFewRows - 1) / kFewRows; };
+  int n = 0, prev = off[min(lane * per, E)];
+#pragma unroll 8
+  for (int i = 1; i <= per; ++i) {   // experts past the last one have no rows
+    const int next = off[min(lane * per + i, E)];
+    n += units(rows_of(prev, next, P));
+    prev = next;
+  }
+  const int end = scan_add(n, lane);
+  const uint64_t past = __ballot(end > u);
+  if (past == 0) return Unit{0, 0, 0};
+  const int at = __ffsll((unsigned long long)past) - 1;
+  int base = __shfl(end - n, at);
+  const int e = at * per + lane;
+  const bool mine = lane < per && e < E;
+  const RowRange r = mine ? rows_of(off[e], off[e + 1], P) : RowRange{0, 0};
+  const int m = units(r), stop = base + scan_add(m, lane);
+  const int found = __ffsll((unsigned long long)__ballot(stop > u)) - 1;
+  const int first = __shfl(stop - m, found), lo = __shfl(r.lo, found), hi = __shfl(r.hi, found);
+  const int row0 = lo + (u - first) * kFewRows;
+  return Unit{__builtin_amdgcn_readfirstlane(at * per + found), __builtin_amdgcn_readfirstlane(row0),
+              __builtin_amdgcn_readfirstlane(min(kFewRows, hi - row0))};
+}
+
+// A workgroup owns 16 output columns of a unit; its waves take every waves-th step of 64
+// of the contraction straight from memory into registers, a step's loads ahead, and add
+// their sums through LDS in wave order. FT: 16-row fragments.
+constexpr int kFewWaves = 16;
+
+template <int FT, bool F32>
+__device__ __forceinline__ void few_rows(const ExpertArgs& a, const Unit& u, float* red) {
+  constexpr int kDepth = 4 / FT;   // steps of loads in flight per wave (128 VGPRs at 16 waves)
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int n0 = blockIdx.x * 16, steps = a.D / 64;
+  const uint16_t* w = a.w + u.expert * a.w_expert + (int64_t)(n0 + c) * a.ws + q * 8;
+  const uint16_t* x[FT];
+#pragma unroll
+  for (int f = 0; f < FT; ++f) x[f] = a.x + (int64_t)(u.row0 + min(16 * f + c, u.rows - 1)) * a.D + q * 8;
+  v4f acc[FT] = {};
+  for (int s = wave; s < steps; s += waves * kDepth) {
+    v4i wv[kDepth][2], xv[kDepth][FT][2];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      const int st = s + d * waves;
+      if (st < steps) {   // wave-uniform
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          wv[d][h] = load16_nt(w + st * 64 + 32 * h);
+#pragma unroll
+          for (int f = 0; f < FT; ++f) xv[d][f][h] = load16(x[f] + st * 64 + 32 * h);
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+      if (s + d * waves < steps) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int f = 0; f < FT; ++f) acc[f] = mfma_bf16(wv[d][h], xv[d][f][h], acc[f]);
+      }
+  }
+  v4f* part = reinterpret_cast<v4f*>(red);
+#pragma unroll
+  for (int f = 0; f < FT; ++f) part[(wave * FT + f) * 64 + lane] = acc[f];
+  __syncthreads();
+  for (int i = threadIdx.x; i < FT * 64; i += blockDim.x) {
+    v4f v = part[i];
+    for (int k = 1; k < waves; ++k) v += part[k * FT * 64 + i];
+    const int row = 16 * (i >> 6) + (i & 15), n = n0 + 4 * ((i & 63) >> 4);
+    if (row < u.rows) {
+      const int64_t at = (int64_t)(u.row0 + row) * a.O + n;
+      if constexpr (F32) *reinterpret_cast<v4f*>(static_cast<float*>(a.y) + at) = v;
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
+            make_uint2(bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]));
+    }
+  }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(64 * kFewWaves) void k_expert_few(ExpertArgs a) {
+  __shared__ __attribute__((aligned(16))) float red[kFewWaves * 4 * 256];
+  const Unit u = find_unit(a.off, a.E, a.P, blockIdx.y);
+  if (u.rows == 0) return;
+  if (u.rows <= 16) few_rows<1, F32>(a, u, red);
+  else if (u.rows <= 32) few_rows<2, F32>(a, u, red);
+  else few_rows<4, F32>(a, u, red);
+}
+
+// ------------------------------------------------------------------ the tile list
+// list[0].x = number of row tiles, then {expert, first row, rows, 0} of each: an expert's
+// rows in tiles of kTileRows, the last one shorter. order: the experts by their number
+// of rows, the most first (in classes of a quarter of an octave; within one by index).
+constexpr int kListThreads = 1024;
+constexpr int kClasses = 128;
+
+__global__ __launch_bounds__(kListThreads) void k_expert_list(const int32_t* off, int E, int P, int4* list, int cap,
+                                                              int32_t* order) {
+  __shared__ int ends[kMaxExperts];        // tiles up to and with expert e
+  __shared__ int waves[kListThreads / 64];
+  __shared__ int classes[kClasses];
+  __shared__ int counts[kMaxExperts / 64 * kClasses];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kPer = kMaxExperts / kListThreads;
+  int n[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * kPer + i;
+    const RowRange r = e < E ? rows_of(off[e], off[e + 1], P) : RowRange{0, 0};
+    n[i] = r.hi - r.lo;
+    sum += (n[i] + kTileRows - 1) / kTileRows;
+  }
+  const int end = scan_add(sum, lane);
+  if (lane == 63) waves[wave] = end;
+  __syncthreads();
+  int at = end - sum;
+  for (int w = 0; w < wave; ++w) at += waves[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    at += (n[i] + kTileRows - 1) / kTileRows;
+    ends[tid * kPer + i] = at;
+  }
+  __syncthreads();
+  if (list) {
+    const int total = min(ends[E - 1], cap);
+    if (tid == 0) list[0] = make_int4(total, 0, 0, 0);
+    for (int t = tid; t < total; t += kListThreads) {
+      int lo = 0, hi = E - 1;   // the first expert whose end is past t
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (ends[mid] > t) hi = mid;
+        else lo = mid + 1;
+      }
+      const RowRange r = rows_of(off[lo], off[lo + 1], P);
+      const int row0 = r.lo + (t - (lo ? ends[lo - 1] : 0)) * kTileRows;
+      list[1 + t] = make_int4(lo, row0, min(kTileRows, r.hi - row0), 0);
+    }
+  }
+  if (!order) return;
+  // Class of n rows, 0 the largest; the rank of an expert is the experts of classes
+  // before its own, those of its class in segments of 64 experts before its own, and
+  // those before it in its segment, which the lanes of a wave find by comparing classes.
+  auto class_of = [&](int v) {
+    if (v == 0) return kClasses - 1;
+    const int b = 31 - __clz(v), frac = b >= 2 ? (v >> (b - 2)) & 3 : 0;
+    return kClasses - 2 - (4 * b + frac);   // b is at most 30
+  };
+  const int segments = (E + 63) / 64;
+  for (int i = tid; i < segments * kClasses; i += kListThreads) counts[i] = 0;
+  __syncthreads();
+  int cls[kPer], before[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = i * kListThreads + tid;
+    const RowRange r = e < E ? rows_of(off[e], off[e + 1], P) : RowRange{0, 0};
+    cls[i] = class_of(r.hi - r.lo);
+    uint64_t same = __ballot(e < E);
+#pragma unroll
+    for (int b = 1; b < kClasses; b <<= 1) {
+      const uint64_t set = __ballot((cls[i] & b) != 0);
+      same &= (cls[i] & b) ? set : ~set;
+    }
+    before[i] = __popcll(same & (((uint64_t)1 << lane) - 1));
+    if (e < E && before[i] == 0) counts[(e >> 6) * kClasses + cls[i]] = __popcll(same);
+  }
+  __syncthreads();
+  if (tid < kClasses) {
+    int s = 0;
+    for (int g = 0; g < segments; ++g) {
+      const int k = counts[g * kClasses + tid];
+      counts[g * kClasses + tid] = s;
+      s += k;
+    }
+    const int upto = scan_add(s, lane);
+    classes[tid] = upto - s;
+    if (tid == 63) waves[0] = upto;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = i * kListThreads + tid;
+    if (e < E)
+      order[classes[cls[i]] + (cls[i] >= 64 ? waves[0] : 0) + counts[(e >> 6) * kClasses + cls[i]] + before[i]] = e;
+  }
+}
+
+// Few rows: on average at most kFewPerExpert per expert.
+constexpr int64_t kFewPerExpert = 16;
+inline bool few(const moe_expert_dims& d) { return d.P <= kFewPerExpert * d.E; }
+
+inline size_t list_bytes(const moe_expert_dims& d) { return sizeof(int4) * (size_t)(1 + expert_tiles_bound(d.P, d.E)); }
+inline size_t order_bytes(const moe_expert_dims& d) { return align_up(sizeof(int32_t) * (size_t)d.E, 16); }
+
+void launch_list(const moe_expert_dims& d, const int32_t* off, int4* list, int32_t* order, hipStream_t s) {
+  hipLaunchKernelGGL(k_expert_list, dim3(1), dim3(kListThreads), 0, s, off, d.E, d.P, list,
+                     (int)expert_tiles_bound(d.P, d.E), order);
+}
+
+}  // namespace
+
+size_t expert_linear_ws_bytes(const moe_expert_dims& d) { return few(d) ? 0 : list_bytes(d); }
+
+hipError_t launch_expert_linear(const moe_expert_dims& d, const uint16_t* x, const uint16_t* w, const int32_t* off,
+                                void* y, void* ws, hipStream_t s) {
+  ExpertArgs a{x, w, off, y, static_cast<const int4*>(ws), (int64_t)d.N * d.K, d.P, d.E, d.K, d.N, d.K};
+  const bool f32 = d.type == MOE_TYPE_F32;
+  if (few(d)) {
+    const int64_t units = d.P / kFewRows + (d.P < d.E ? d.P : d.E);
+    const int waves = d.K / 64 < kFewWaves ? d.K / 64 : kFewWaves;
+    const dim3 grid((unsigned)(d.N / 16), (unsigned)units), block(64 * (unsigned)waves);
+    if (f32) hipLaunchKernelGGL(k_expert_few<true>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(k_expert_few<false>, grid, block, 0, s, a);
+  } else {
+    launch_list(d, off, static_cast<int4*>(ws), nullptr, s);
+    launch_expert_tiles(a, false, f32, s);
+  }
+  return hipGetLastError();
+}
+
+size_t expert_linear_grad_ws_bytes(const moe_expert_dims& d) { return order_bytes(d) + list_bytes(d); }
+
+hipError_t launch_expert_linear_grad(const moe_expert_dims& d, const uint16_t* dy, const uint16_t* x, const uint16_t* w,
+                                     const int32_t* off, uint16_t* dx, void* dw, void* ws, hipStream_t s) {
+  int32_t* const order = static_cast<int32_t*>(ws);
+  int4* const list = reinterpret_cast<int4*>(static_cast<char*>(ws) + order_bytes(d));
+  if (!(dx && d.P > 0) && !dw) return hipSuccess;
+  launch_list(d, off, dx ? list : nullptr, dw ? order : nullptr, s);
+  if (dx && d.P > 0) {   // [P, K] = dy [P, N] . w [E, N, K], contracted over N
+    const ExpertArgs a{dy, w, off, dx, list, (int64_t)d.N * d.K, d.P, d.E, d.N, d.K, d.K};
+    launch_expert_tiles(a, true, false, s);
+  }
+  if (dw) launch_expert_wgrad(ExpertGradArgs{dy, x, off, dw, order, d.P, d.E, d.N, d.K}, d.type == MOE_TYPE_F32, s);
+  return hipGetLastError();
+}
+
+}  // namespace moe

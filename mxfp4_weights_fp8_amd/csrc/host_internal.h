@@ -240,4 +240,28 @@ int balance_parts(const moe_gate_dims& d, int B);   // doubles of its workspace
 hipError_t launch_balance(const moe_gate_dims& d, int B, float alpha, const void* logits, const int32_t* ids,
                           const int32_t* off, float* loss, int32_t* counts, float* dl, double* parts, hipStream_t s);
 
+// ---------------------------------------------------------------- training the experts
+constexpr int kMaxPairs = 1 << 27;   // T K, or rows of the experts' products
+// Rows of tokens by expert and back; x_s null: x is bf16; pair_rows null: the rows are the
+// tokens (K 1).
+hipError_t launch_sort_rows(int T, int H, int K, const void* x, const uint8_t* x_s, const int32_t* pair_rows,
+                            uint16_t* rows, hipStream_t s);
+hipError_t launch_return_rows(int T, int H, int K, const uint16_t* rows, const int32_t* pair_rows, const float* w,
+                              const void* add, bool f32, void* y, hipStream_t s);
+hipError_t launch_return_rows_grad(int T, int H, int K, const void* dy, bool f32, const uint16_t* rows,
+                                   const int32_t* pair_rows, const float* w, uint16_t* d_rows, float* d_w,
+                                   hipStream_t s);
+// Experts' products.
+size_t expert_linear_ws_bytes(const moe_expert_dims& d);
+hipError_t launch_expert_linear(const moe_expert_dims& d, const uint16_t* x, const uint16_t* w, const int32_t* off,
+                                void* y, void* ws, hipStream_t s);
+size_t expert_linear_grad_ws_bytes(const moe_expert_dims& d);
+hipError_t launch_expert_linear_grad(const moe_expert_dims& d, const uint16_t* dy, const uint16_t* x, const uint16_t* w,
+                                     const int32_t* off, uint16_t* dx, void* dw, void* ws, hipStream_t s);
+// Gated activation; live (optional): rows on the device from which on nothing is done.
+hipError_t launch_glu(const moe_glu_dims& d, const uint16_t* z, const int32_t* live, uint16_t* h, uint8_t* z_q,
+                      uint8_t* z_s, hipStream_t s);
+hipError_t launch_glu_grad(const moe_glu_dims& d, const uint16_t* dh, const uint16_t* z, const uint8_t* z_q,
+                           const uint8_t* z_s, const int32_t* live, uint16_t* dz, uint16_t* h, hipStream_t s);
+
 }  // namespace moe

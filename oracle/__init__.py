@@ -33,6 +33,8 @@ Modules:
               to pin ``moe`` on tiny inputs.
   block    -- the operators in front of the FFN (residual add + norm, dense product,
               gate, balance loss) and their gradients, in float64.
+  train    -- training the experts (rows by expert and back, the experts' products, the
+              gated activation with its input in 8 bits) and the gradients, in float64.
   compare  -- the parity metrics and the SwiGLU-code comparison rule.
 
 Parity status of each function is stated in its docstring; every function here
