@@ -62,13 +62,18 @@ __device__ __forceinline__ Unit find_unit(const int32_t* off, int E, int P, int 
 }
 
 // A workgroup owns 16 output columns of a unit; its waves take every waves-th step of 64
-// of the contraction straight from memory into registers, a step's loads ahead, and add
-// their sums through LDS in wave order. FT: 16-row fragments.
-constexpr int kFewWaves = 16;
+// of the contraction straight from memory into registers, kDepth steps' loads at a time,
+// and add their sums through LDS in wave order. FT: 16-row fragments.
+//
+// 56 rows of 30 experts, 768 x 7168 (330 MB of weights) 74 us, 4.5 TB/s. Eight workgroups of
+// four waves share a CU, so that one looks up its rows or adds its sums while others load:
+// with eight waves each 78 us, with sixteen 88 us. A row's 128 bytes come by two loads of 64;
+// with the nontemporal hint, which lets go of the line between them, 101 us.
+constexpr int kFewWaves = 4;
 
 template <int FT, bool F32>
 __device__ __forceinline__ void few_rows(const ExpertArgs& a, const Unit& u, float* red) {
-  constexpr int kDepth = 4 / FT;   // steps of loads in flight per wave (128 VGPRs at 16 waves)
+  constexpr int kDepth = 4 / FT;
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int n0 = blockIdx.x * 16, steps = a.D / 64;
@@ -85,7 +90,7 @@ __device__ __forceinline__ void few_rows(const ExpertArgs& a, const Unit& u, flo
       if (st < steps) {   // wave-uniform
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          wv[d][h] = load16_nt(w + st * 64 + 32 * h);
+          wv[d][h] = load16(w + st * 64 + 32 * h);
 #pragma unroll
           for (int f = 0; f < FT; ++f) xv[d][f][h] = load16(x[f] + st * 64 + 32 * h);
         }
@@ -130,51 +135,76 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_expert_few(ExpertArgs a) {
 
 // ------------------------------------------------------------------ the tile list
 // list[0].x = number of row tiles, then {expert, first row, rows, 0} of each: an expert's
-// rows in tiles of kTileRows, the last one shorter. order: the experts by their number
-// of rows, the most first (in classes of a quarter of an octave; within one by index).
+// rows in tiles of kTileRows, the last one shorter. Tiles of more than 128 rows come
+// first, then those of more than 64, then the rest (the kernel's three sizes), experts in
+// rising order in each: the short ones fill up the last round.
+// order: the experts by their number of rows, the most first (in classes of a quarter of
+// an octave; within one by index).
 constexpr int kListThreads = 1024;
 constexpr int kClasses = 128;
 
 __global__ __launch_bounds__(kListThreads) void k_expert_list(const int32_t* off, int E, int P, int4* list, int cap,
                                                               int32_t* order) {
-  __shared__ int ends[kMaxExperts];        // tiles up to and with expert e
-  __shared__ int waves[kListThreads / 64];
+  __shared__ int ends[kMaxExperts];        // tall tiles up to and with expert e
+  __shared__ int waves[3][kListThreads / 64];
   __shared__ int classes[kClasses];
   __shared__ int counts[kMaxExperts / 64 * kClasses];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int kPer = kMaxExperts / kListThreads;
-  int n[kPer], sum = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = tid * kPer + i;
-    const RowRange r = e < E ? rows_of(off[e], off[e + 1], P) : RowRange{0, 0};
-    n[i] = r.hi - r.lo;
-    sum += (n[i] + kTileRows - 1) / kTileRows;
-  }
-  const int end = scan_add(sum, lane);
-  if (lane == 63) waves[wave] = end;
-  __syncthreads();
-  int at = end - sum;
-  for (int w = 0; w < wave; ++w) at += waves[w];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    at += (n[i] + kTileRows - 1) / kTileRows;
-    ends[tid * kPer + i] = at;
-  }
-  __syncthreads();
   if (list) {
-    const int total = min(ends[E - 1], cap);
-    if (tid == 0) list[0] = make_int4(total, 0, 0, 0);
-    for (int t = tid; t < total; t += kListThreads) {
+    // Each thread's kPer experts: tall tiles, and a last one of middle or small size.
+    RowRange r[kPer];
+    int tall[kPer], n[3] = {0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid * kPer + i;
+      r[i] = e < E ? rows_of(off[e], off[e + 1], P) : RowRange{0, 0};
+      const int rows = r[i].hi - r[i].lo, last = rows % kTileRows;
+      tall[i] = rows / kTileRows + (last > 128);
+      n[0] += tall[i];
+      n[1] += last > 64 && last <= 128;
+      n[2] += last > 0 && last <= 64;
+    }
+    int at[3], total[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      at[k] = scan_add(n[k], lane);
+      if (lane == 63) waves[k][wave] = at[k];
+      at[k] -= n[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      total[k] = 0;
+#pragma unroll
+      for (int w = 0; w < kListThreads / 64; ++w) {
+        at[k] += w < wave ? waves[k][w] : 0;
+        total[k] += waves[k][w];
+      }
+    }
+    at[1] += total[0];
+    at[2] += total[0] + total[1];
+    auto write = [&](int t, int e, const RowRange& x, int k) {   // tile k of expert e at place t
+      const int row0 = x.lo + k * kTileRows;
+      if (t < cap) list[1 + t] = make_int4(e, row0, min(kTileRows, x.hi - row0), 0);
+    };
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      at[0] += tall[i];
+      ends[tid * kPer + i] = at[0];
+      const int last = (r[i].hi - r[i].lo) % kTileRows;
+      if (last > 0 && last <= 128) write(last > 64 ? at[1]++ : at[2]++, tid * kPer + i, r[i], tall[i]);
+    }
+    __syncthreads();
+    if (tid == 0) list[0] = make_int4(min(total[0] + total[1] + total[2], cap), 0, 0, 0);
+    for (int t = tid; t < min(total[0], cap); t += kListThreads) {
       int lo = 0, hi = E - 1;   // the first expert whose end is past t
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
         if (ends[mid] > t) hi = mid;
         else lo = mid + 1;
       }
-      const RowRange r = rows_of(off[lo], off[lo + 1], P);
-      const int row0 = r.lo + (t - (lo ? ends[lo - 1] : 0)) * kTileRows;
-      list[1 + t] = make_int4(lo, row0, min(kTileRows, r.hi - row0), 0);
+      write(t, lo, rows_of(off[lo], off[lo + 1], P), t - (lo ? ends[lo - 1] : 0));
     }
   }
   if (!order) return;
@@ -186,6 +216,7 @@ __global__ __launch_bounds__(kListThreads) void k_expert_list(const int32_t* off
     const int b = 31 - __clz(v), frac = b >= 2 ? (v >> (b - 2)) & 3 : 0;
     return kClasses - 2 - (4 * b + frac);   // b is at most 30
   };
+  __syncthreads();
   const int segments = (E + 63) / 64;
   for (int i = tid; i < segments * kClasses; i += kListThreads) counts[i] = 0;
   __syncthreads();
@@ -214,14 +245,14 @@ __global__ __launch_bounds__(kListThreads) void k_expert_list(const int32_t* off
     }
     const int upto = scan_add(s, lane);
     classes[tid] = upto - s;
-    if (tid == 63) waves[0] = upto;
+    if (tid == 63) waves[0][0] = upto;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = i * kListThreads + tid;
     if (e < E)
-      order[classes[cls[i]] + (cls[i] >= 64 ? waves[0] : 0) + counts[(e >> 6) * kClasses + cls[i]] + before[i]] = e;
+      order[classes[cls[i]] + (cls[i] >= 64 ? waves[0][0] : 0) + counts[(e >> 6) * kClasses + cls[i]] + before[i]] = e;
   }
 }
 
@@ -243,8 +274,8 @@ size_t expert_linear_ws_bytes(const moe_expert_dims& d) { return few(d) ? 0 : li
 
 hipError_t launch_expert_linear(const moe_expert_dims& d, const uint16_t* x, const uint16_t* w, const int32_t* off,
                                 void* y, void* ws, hipStream_t s) {
-  ExpertArgs a{x, w, off, y, static_cast<const int4*>(ws), (int64_t)d.N * d.K, d.P, d.E, d.K, d.N, d.K};
   const bool f32 = d.type == MOE_TYPE_F32;
+  const ExpertArgs a{x, w, off, y, static_cast<const int4*>(ws), (int64_t)d.N * d.K, d.P, d.E, d.K, d.N, d.K};
   if (few(d)) {
     const int64_t units = d.P / kFewRows + (d.P < d.E ? d.P : d.E);
     const int waves = d.K / 64 < kFewWaves ? d.K / 64 : kFewWaves;

@@ -33,11 +33,14 @@ constexpr int kCus = 256;
 constexpr int kGroup = 8;   // row tiles that share a pass over the column tiles
 constexpr int kFirstStages = 3, kSecondStages = 2;
 
-// acc += A B, acc in AGPRs. The compiler does not know that the statement is an MFMA and
+// acc += A B, or acc = A B (FIRST, which saves writing zeros: 5 % of a tile of three
+// steps), acc in AGPRs. The compiler does not know that the statement is an MFMA and
 // inserts no wait states after a VALU write of an operand: s_nop provides them.
+template <bool FIRST>
 __device__ __forceinline__ void mma_agpr(v4f& acc, const v4i& a, const v4i& b) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+  if constexpr (FIRST) asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, 0" : "=a"(acc) : "v"(a), "v"(b));
+  else asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 #endif
 }
 // ... nor before the accumulators are read: 64 of them.
@@ -64,47 +67,80 @@ struct OutTile {
     cols_left = O - n0;
     r = make_rsrc(static_cast<char*>(y) + row0 * row_bytes + n0 * kSize, (uint32_t)(rows * row_bytes - n0 * kSize));
   }
+  __device__ __forceinline__ void put(const v4i v, int voff) const {
+    typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, voff, 0, 2);   // nontemporal
+  }
 };
 constexpr int kOutside = 1 << 30;   // past any tile: 256 rows of 64 K columns at most
 
 // The accumulators acc[i][j], columns 16 i + 4q .. + 3 of row 16 j + c of the wave's part,
-// which starts at row `m0` and column `n0` of the tile. Always FT FW stores (half of them in
-// bf16); rows and columns past the end are dropped by the resource's bounds check.
+// which starts at row `m0` and column `n0` of the tile. A piece is the 16 bytes that a
+// lane stores; four lanes (q) have 64 neighbouring bytes of a row. Lanes of neighbouring
+// rows trade pieces that are 64 bytes apart, so that a store writes 128-byte lines whole:
+// the gradient of 384 experts' 768 x 7168 weights from 64 rows each, nearly all stores,
+// took 1125 us in half lines, 956 in whole ones, and 907 with these nontemporal. (Small
+// results that the next kernel reads at once lose nothing by it: 8192 x 768 and its
+// gated activation 40.1 us, 41.7 without; 65536 x 768 141 and 139.)
+// Always FT FW stores (half of them in bf16); rows and columns past the end are dropped by
+// the resource's bounds check.
 template <int FT, int FW, int FTM, bool F32>
 __device__ __forceinline__ void store_tile(const OutTile& o, v4f (&acc)[FW][FTM], int m0, int n0, int lane) {
-  constexpr int kCols = F32 ? 4 : 8, kSize = F32 ? 4 : 2;   // per lane and store
+  constexpr int kCols = F32 ? 4 : 8, kSize = F32 ? 4 : 2;   // of a piece
+  constexpr int kFrags = F32 ? 1 : 2;                       // that a piece comes from
   const int c = lane & 15, q = lane >> 4;
+  const bool odd = c & 1;
   int at = (m0 + c) * o.row_bytes + (n0 + kCols * q) * kSize, step = 16 * o.row_bytes;
 #if defined(__HIP_DEVICE_COMPILE__)
   asm volatile("" : "+v"(at), "+s"(step));   // else every store's offset is kept in a register from tile to tile
 #endif
   const int left = o.cols_left - n0 - kCols * q;
+  // the piece of the fragments from i on
+  auto piece = [&](int i, int j) {
+    if constexpr (F32) {
+      return __builtin_bit_cast(v4i, acc[i][j]);
+    } else {
+      v4f t0 = acc[i][j], t1 = acc[i + 1][j];
+#if defined(__HIP_DEVICE_COMPILE__)
+      asm volatile("" : "+v"(t0), "+v"(t1));   // here and not all at once, which takes registers that are not there
+#endif
+      v4i r;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // lane groups q of (f0, f1): (0 1 2 3, 0 1 2 3) -> (f0: 0 1, f1: 0 1; f0: 2 3, f1: 2 3)
+        // -> (f0: 0 2, f1: 0 2; f0: 1 3, f1: 1 3): group q holds columns 8q .. 8q + 7 of 32
+        const auto half = __builtin_amdgcn_permlane32_swap(bf16_pack2(t0[2 * h], t0[2 * h + 1]),
+                                                           bf16_pack2(t1[2 * h], t1[2 * h + 1]), false, false);
+        const auto quarter = __builtin_amdgcn_permlane16_swap(half[0], half[1], false, false);
+        r[h] = (int)quarter[0];
+        r[2 + h] = (int)quarter[1];
+      }
+      return r;
+    }
+  };
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
-    if constexpr (F32) {
 #pragma unroll
-      for (int i = 0; i < FW; ++i)
-        buf_store16(o.r, __builtin_bit_cast(v4i, acc[i][j]), 16 * i < left ? at + 64 * i : kOutside);
-    } else {
+    for (int i = 0; i < FW; i += 2 * kFrags) {
+      const v4i a = piece(i, j);
+      const int col = 16 * i;
+      if (i + kFrags < FW) {
+        // rows c and c + 1 of an even lane and its neighbour: the even one stores the first
+        // 64 bytes of both, the odd one the second
+        const v4i b = piece(i + kFrags, j);
+        v4i first, second;
 #pragma unroll
-      for (int i = 0; i < FW; i += 2) {
-        v4f t0 = acc[i][j], t1 = acc[i + 1][j];
-#if defined(__HIP_DEVICE_COMPILE__)
-        asm volatile("" : "+v"(t0), "+v"(t1));   // here and not all at once, which takes registers that are not there
-#endif
-        uint32_t f0[2], f1[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          f0[h] = bf16_pack2(t0[2 * h], t0[2 * h + 1]);
-          f1[h] = bf16_pack2(t1[2 * h], t1[2 * h + 1]);
-          // lane groups q of (f0, f1): (0 1 2 3, 0 1 2 3) -> (f0: 0 1, f1: 0 1; f0: 2 3, f1: 2 3)
-          // -> (f0: 0 2, f1: 0 2; f0: 1 3, f1: 1 3): group q holds columns 8q .. 8q + 7 of 32
-          const auto half = __builtin_amdgcn_permlane32_swap(f0[h], f1[h], false, false);
-          const auto quarter = __builtin_amdgcn_permlane16_swap(half[0], half[1], false, false);
-          f0[h] = quarter[0];
-          f1[h] = quarter[1];
+        for (int h = 0; h < 4; ++h) {
+          const int give = odd ? a[h] : b[h], got = __builtin_amdgcn_update_dpp(give, give, 0xB1, 0xF, 0xF, true);
+          first[h] = odd ? got : a[h];
+          second[h] = odd ? b[h] : got;
         }
-        buf_store16(o.r, v4i{(int)f0[0], (int)f0[1], (int)f1[0], (int)f1[1]}, 16 * i < left ? at + 32 * i : kOutside);
+        const int mine = at + kSize * col + (odd ? 64 - o.row_bytes : 0);   // of the even row
+        const bool in = col + (odd ? 16 * kFrags : 0) < left;
+        o.put(first, in ? mine : kOutside);
+        o.put(second, in ? mine + o.row_bytes : kOutside);
+      } else {
+        o.put(a, col < left ? at + kSize * col : kOutside);
       }
     }
     at += step;
@@ -161,65 +197,72 @@ struct Stream {
     __syncthreads();
   }
 
-  // One tile of `steps` steps, FT row fragments per wave.
-  template <int FT, typename Next>
-  __device__ __forceinline__ void tile(int steps, Next next) {
+  // Step of a tile with FT row fragments per wave, its first half's fragments read.
+  template <int FT, bool FIRST, typename Next>
+  __device__ __forceinline__ void step(Next next) {
+    const int ab1 = ab + 1 == kFirstStages ? 0 : ab + 1, ab2 = ab1 + 1 == kFirstStages ? 0 : ab1 + 1;
+    v4i_s sa, sb;
+    next(sa, sb);
+    const uint8_t *pa = stage_a(ab), *pb = stage_b(bb);
 #pragma unroll
-    for (int i = 0; i < FW; ++i)
+    for (int p = 0; p < FW; ++p) {   // half A
 #pragma unroll
-      for (int j = 0; j < FT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int j = p * FT / FW; j < (p + 1) * FT / FW; ++j) a[1][j] = ra.template read<1>(pa, FT * wm + j);
+      b[1][p] = rb.template read<1>(pb, FW * wn + p);
 #pragma unroll
-    for (int j = 0; j < FT; ++j) a[0][j] = ra.template read<0>(stage_a(ab), FT * wm + j);
+      for (int i = p * A::kCopies / FW; i < (p + 1) * A::kCopies / FW; ++i) oa.copy(sa, stage_a(ab2), wave, i);
 #pragma unroll
-    for (int i = 0; i < FW; ++i) b[0][i] = rb.template read<0>(stage_b(bb), FW * wn + i);
-    int s = 0;
-    do {   // one step at least: a path around the loop costs copies of the accumulators
-      const int ab1 = ab + 1 == kFirstStages ? 0 : ab + 1, ab2 = ab1 + 1 == kFirstStages ? 0 : ab1 + 1;
-      v4i_s sa, sb;
-      next(sa, sb);
-      const uint8_t *pa = stage_a(ab), *pb = stage_b(bb);
-#pragma unroll
-      for (int p = 0; p < FW; ++p) {   // half A
-#pragma unroll
-        for (int j = p * FT / FW; j < (p + 1) * FT / FW; ++j) a[1][j] = ra.template read<1>(pa, FT * wm + j);
-        b[1][p] = rb.template read<1>(pb, FW * wn + p);
-#pragma unroll
-        for (int i = p * A::kCopies / FW; i < (p + 1) * A::kCopies / FW; ++i) oa.copy(sa, stage_a(ab2), wave, i);
-#pragma unroll
-        for (int j = 0; j < FT; ++j) mma_agpr(acc[p][j], b[0][p], a[0][j]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      // behind the copies that are waited for: this half's, and in a tile's first step the
-      // stores of the tile before
-      constexpr int kStores = F32 ? FTM * FW : FTM * FW / 2;
-      constexpr int kPast = A::kCopies + kStores < 63 ? A::kCopies + kStores : 63;
-      if (s == 0 && stores) wait_vmcnt<kPast>();
-      else wait_vmcnt<A::kCopies>();
-      __syncthreads();
+      for (int j = 0; j < FT; ++j) mma_agpr<FIRST>(acc[p][j], b[0][p], a[0][j]);
       __builtin_amdgcn_sched_barrier(0);
-      pa = stage_a(ab1);
-      pb = stage_b(bb ^ 1);
+    }
+    // behind the copies that are waited for: this half's, and in a tile's first step the
+    // stores of the tile before
+    constexpr int kStores = F32 ? FTM * FW : FTM * FW / 2;
+    constexpr int kPast = A::kCopies + kStores < 63 ? A::kCopies + kStores : 63;
+    if (FIRST && stores) wait_vmcnt<kPast>();
+    else wait_vmcnt<A::kCopies>();
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    pa = stage_a(ab1);
+    pb = stage_b(bb ^ 1);
 #pragma unroll
-      for (int p = 0; p < FW; ++p) {   // half B
+    for (int p = 0; p < FW; ++p) {   // half B
 #pragma unroll
-        for (int j = p * FT / FW; j < (p + 1) * FT / FW; ++j) a[0][j] = ra.template read<0>(pa, FT * wm + j);
-        b[0][p] = rb.template read<0>(pb, FW * wn + p);
+      for (int j = p * FT / FW; j < (p + 1) * FT / FW; ++j) a[0][j] = ra.template read<0>(pa, FT * wm + j);
+      b[0][p] = rb.template read<0>(pb, FW * wn + p);
 #pragma unroll
-        for (int i = p * B::kCopies / FW; i < (p + 1) * B::kCopies / FW; ++i) ob.copy(sb, stage_b(bb), wave, i);
+      for (int i = p * B::kCopies / FW; i < (p + 1) * B::kCopies / FW; ++i) ob.copy(sb, stage_b(bb), wave, i);
 #pragma unroll
-        for (int j = 0; j < FT; ++j) mma_agpr(acc[p][j], b[1][p], a[1][j]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      ab = ab1;
-      bb ^= 1;
-    } while (++s < steps);
-    mma_done();
+      for (int j = 0; j < FT; ++j) mma_agpr<false>(acc[p][j], b[1][p], a[1][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    ab = ab1;
+    bb ^= 1;
+    pin<FT>();
+  }
+  // The accumulators in AGPRs here: else the compiler copies them all to the other register
+  // file, which spills, where the loop over the steps begins and ends.
+  template <int FT>
+  __device__ __forceinline__ void pin() {
 #if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
     for (int i = 0; i < FW; ++i)
 #pragma unroll
-      for (int j = 0; j < FT; ++j) asm volatile("; still in an AGPR" : "+a"(acc[i][j]));
+      for (int j = 0; j < FT; ++j) asm volatile("; in an AGPR" : "+a"(acc[i][j]));
 #endif
+  }
+
+  // One tile of `steps` (at least one) steps.
+  template <int FT, typename Next>
+  __device__ __forceinline__ void tile(int steps, Next next) {
+#pragma unroll
+    for (int j = 0; j < FT; ++j) a[0][j] = ra.template read<0>(stage_a(ab), FT * wm + j);
+#pragma unroll
+    for (int i = 0; i < FW; ++i) b[0][i] = rb.template read<0>(stage_b(bb), FW * wn + i);
+    step<FT, true>(next);
+    for (int s = 1; s < steps; ++s) step<FT, false>(next);
+    mma_done();
+    pin<FT>();
     stores = FT == FTM;
   }
   template <int FT>
@@ -228,17 +271,18 @@ struct Stream {
   }
 };
 
-// Tiles are dealt to the XCDs in contiguous runs of the order (group of kGroup row tiles,
-// column tile, row tile), so that the tiles that share operand rows share an L2.
+// Tiles in the order (group of kGroup row tiles, column tile, row tile), dealt to the XCDs
+// in runs of as many as each has workgroups, so that the tiles that share operand rows
+// and run at the same time share an L2, and so that every XCD has its share of the tall
+// tiles, which come first, and of the short ones.
 template <int FW, bool WT, bool F32>
 __global__ __launch_bounds__(kThreads, 1) void k_expert_tile(ExpertArgs a) {
   typedef Stream<8, FW, false, WT, F32> S;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kSmem];
   const const_ints list = as_const(a.list);
   const int row_tiles = list[0], n_tiles = (a.O + 32 * FW - 1) / (32 * FW), steps = a.D / 64;
-  const int total = row_tiles * n_tiles, run = (total + kXcds - 1) / kXcds;
-  const int begin = blockIdx.x % kXcds * run + blockIdx.x / kXcds, stride = gridDim.x / kXcds;
-  const int end = min((int)(blockIdx.x % kXcds + 1) * run, total);
+  const int end = row_tiles * n_tiles, stride = gridDim.x;
+  const int begin = blockIdx.x % kXcds * (stride / kXcds) + blockIdx.x / kXcds;
   if (begin >= end) return;
 
   struct Tile {
