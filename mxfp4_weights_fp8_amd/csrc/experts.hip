@@ -3,12 +3,14 @@
 // for the rows r in [offsets[e], offsets[e + 1]). The offsets live on the device, so
 // grids are sized by bounds and workgroups look up what is theirs.
 //
-// Few rows per expert (a decode step): bound by streaming the weights of the experts that
-// have rows, on k_expert_few. More rows: tiles (experts_tile.hip), along a list that one
-// workgroup writes first.
+// Few rows (a decode step): bound by streaming the weights of the experts that have rows,
+// on k_expert_few. More rows: tiles (experts_tile.hip), along a list that one workgroup
+// writes first.
 #include "experts.h"
 #include "linear.h"
 #include "lane_reduce.h"
+
+#include <math.h>
 
 namespace moe {
 namespace {
@@ -256,9 +258,26 @@ __global__ __launch_bounds__(kListThreads) void k_expert_list(const int32_t* off
   }
 }
 
-// Few rows: on average at most kFewPerExpert per expert.
-constexpr int64_t kFewPerExpert = 16;
-inline bool few(const moe_expert_dims& d) { return d.P <= kFewPerExpert * d.E; }
+// Which kernel: the least estimated time, in us, with as many experts at work as a mildly
+// uneven router gives P picks. k_expert_few streams weights at 5.3 TB/s, pays for every
+// workgroup of 16 columns (4.5 ns with all CUs at it) and for its rows (110 TFLOP/s, partly
+// hidden); the tiles stream at 5.2 TB/s behind the list, but a tile takes 0.75 us per step
+// however few rows it has. k_expert_few and tiles, in us:
+//   768 x 7168, 384 experts, 8 rows 13 and 76, 56 rows 78 and 135, 208 rows 156 and 160, 512
+//   rows 319 and 327, 1363 rows 730 and 785, 5945 rows 1084 and 802
+//   7168 x 384, 384 experts, 8 rows 11 and 14, 56 rows 68 and 41, 512 rows 429 and 170
+//   4096 x 4096, 16 experts, 2 rows 15 and 44, 64 rows 90 and 120, 256 rows 141 and 129
+//   1024 x 2048, 64 experts, 32 rows 14 and 28, 222 rows 54 and 46, 992 rows 80 and 53
+//   512 x 256, 8 experts, 3 rows 7 and 11, 959 rows 7 and 16; 1024 x 512, 2048 rows 25 and 21
+inline bool few(const moe_expert_dims& d) {
+  const double rows = d.P, matrix = (double)d.N * d.K, steps = d.K / 64;
+  const double experts = fmax(1.0, d.E * (1.0 - exp(-0.65 * rows / d.E))), bytes = 2.0 * experts * matrix;
+  const double column_tiles = (double)ceil_div(d.N, kTileRows), row_tiles = fmax(experts, rows / kTileRows);
+  const double rounds = ceil(row_tiles * column_tiles / 256);
+  const double tiles = 8 + fmax(bytes / 5.2e6, 0.75 * rounds * steps) + 0.2 * steps;
+  const double units = experts + rows / kFewRows;
+  return 6 + fmax(bytes / 5.3e6, 0.0045 * units * (d.N / 16)) + 1.2 * rows * matrix / 1.1e8 <= tiles;
+}
 
 inline size_t list_bytes(const moe_expert_dims& d) { return sizeof(int4) * (size_t)(1 + expert_tiles_bound(d.P, d.E)); }
 inline size_t order_bytes(const moe_expert_dims& d) { return align_up(sizeof(int32_t) * (size_t)d.E, 16); }

@@ -195,15 +195,16 @@ def test_infinities_stay_in_their_rows(dev):
     xr = moe.sort_rows(x.to(dev), p)
     for big in (False, True):            # few rows, and tiles
         if big:
-            p, off = sized(dev, [90, 0, 300, 5, 100], behind=1)
-            xr = randn(496, 128, seed=5, dtype=BF16).to(dev)
+            p, off = sized(dev, [90, 0, 300, 5, 20100], behind=1)
+            assert in_tiles(20496, 128, 128, 5)
+            xr = randn(20496, 128, seed=5, dtype=BF16).to(dev)
             xr[100, 7] = math.nan
         z = moe.expert_linear(xr, w.to(dev), p).cpu()
         nan_rows = torch.isnan(xr.cpu()).any(1)
         live = int(off[-1])
         assert torch.equal(torch.isnan(z[:live]).all(1), nan_rows[:live])
         assert torch.equal(torch.isnan(z[:live]).any(1), nan_rows[:live])
-    d = randn(496, 128, seed=6, dtype=BF16).to(dev)
+    d = randn(20496, 128, seed=6, dtype=BF16).to(dev)
     _, dw = moe.expert_linear_grad(d, xr, w.to(dev), p)
     hit = torch.isnan(dw).flatten(1).any(1).cpu().tolist()
     assert hit == [False, False, True, False, False]         # row 100 is expert 2's
@@ -245,13 +246,27 @@ def check_products(dev, sizes, N, C, behind=0, dtype=BF16, seed=0, grad=True):
         assert a is not None or torch.equal(b, dw)
 
 
+def in_tiles(rows, N, C, E):
+    """Whether the forward product runs in tiles (then it has a list in its workspace)."""
+    return moe.lib().moe_expert_linear_workspace_bytes(moe.ExpertDims(rows, N, C, E, 0)) > 0
+
+
+def with_filler(sizes, N, C):
+    """These experts and one more, with as many rows as the product needs to run in tiles."""
+    n = 0
+    while not in_tiles(sum(sizes) + n, N, C, len(sizes) + 1):
+        n += 61
+    return sizes + [n]
+
+
 # few rows per expert: one to 64 in a unit, more units, more experts than lanes
 @pytest.mark.parametrize("sizes,N,C", [
     ([1], 128, 128), ([0, 3, 0], 128, 256), ([16, 17, 0, 1, 33, 32], 384, 128), ([15, 2, 0, 0, 9], 128, 1152),
     ([64, 0, 0, 0, 0, 1], 256, 384), ([65, 0, 0, 0, 0, 0, 0, 0, 0], 128, 7168), ([0] * 70 + [3, 130] + [0] * 60 + [7], 128, 128),
-    ([1] * 300, 256, 128), ([0] * 4000 + [2, 5], 128, 128), ([2] * 65, 768, 512)])
+    ([1] * 200, 128, 384), ([0] * 4000 + [2, 5], 128, 128), ([2] * 65, 256, 1024)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_products_of_few_rows(dev, sizes, N, C, dtype):
+    assert not in_tiles(sum(sizes) + 3, N, C, len(sizes))
     check_products(dev, sizes, N, C, behind=3, dtype=dtype, seed=N)
 
 
@@ -264,18 +279,19 @@ def test_products_of_few_rows(dev, sizes, N, C, dtype):
     ([400], 128, 3200)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_products_in_tiles(dev, sizes, N, C, dtype):
-    check_products(dev, sizes, N, C, behind=37, dtype=dtype, seed=N + C)
+    check_products(dev, with_filler(sizes, N, C), N, C, behind=37, dtype=dtype, seed=N + C)
 
 
 @pytest.mark.parametrize("sizes,N,C", [([5000, 0, 7000, 300, 1200], 512, 1024), ([700] * 24, 768, 256),
                                        ([90] * 384, 256, 384)])
 def test_products_of_many_tiles(dev, sizes, N, C):
+    assert in_tiles(sum(sizes), N, C, len(sizes))
     check_products(dev, sizes, N, C, seed=N)
 
 
 def test_products_with_most_experts(dev):
-    sizes = [(7 * i) % 41 for i in range(4096)]
-    check_products(dev, sizes, 128, 128, behind=11)
+    for sizes in ([(7 * i) % 41 for i in range(4096)], [i % 2 for i in range(4096)]):
+        check_products(dev, sizes, 128, 128, behind=11)
 
 
 def test_offsets_past_32_bits(dev):
@@ -313,10 +329,17 @@ def test_offsets_past_32_bits(dev):
 def test_offsets_out_of_order_stay_inside(dev):
     """Offsets that no plan gives: results are unspecified, the buffers' guards are not
     touched and every kernel ends."""
-    E, P, N, C = 5, 700, 256, 128
-    p, _ = sized(dev, [140] * E)
+    E, N, C = 5, 256, 128
+    for P, k in ((700, 1), (700, -1), (14000, 20)):
+        _disorder(dev, E, P, N, C, k)
+
+
+def _disorder(dev, E, P, N, C, k):
+    assert in_tiles(P, N, C, E) == (k == 20)
+    p, _ = sized(dev, [P // E] * E)
     x, w, dy = (randn(*s, seed=i, dtype=BF16).to(dev) for i, s in enumerate(((P, C), (E, N, C), (P, N))))
     for bad in ([0, 650, 20, 690, 5, 700], [-9, 100, 2 ** 31 - 1, 300, -2 ** 31, 900], [700, 600, 500, 400, 300, 0]):
+        bad = [max(min(v * k, 2 ** 31 - 1), -2 ** 31) for v in bad]
         p.expert_offsets.copy_(torch.tensor(bad, dtype=torch.int32))
         guard = [marked(dev, n + 2 * 4096) for n in (P * N, P * C, E * N * C)]
         y, dx, dw = (t[4096:-4096].view(*s) for t, s in zip(guard, ((P, N), (P, C), (E, N, C))))
