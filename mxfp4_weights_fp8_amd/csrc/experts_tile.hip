@@ -4,18 +4,21 @@
 // the AGPR file.
 //
 // One workgroup per CU walks its tiles as one run of steps of 64 of the contraction: the
-// ring of LDS stages (three of the first operand, two of the second, filled by
+// ring of LDS stages (two of the rows' operand A, three of the columns' B, filled by
 // direct-to-LDS copies) goes on across the tiles, so that a tile's first steps arrive
 // while the tile before is multiplied and stored. Contractions here are short: 6 to 12
 // steps where an expert's inner size is contracted, 3 where its rows are.
 //
 // Step s, in two halves of 32:
-//   half A: the first half's MFMAs, the second half's fragment reads, the copies of the
-//           first operand of step s + 2;
+//   half A: the first half's MFMAs, the second half's fragment reads, the copies of B of
+//           step s + 2;
 //   wait for this wave's copies of step s + 1, and barrier: they have landed, and
 //           everybody has read step s to its end;
-//   half B: the second half's MFMAs, the next step's first fragments, the copies of the
-//           second operand of step s + 2 into the stage of step s.
+//   half B: the second half's MFMAs, the next step's first fragments, the copies of A of
+//           step s + 2 into the stage of step s.
+// B, an expert's weights, is copied half a step further ahead than A: it comes from HBM,
+// for a few row tiles (384 experts of 50 rows, 768 x 7168: 798 us, 834 the other way
+// round).
 // Results go from the registers to memory: neighbouring column fragments trade lanes, so
 // that a lane holds 8 columns (bf16) and four lanes 64 bytes of a row. The stores are in
 // flight during the next tile's first step: its wait counts past them.
@@ -31,7 +34,7 @@ constexpr int kThreads = 256;
 constexpr int kXcds = 8;
 constexpr int kCus = 256;
 constexpr int kGroup = 8;   // row tiles that share a pass over the column tiles
-constexpr int kFirstStages = 3, kSecondStages = 2;
+constexpr int kAStages = 2, kBStages = 3;
 
 // acc += A B, or acc = A B (FIRST, which saves writing zeros: 5 % of a tile of three
 // steps), acc in AGPRs. The compiler does not know that the statement is an MFMA and
@@ -154,7 +157,7 @@ template <int FTM, int FW, bool AT, bool BT, bool F32>
 struct Stream {
   typedef Operand<32 * FTM, AT> A;
   typedef Operand<32 * FW, BT> B;
-  static constexpr int kSmem = kFirstStages * A::kBytes + kSecondStages * B::kBytes;
+  static constexpr int kSmem = kAStages * A::kBytes + kBStages * B::kBytes;
 
   uint8_t* smem;
   int wave, lane, wm, wn;
@@ -179,7 +182,7 @@ struct Stream {
     rb.init(lane);
   }
   __device__ __forceinline__ uint8_t* stage_a(int i) const { return smem + i * A::kBytes; }
-  __device__ __forceinline__ uint8_t* stage_b(int i) const { return smem + kFirstStages * A::kBytes + i * B::kBytes; }
+  __device__ __forceinline__ uint8_t* stage_b(int i) const { return smem + kAStages * A::kBytes + i * B::kBytes; }
 
   // Steps 0 and 1 on their way, step 0 landed. next(ra, rb): the resources of the next step.
   template <typename Next>
@@ -200,7 +203,7 @@ struct Stream {
   // Step of a tile with FT row fragments per wave, its first half's fragments read.
   template <int FT, bool FIRST, typename Next>
   __device__ __forceinline__ void step(Next next) {
-    const int ab1 = ab + 1 == kFirstStages ? 0 : ab + 1, ab2 = ab1 + 1 == kFirstStages ? 0 : ab1 + 1;
+    const int bb1 = bb + 1 == kBStages ? 0 : bb + 1, bb2 = bb1 + 1 == kBStages ? 0 : bb1 + 1;
     v4i_s sa, sb;
     next(sa, sb);
     const uint8_t *pa = stage_a(ab), *pb = stage_b(bb);
@@ -210,7 +213,7 @@ struct Stream {
       for (int j = p * FT / FW; j < (p + 1) * FT / FW; ++j) a[1][j] = ra.template read<1>(pa, FT * wm + j);
       b[1][p] = rb.template read<1>(pb, FW * wn + p);
 #pragma unroll
-      for (int i = p * A::kCopies / FW; i < (p + 1) * A::kCopies / FW; ++i) oa.copy(sa, stage_a(ab2), wave, i);
+      for (int i = p * B::kCopies / FW; i < (p + 1) * B::kCopies / FW; ++i) ob.copy(sb, stage_b(bb2), wave, i);
 #pragma unroll
       for (int j = 0; j < FT; ++j) mma_agpr<FIRST>(acc[p][j], b[0][p], a[0][j]);
       __builtin_amdgcn_sched_barrier(0);
@@ -218,26 +221,26 @@ struct Stream {
     // behind the copies that are waited for: this half's, and in a tile's first step the
     // stores of the tile before
     constexpr int kStores = F32 ? FTM * FW : FTM * FW / 2;
-    constexpr int kPast = A::kCopies + kStores < 63 ? A::kCopies + kStores : 63;
+    constexpr int kPast = B::kCopies + kStores < 63 ? B::kCopies + kStores : 63;
     if (FIRST && stores) wait_vmcnt<kPast>();
-    else wait_vmcnt<A::kCopies>();
+    else wait_vmcnt<B::kCopies>();
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
-    pa = stage_a(ab1);
-    pb = stage_b(bb ^ 1);
+    pa = stage_a(ab ^ 1);
+    pb = stage_b(bb1);
 #pragma unroll
     for (int p = 0; p < FW; ++p) {   // half B
 #pragma unroll
       for (int j = p * FT / FW; j < (p + 1) * FT / FW; ++j) a[0][j] = ra.template read<0>(pa, FT * wm + j);
       b[0][p] = rb.template read<0>(pb, FW * wn + p);
 #pragma unroll
-      for (int i = p * B::kCopies / FW; i < (p + 1) * B::kCopies / FW; ++i) ob.copy(sb, stage_b(bb), wave, i);
+      for (int i = p * A::kCopies / FW; i < (p + 1) * A::kCopies / FW; ++i) oa.copy(sa, stage_a(ab), wave, i);
 #pragma unroll
       for (int j = 0; j < FT; ++j) mma_agpr<false>(acc[p][j], b[1][p], a[1][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    ab = ab1;
-    bb ^= 1;
+    ab ^= 1;
+    bb = bb1;
     pin<FT>();
   }
   // The accumulators in AGPRs here: else the compiler copies them all to the other register

@@ -20,7 +20,6 @@ namespace {
 
 constexpr int kGluThreads = 256;
 
-
 struct GluArgs {
   const uint16_t* z;     // [R, 2I] bf16; null in the gradient from codes
   const uint16_t* dh;    // [R, I]
@@ -58,6 +57,7 @@ __device__ __forceinline__ void save8(const GluArgs& a, int64_t at, const float 
   if ((threadIdx.x & 15) == 0) a.z_s[at / 128] = (uint8_t)(e + 127);
 }
 
+template <bool NT>
 __global__ __launch_bounds__(kGluThreads) void k_glu(GluArgs a) {
   const Spot p = spot_of(a);
   if (p.row >= a.R) return;
@@ -72,10 +72,10 @@ __global__ __launch_bounds__(kGluThreads) void k_glu(GluArgs a) {
   activate(g, a.act);
 #pragma unroll
   for (int i = 0; i < 8; ++i) g[i] *= u[i];
-  *reinterpret_cast<v4i*>(a.h + p.row * a.I + p.col) = pack8(g);
+  store_row<NT>(a.h + p.row * a.I + p.col, pack8(g));
 }
 
-template <bool CODES>
+template <bool CODES, bool NT>
 __global__ __launch_bounds__(kGluThreads) void k_glu_grad(GluArgs a) {
   const Spot p = spot_of(a);
   if (p.row >= a.R) return;
@@ -98,11 +98,12 @@ __global__ __launch_bounds__(kGluThreads) void k_glu_grad(GluArgs a) {
     du[i] = d[i] * g[i];
     u[i] *= g[i];
   }
-  *reinterpret_cast<v4i*>(a.dz + gate) = pack8(dg);
-  *reinterpret_cast<v4i*>(a.dz + up) = pack8(du);
-  if (a.h) *reinterpret_cast<v4i*>(a.h + at) = pack8(u);
+  store_row<NT>(a.dz + gate, pack8(dg));
+  store_row<NT>(a.dz + up, pack8(du));
+  if (a.h) store_row<NT>(a.h + at, pack8(u));
 }
 
+inline bool past_cache(const GluArgs& a) { return (int64_t)a.R * 2 * a.I > kCachedRows; }
 inline dim3 grid_of(const GluArgs& a) { return grid_of_blocks(ceil_div((int64_t)a.R * (a.I / 8), kGluThreads)); }
 
 }  // namespace
@@ -110,15 +111,17 @@ inline dim3 grid_of(const GluArgs& a) { return grid_of_blocks(ceil_div((int64_t)
 hipError_t launch_glu(const moe_glu_dims& d, const uint16_t* z, const int32_t* live, uint16_t* h, uint8_t* z_q,
                       uint8_t* z_s, hipStream_t s) {
   const GluArgs a{z, nullptr, live, h, nullptr, z_q, z_s, d.R, d.I, d.act};
-  hipLaunchKernelGGL(k_glu, grid_of(a), dim3(kGluThreads), 0, s, a);
+  if (past_cache(a)) hipLaunchKernelGGL(k_glu<true>, grid_of(a), dim3(kGluThreads), 0, s, a);
+  else hipLaunchKernelGGL(k_glu<false>, grid_of(a), dim3(kGluThreads), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_glu_grad(const moe_glu_dims& d, const uint16_t* dh, const uint16_t* z, const uint8_t* z_q,
                            const uint8_t* z_s, const int32_t* live, uint16_t* dz, uint16_t* h, hipStream_t s) {
   const GluArgs a{z, dh, live, h, dz, const_cast<uint8_t*>(z_q), const_cast<uint8_t*>(z_s), d.R, d.I, d.act};
-  if (z) hipLaunchKernelGGL(k_glu_grad<false>, grid_of(a), dim3(kGluThreads), 0, s, a);
-  else hipLaunchKernelGGL(k_glu_grad<true>, grid_of(a), dim3(kGluThreads), 0, s, a);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid_of(a), dim3(kGluThreads), 0, s, a); };
+  if (past_cache(a)) z ? go(k_glu_grad<false, true>) : go(k_glu_grad<true, true>);
+  else z ? go(k_glu_grad<false, false>) : go(k_glu_grad<true, false>);
   return hipGetLastError();
 }
 

@@ -12,6 +12,8 @@
 #include "lane_reduce.h"
 #include "rows.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -32,7 +34,8 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) 
     unpack8(load16(static_cast<const uint16_t*>(p) + at), v);
   }
 }
-// A thread's 8 columns of a token: `g` counts groups of 8 over all tokens.
+
+// A thread's 8 columns of a token.
 struct Place {
   int64_t t;
   int c8;   // group within the row
@@ -53,7 +56,8 @@ struct SortArgs {
   int T, H, K;
 };
 
-template <bool CODES>
+// From codes the stores stay cached whatever the size (16K tokens 364 us, nontemporal 378).
+template <bool CODES, bool NT>
 __global__ __launch_bounds__(kRowThreads) void k_sort_rows(SortArgs a) {
   const int groups = a.H / 8;
   const Place p = place_of(groups);
@@ -75,7 +79,7 @@ __global__ __launch_bounds__(kRowThreads) void k_sort_rows(SortArgs a) {
   const int32_t* rows = a.pair_rows + p.t * a.K;
   for (int j = 0; j < a.K; ++j) {
     const uint32_t r = (uint32_t)rows[j];   // -1 is no row
-    if (r < a.P) *reinterpret_cast<v4i*>(a.rows + (int64_t)r * a.H + 8 * p.c8) = v;
+    if (r < a.P) store_row<NT>(a.rows + (int64_t)r * a.H + 8 * p.c8, v);
   }
 }
 
@@ -91,7 +95,7 @@ struct ReturnArgs {
 
 constexpr int kPicks = 8;   // rows on their way at once
 
-template <bool F32>
+template <bool F32, bool NT>
 __global__ __launch_bounds__(kRowThreads) void k_return_rows(ReturnArgs a) {
   const int groups = a.H / 8;
   const Place p = place_of(groups);
@@ -127,10 +131,10 @@ __global__ __launch_bounds__(kRowThreads) void k_return_rows(ReturnArgs a) {
   }
   if constexpr (F32) {
     float* y = static_cast<float*>(a.y) + at;
-    *reinterpret_cast<v4f*>(y) = v4f{acc[0], acc[1], acc[2], acc[3]};
-    *reinterpret_cast<v4f*>(y + 4) = v4f{acc[4], acc[5], acc[6], acc[7]};
+    store_row<NT>(reinterpret_cast<uint16_t*>(y), __builtin_bit_cast(v4i, v4f{acc[0], acc[1], acc[2], acc[3]}));
+    store_row<NT>(reinterpret_cast<uint16_t*>(y + 4), __builtin_bit_cast(v4i, v4f{acc[4], acc[5], acc[6], acc[7]}));
   } else {
-    *reinterpret_cast<v4i*>(static_cast<uint16_t*>(a.y) + at) = pack8(acc);
+    store_row<NT>(static_cast<uint16_t*>(a.y) + at, pack8(acc));
   }
 }
 
@@ -146,7 +150,7 @@ struct ReturnGradArgs {
 };
 
 // A wave per pick: its row's dot product with the token's gradient in lane sums.
-template <bool F32>
+template <bool F32, bool NT>
 __global__ __launch_bounds__(kRowThreads) void k_return_rows_grad(ReturnGradArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t pair = block_id() * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -170,13 +174,25 @@ __global__ __launch_bounds__(kRowThreads) void k_return_rows_grad(ReturnGradArgs
       if (a.d_rows) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) dy[i] *= w;
-        *reinterpret_cast<v4i*>(a.d_rows + row + c) = pack8(dy);
+        store_row<NT>(a.d_rows + row + c, pack8(dy));
       }
     }
   }
   if (a.d_w) {
     dot = row_sum<64>(dot);
     if (lane == 0) a.d_w[pair] = dot;
+  }
+}
+
+// f<fp32, nontemporal>()
+template <typename F>
+void by_kind(bool f32, bool nt, F f) {
+  if (f32) {
+    if (nt) f(std::true_type{}, std::true_type{});
+    else f(std::true_type{}, std::false_type{});
+  } else {
+    if (nt) f(std::false_type{}, std::true_type{});
+    else f(std::false_type{}, std::false_type{});
   }
 }
 
@@ -188,8 +204,9 @@ hipError_t launch_sort_rows(int T, int H, int K, const void* x, const uint8_t* x
                             uint16_t* rows, hipStream_t s) {
   const SortArgs a{x, x_s, pair_rows, rows, (int64_t)T * K, T, H, K};
   const dim3 grid = token_groups(T, H), block(kRowThreads);
-  if (x_s) hipLaunchKernelGGL(k_sort_rows<true>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(k_sort_rows<false>, grid, block, 0, s, a);
+  if (x_s) hipLaunchKernelGGL((k_sort_rows<true, false>), grid, block, 0, s, a);
+  else if (a.P * H > kCachedRows) hipLaunchKernelGGL((k_sort_rows<false, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_sort_rows<false, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -197,8 +214,9 @@ hipError_t launch_return_rows(int T, int H, int K, const uint16_t* rows, const i
                               const void* add, bool f32, void* y, hipStream_t s) {
   const ReturnArgs a{rows, pair_rows, w, add, y, (int64_t)T * K, T, H, K};
   const dim3 grid = token_groups(T, H), block(kRowThreads);
-  if (f32) hipLaunchKernelGGL(k_return_rows<true>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(k_return_rows<false>, grid, block, 0, s, a);
+  by_kind(f32, a.P * H > kCachedRows, [&](auto f, auto nt) {
+    hipLaunchKernelGGL((k_return_rows<decltype(f)::value, decltype(nt)::value>), grid, block, 0, s, a);
+  });
   return hipGetLastError();
 }
 
@@ -207,8 +225,9 @@ hipError_t launch_return_rows_grad(int T, int H, int K, const void* dy, bool f32
                                    hipStream_t s) {
   const ReturnGradArgs a{dy, rows, pair_rows, w, d_rows, d_w, (int64_t)T * K, T, H, K};
   const dim3 grid = grid_of_blocks(ceil_div(a.P, kRowThreads / 64)), block(kRowThreads);
-  if (f32) hipLaunchKernelGGL(k_return_rows_grad<true>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(k_return_rows_grad<false>, grid, block, 0, s, a);
+  by_kind(f32, a.P * H > kCachedRows, [&](auto f, auto nt) {
+    hipLaunchKernelGGL((k_return_rows_grad<decltype(f)::value, decltype(nt)::value>), grid, block, 0, s, a);
+  });
   return hipGetLastError();
 }
 
