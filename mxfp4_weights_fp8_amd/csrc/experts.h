@@ -18,6 +18,7 @@ struct ExpertArgs {
   const int4* list;      // the tiled kernel's
   int64_t w_expert;      // elements of one expert's matrix
   int P, E, D, O, ws;
+  int splits;            // of the contraction; with more than one, y is [splits, P, O] fp32 parts
 };
 
 // dW[e][n, c] = sum over the rows r of expert e of dy[r, n] x[r, c]
@@ -28,6 +29,7 @@ struct ExpertGradArgs {
   void* dw;              // [E, N, C] bf16 or fp32
   const int32_t* order;  // [E] experts, those with the most rows first
   int P, E, N, C;
+  int splits;            // of every expert's rows; with more than one, dw is [splits, E, N, C] fp32 parts
 };
 
 // Rows [lo, hi) of expert e, inside the buffers whatever the offsets hold.
@@ -40,6 +42,7 @@ __device__ __forceinline__ RowRange rows_of(int at, int next, int P) {
 }
 
 constexpr int kTileRows = 256;   // most rows of a tile
+int tile_fragments(int cols);    // the tiles are 32 times as many columns (rows) wide
 inline int64_t expert_tiles_bound(int64_t P, int64_t E) { return P / kTileRows + (P < E ? P : E); }
 
 void launch_expert_tiles(const ExpertArgs& a, bool w_trans, bool f32, hipStream_t s);

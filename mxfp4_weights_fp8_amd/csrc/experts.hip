@@ -9,6 +9,7 @@
 #include "experts.h"
 #include "linear.h"
 #include "lane_reduce.h"
+#include "rows.h"
 
 #include <math.h>
 
@@ -260,41 +261,141 @@ __global__ __launch_bounds__(kListThreads) void k_expert_list(const int32_t* off
 
 // Which kernel: the least estimated time, in us, with as many experts at work as a mildly
 // uneven router gives P picks. k_expert_few streams weights at 5.3 TB/s, pays for every
-// workgroup of 16 columns (4.5 ns with all CUs at it) and for its rows (110 TFLOP/s, partly
-// hidden); the tiles stream at 5.2 TB/s behind the list, but a tile takes 0.75 us per step
-// however few rows it has. k_expert_few and tiles, in us:
+// workgroup of 16 columns (4.5 ns with all CUs at it), for its steps (their loads of x keep
+// a CU busy for 0.08 to 0.25 us) and for its rows (110 TFLOP/s, partly hidden); the tiles
+// stream at 5.2 TB/s behind the list, but a tile takes 0.75 us per step however few rows it
+// has. k_expert_few and tiles (with an unsplit contraction), in us:
 //   768 x 7168, 384 experts, 8 rows 13 and 76, 56 rows 78 and 135, 208 rows 156 and 160, 512
 //   rows 319 and 327, 1363 rows 730 and 785, 5945 rows 1084 and 802
 //   7168 x 384, 384 experts, 8 rows 11 and 14, 56 rows 68 and 41, 512 rows 429 and 170
 //   4096 x 4096, 16 experts, 2 rows 15 and 44, 64 rows 90 and 120, 256 rows 141 and 129
 //   1024 x 2048, 64 experts, 32 rows 14 and 28, 222 rows 54 and 46, 992 rows 80 and 53
 //   512 x 256, 8 experts, 3 rows 7 and 11, 959 rows 7 and 16; 1024 x 512, 2048 rows 25 and 21
-inline bool few(const moe_expert_dims& d) {
-  const double rows = d.P, matrix = (double)d.N * d.K, steps = d.K / 64;
-  const double experts = fmax(1.0, d.E * (1.0 - exp(-0.65 * rows / d.E))), bytes = 2.0 * experts * matrix;
-  const double column_tiles = (double)ceil_div(d.N, kTileRows), row_tiles = fmax(experts, rows / kTileRows);
-  const double rounds = ceil(row_tiles * column_tiles / 256);
-  const double tiles = 8 + fmax(bytes / 5.2e6, 0.75 * rounds * steps) + 0.2 * steps;
-  const double units = experts + rows / kFewRows;
-  return 6 + fmax(bytes / 5.3e6, 0.0045 * units * (d.N / 16)) + 1.2 * rows * matrix / 1.1e8 <= tiles;
+struct Estimate {
+  double us;
+  int splits;
+};
+// Experts at work, of E that P picks go to.
+inline double at_work(double P, double E) { return fmax(1.0, E * (1.0 - exp(-0.65 * P / E))); }
+
+// The tiles' product, its contraction of D split over workgroups where there are fewer
+// tiles than CUs: each part at least 8 steps, joined at 4 TB/s. Unsplit and split: 8
+// experts of 64 rows x 768 x 7168 65 and 31 us, of 200 x 1024 x 2048 49 and 35; as dx 8 of 128
+// rows x 384 from 7168 columns 89 and 27.
+inline Estimate tiles_estimate(double P, double E, int D, int O) {
+  const double experts = at_work(P, E), steps = D / 64, rows = P / experts;
+  const double tiles = fmax(experts, P / kTileRows) * (double)ceil_div(O, 32 * tile_fragments(O));
+  const double step = 0.75 + 0.85 * fmin(1.0, rows / kTileRows);
+  Estimate best{1e30, 1};
+  for (int k = 1; k == 1 || (k <= steps / 8 && tiles * k <= 512); k += k < 8 ? 1 : k / 4) {
+    const double t = 8 + fmax(2.0 * experts * D * O / 5.2e6, step * ceil(tiles * k / 256) * ceil(steps / k)) +
+                     0.2 * steps / k + (k > 1 ? 4 + k * P * O * 8 / 4e6 : 0);
+    if (t < best.us) best = Estimate{t, k};
+  }
+  return best;
 }
 
-inline size_t list_bytes(const moe_expert_dims& d) { return sizeof(int4) * (size_t)(1 + expert_tiles_bound(d.P, d.E)); }
-inline size_t order_bytes(const moe_expert_dims& d) { return align_up(sizeof(int32_t) * (size_t)d.E, 16); }
+inline bool few(const moe_expert_dims& d) {
+  const double rows = d.P, matrix = (double)d.N * d.K, experts = at_work(rows, d.E);
+  const double workgroups = (experts + rows / kFewRows) * (d.N / 16), per_expert = rows / experts;
+  const double turn = per_expert > 32 ? 0.25 : per_expert > 16 ? 0.15 : 0.08;   // us of a workgroup's step
+  const double t = 6 + fmax(fmax(2.0 * experts * matrix / 5.3e6, 0.0045 * workgroups),
+                            turn * (d.K / 64) * ceil(workgroups / 256)) + 1.2 * rows * matrix / 1.1e8;
+  return t <= tiles_estimate(rows, d.E, d.K, d.N).us;
+}
+
+// Splits of every expert's rows for the weights' gradient: as many as fill the CUs, where
+// the weights are few, each at least 4 steps of an average expert. Unsplit and split: one
+// expert of 65536 rows, 128 x 128 617 and 24 us, of 20000, 512 x 512 452 and 40, four of 5000,
+// 256 x 256 122 and 26.
+inline int wgrad_splits(const moe_expert_dims& d) {
+  const double tiles = (double)d.E * ceil_div(d.N, 32 * tile_fragments(d.N)) * ceil_div(d.K, 32 * tile_fragments(d.K));
+  const double steps = ceil((double)d.P / d.E / 64), elements = (double)d.E * d.N * d.K;
+  double least = 1e30;
+  int best = 1;
+  for (int k = 1; k == 1 || (k <= steps / 4 && tiles * k <= 512); k += k < 8 ? 1 : k / 4) {
+    const double t = 1.6 * ceil(tiles * k / 256) * ceil(steps / k) + (k > 1 ? 4 + k * elements * 8 / 4e6 : 0);
+    if (t < least) {
+      least = t;
+      best = k;
+    }
+  }
+  return best;
+}
+
+// out[i] = sum over the parts, of [P, O] results for the rows that experts have. A
+// workgroup joins 256 elements, four per lane: each of its waves adds every waves-th part,
+// eight loads on their way, then their sums are added in wave order.
+constexpr int kJoinWaves = 16;
+template <bool F32>
+__global__ __launch_bounds__(64 * kJoinWaves) void k_expert_join(const float* parts, int splits, int64_t n, void* out,
+                                                                 const int32_t* off, int E, int P, int O) {
+  __shared__ v4f sums[kJoinWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int64_t at = 4 * (block_id() * 64 + lane);
+  bool mine = at < n;
+  if (off) {
+    const RowRange r = rows_of(off[0], off[E], P);
+    mine = at >= (int64_t)r.lo * O && at < (int64_t)r.hi * O;
+  }
+  v4f v{0.f, 0.f, 0.f, 0.f};
+  if (mine) {
+#pragma unroll 8
+    for (int k = wave; k < splits; k += waves) v += *reinterpret_cast<const v4f*>(parts + k * n + at);
+  }
+  if (waves > 1) {
+    sums[wave][lane] = v;
+    __syncthreads();
+    if (wave > 0) return;
+    for (int w = 1; w < waves; ++w) v += sums[w][lane];
+  }
+  if (!mine) return;
+  if constexpr (F32) *reinterpret_cast<v4f*>(static_cast<float*>(out) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+        make_uint2(bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]));
+}
+
+void launch_join(const float* parts, int splits, int64_t n, void* out, bool f32, const int32_t* off, int E, int P, int O,
+                 hipStream_t s) {
+  const int waves = splits < 8 ? 1 : splits < 32 ? 4 : kJoinWaves;
+  const dim3 grid = grid_of_blocks(ceil_div(n, 256)), block(64 * waves);
+  if (f32) hipLaunchKernelGGL(k_expert_join<true>, grid, block, 0, s, parts, splits, n, out, off, E, P, O);
+  else hipLaunchKernelGGL(k_expert_join<false>, grid, block, 0, s, parts, splits, n, out, off, E, P, O);
+}
+
+inline size_t list_bytes(const moe_expert_dims& d) {
+  return align_up(sizeof(int4) * (size_t)(1 + expert_tiles_bound(d.P, d.E)), 256);
+}
+inline size_t order_bytes(const moe_expert_dims& d) { return align_up(sizeof(int32_t) * (size_t)d.E, 256); }
+inline size_t parts_bytes(int splits, int64_t elements) { return splits > 1 ? sizeof(float) * splits * elements : 0; }
 
 void launch_list(const moe_expert_dims& d, const int32_t* off, int4* list, int32_t* order, hipStream_t s) {
   hipLaunchKernelGGL(k_expert_list, dim3(1), dim3(kListThreads), 0, s, off, d.E, d.P, list,
                      (int)expert_tiles_bound(d.P, d.E), order);
 }
 
+// A product in tiles along the list, into parts where its contraction is split.
+void launch_tiled(ExpertArgs a, bool w_trans, bool f32, float* parts, hipStream_t s) {
+  a.splits = tiles_estimate(a.P, a.E, a.D, a.O).splits;
+  if (a.splits == 1) return launch_expert_tiles(a, w_trans, f32, s);
+  void* const y = a.y;
+  a.y = parts;
+  launch_expert_tiles(a, w_trans, true, s);
+  launch_join(parts, a.splits, (int64_t)a.P * a.O, y, f32, a.off, a.E, a.P, a.O, s);
+}
+
 }  // namespace
 
-size_t expert_linear_ws_bytes(const moe_expert_dims& d) { return few(d) ? 0 : list_bytes(d); }
+size_t expert_linear_ws_bytes(const moe_expert_dims& d) {
+  if (few(d)) return 0;
+  return list_bytes(d) + parts_bytes(tiles_estimate(d.P, d.E, d.K, d.N).splits, (int64_t)d.P * d.N);
+}
 
 hipError_t launch_expert_linear(const moe_expert_dims& d, const uint16_t* x, const uint16_t* w, const int32_t* off,
                                 void* y, void* ws, hipStream_t s) {
   const bool f32 = d.type == MOE_TYPE_F32;
-  const ExpertArgs a{x, w, off, y, static_cast<const int4*>(ws), (int64_t)d.N * d.K, d.P, d.E, d.K, d.N, d.K};
+  const ExpertArgs a{x, w, off, y, static_cast<const int4*>(ws), (int64_t)d.N * d.K, d.P, d.E, d.K, d.N, d.K, 1};
   if (few(d)) {
     const int64_t units = d.P / kFewRows + (d.P < d.E ? d.P : d.E);
     const int waves = d.K / 64 < kFewWaves ? d.K / 64 : kFewWaves;
@@ -303,24 +404,34 @@ hipError_t launch_expert_linear(const moe_expert_dims& d, const uint16_t* x, con
     else hipLaunchKernelGGL(k_expert_few<false>, grid, block, 0, s, a);
   } else {
     launch_list(d, off, static_cast<int4*>(ws), nullptr, s);
-    launch_expert_tiles(a, false, f32, s);
+    launch_tiled(a, false, f32, reinterpret_cast<float*>(static_cast<char*>(ws) + list_bytes(d)), s);
   }
   return hipGetLastError();
 }
 
-size_t expert_linear_grad_ws_bytes(const moe_expert_dims& d) { return order_bytes(d) + list_bytes(d); }
+size_t expert_linear_grad_ws_bytes(const moe_expert_dims& d) {   // the two products run one after the other
+  const size_t x = d.P ? parts_bytes(tiles_estimate(d.P, d.E, d.N, d.K).splits, (int64_t)d.P * d.K) : 0;
+  const size_t w = parts_bytes(wgrad_splits(d), (int64_t)d.E * d.N * d.K);
+  return order_bytes(d) + list_bytes(d) + (x > w ? x : w);
+}
 
 hipError_t launch_expert_linear_grad(const moe_expert_dims& d, const uint16_t* dy, const uint16_t* x, const uint16_t* w,
                                      const int32_t* off, uint16_t* dx, void* dw, void* ws, hipStream_t s) {
   int32_t* const order = static_cast<int32_t*>(ws);
   int4* const list = reinterpret_cast<int4*>(static_cast<char*>(ws) + order_bytes(d));
-  if (!(dx && d.P > 0) && !dw) return hipSuccess;
+  float* const parts = reinterpret_cast<float*>(static_cast<char*>(ws) + order_bytes(d) + list_bytes(d));
+  if (d.P == 0) dx = nullptr;
+  if (!dx && !dw) return hipSuccess;
   launch_list(d, off, dx ? list : nullptr, dw ? order : nullptr, s);
-  if (dx && d.P > 0) {   // [P, K] = dy [P, N] . w [E, N, K], contracted over N
-    const ExpertArgs a{dy, w, off, dx, list, (int64_t)d.N * d.K, d.P, d.E, d.N, d.K, d.K};
-    launch_expert_tiles(a, true, false, s);
+  if (dx)   // [P, K] = dy [P, N] . w [E, N, K], contracted over N
+    launch_tiled(ExpertArgs{dy, w, off, dx, list, (int64_t)d.N * d.K, d.P, d.E, d.N, d.K, d.K, 1}, true, false, parts, s);
+  if (dw) {
+    const bool f32 = d.type == MOE_TYPE_F32;
+    const int splits = wgrad_splits(d);
+    launch_expert_wgrad(ExpertGradArgs{dy, x, off, splits > 1 ? parts : dw, order, d.P, d.E, d.N, d.K, splits},
+                        f32 || splits > 1, s);
+    if (splits > 1) launch_join(parts, splits, (int64_t)d.E * d.N * d.K, dw, f32, nullptr, 0, 0, 0, s);
   }
-  if (dw) launch_expert_wgrad(ExpertGradArgs{dy, x, off, dw, order, d.P, d.E, d.N, d.K}, d.type == MOE_TYPE_F32, s);
   return hipGetLastError();
 }
 

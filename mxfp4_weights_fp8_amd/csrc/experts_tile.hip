@@ -59,6 +59,10 @@ __device__ __forceinline__ void mma_done() {
 typedef const __attribute__((address_space(4))) int32_t* const_ints;
 __device__ __forceinline__ const_ints as_const(const void* p) { return (const_ints)(uintptr_t)p; }
 
+// The quotient of two wave-uniform values, in a scalar register (the division itself is done
+// by the vector unit).
+__device__ __forceinline__ int uniform_div(int a, int b) { return __builtin_amdgcn_readfirstlane(a / b); }
+
 // Where a wave stores its part of a tile: `base` the tile's first row, `rows` of them.
 struct OutTile {
   rsrc_t r;
@@ -284,25 +288,29 @@ __global__ __launch_bounds__(kThreads, 1) void k_expert_tile(ExpertArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kSmem];
   const const_ints list = as_const(a.list);
   const int row_tiles = list[0], n_tiles = (a.O + 32 * FW - 1) / (32 * FW), steps = a.D / 64;
-  const int end = row_tiles * n_tiles, stride = gridDim.x;
+  const int tiles = row_tiles * n_tiles, end = tiles * a.splits, stride = gridDim.x;
   const int begin = blockIdx.x % kXcds * (stride / kXcds) + blockIdx.x / kXcds;
   if (begin >= end) return;
 
   struct Tile {
-    int expert, row0, rows, n0;
+    int expert, row0, rows, n0, split, s0, s1;
   };
   auto tile_of = [&](int id) {
-    const int group = id / (kGroup * n_tiles), in = id % (kGroup * n_tiles);
+    const int split = uniform_div(id, tiles), in_split = id - split * tiles;
+    const int group = uniform_div(in_split, kGroup * n_tiles), in = in_split - group * kGroup * n_tiles;
     const int in_group = min(kGroup, row_tiles - group * kGroup);
-    const int mt = group * kGroup + in % in_group;
-    return Tile{list[4 * mt + 4], list[4 * mt + 5], list[4 * mt + 6], in / in_group * 32 * FW};
+    const int nt = uniform_div(in, in_group), mt = group * kGroup + in - nt * in_group;
+    return Tile{list[4 * mt + 4], list[4 * mt + 5], list[4 * mt + 6], nt * 32 * FW, split,
+                uniform_div(steps * split, a.splits), uniform_div(steps * (split + 1), a.splits)};
   };
 
   S st;
   st.init(smem, a.D, a.ws);
-  int at = begin, step = 0;   // what is copied next
+  int at = begin, step = 0, stop = 0;   // what is copied next, up to which step
   auto place = [&]() {
     const Tile t = tile_of(min(at, end - 1));
+    step = t.s0;
+    stop = t.s1;
     st.oa.place(a.x, a.D, t.row0, t.row0 + t.rows, a.D);
     st.ob.place(a.w + t.expert * a.w_expert, a.ws, t.n0, a.O, a.D);
   };
@@ -310,8 +318,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_expert_tile(ExpertArgs a) {
   auto next = [&](v4i_s& sa, v4i_s& sb) {
     sa = st.oa.rsrc(step, at < end);
     sb = st.ob.rsrc(step, at < end);
-    if (++step == steps) {
-      step = 0;
+    if (++step == stop) {
       at += stride;
       place();
     }
@@ -320,10 +327,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_expert_tile(ExpertArgs a) {
   for (int id = begin; id < end; id += stride) {
     const Tile t = tile_of(id);
     OutTile o;
-    o.place<F32>(a.y, t.row0, t.rows, t.n0, a.O);
+    o.place<F32>(static_cast<char*>(a.y) + (int64_t)t.split * a.P * a.O * 4, t.row0, t.rows, t.n0, a.O);   // split 0 in bf16
     auto go = [&](auto ft) {
       constexpr int FT = decltype(ft)::value;
-      st.template tile<FT>(steps, next);
+      st.template tile<FT>(t.s1 - t.s0, next);
       st.template store<FT>(o);
     };
     if (t.rows > 128) go(std::integral_constant<int, 8>{});
@@ -339,21 +346,27 @@ __global__ __launch_bounds__(kThreads, 1) void k_expert_wgrad(ExpertGradArgs a) 
   typedef Stream<FT, FW, true, true, F32> S;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kSmem];
   const int m_tiles = (a.N + 32 * FT - 1) / (32 * FT), n_tiles = (a.C + 32 * FW - 1) / (32 * FW);
-  const int per = m_tiles * n_tiles, parts = min(kXcds, per), len = (per + parts - 1) / parts;
+  const int tiles = m_tiles * n_tiles, per = tiles * a.splits;   // of an expert
+  const int parts = min(kXcds, per), len = (per + parts - 1) / parts;
   const int xcd = blockIdx.x % kXcds, stride = gridDim.x / kXcds;
   const int end = len * ((a.E * parts - xcd + kXcds - 1) / kXcds);   // this XCD's parts
   const const_ints off = as_const(a.off), order = as_const(a.order);
 
   struct Tile {
-    int expert, m0, n0, lo, hi, steps;
+    int expert, m0, n0, lo, hi, steps, split;
   };
-  // tile i of this XCD: part i / len of its parts; expert -1 where a part is short
+  // tile i of this XCD: part i / len of its parts; expert -1 where a part is short. Rows
+  // [lo, hi), none where a split has no step: then its one step reads zeros.
   auto tile_of = [&](int i) {
-    const int part = i / len * kXcds + xcd, k = part % parts * len + i % len;
-    if (i >= end || k >= per) return Tile{-1, 0, 0, 0, 0, 0};
-    const int e = order[part / parts];
+    const int run = uniform_div(i, len), part = run * kXcds + xcd, at = uniform_div(part, parts);
+    const int k = (part - at * parts) * len + i - run * len;
+    if (i >= end || k >= per) return Tile{-1, 0, 0, 0, 0, 0, 0};
+    const int e = order[at], split = uniform_div(k, tiles), t = k - split * tiles, nt = uniform_div(t, m_tiles);
     const int lo = min(max(off[e], 0), a.P), hi = min(max(off[e + 1], lo), a.P);
-    return Tile{e, k % m_tiles * 32 * FT, k / m_tiles * 32 * FW, lo, hi, max((hi - lo + 63) / 64, 1)};
+    const int steps = (hi - lo + 63) / 64;
+    const int s0 = uniform_div(steps * split, a.splits), s1 = uniform_div(steps * (split + 1), a.splits);
+    return Tile{e, (t - nt * m_tiles) * 32 * FT, nt * 32 * FW, lo + 64 * s0, min(hi, lo + 64 * s1), max(s1 - s0, 1),
+                split};
   };
   int id = blockIdx.x / kXcds;
   auto skip = [&](int& i) {   // to the next tile that there is
@@ -389,7 +402,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_expert_wgrad(ExpertGradArgs a) 
   st.start(next);
   while (now.expert >= 0) {
     OutTile o;
-    o.place<F32>(static_cast<char*>(a.dw) + (int64_t)now.expert * a.N * a.C * (F32 ? 4 : 2), now.m0,
+    o.place<F32>(static_cast<char*>(a.dw) + ((int64_t)now.split * a.E + now.expert) * a.N * a.C * (F32 ? 4 : 2), now.m0,
                  min(32 * FT, a.N - now.m0), now.n0, a.C);
     st.template tile<FT>(now.steps, next);
     st.template store<FT>(o);
@@ -401,7 +414,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_expert_wgrad(ExpertGradArgs a) 
 
 template <int FW, bool WT>
 void run_tiles(const ExpertArgs& a, bool f32, hipStream_t s) {
-  const int64_t most = expert_tiles_bound(a.P, a.E) * ceil_div(a.O, 32 * FW);
+  const int64_t most = expert_tiles_bound(a.P, a.E) * ceil_div(a.O, 32 * FW) * a.splits;
   const dim3 grid((unsigned)(most < kCus ? ceil_div(most, kXcds) * kXcds : kCus)), block(kThreads);
   if (f32) hipLaunchKernelGGL((k_expert_tile<FW, WT, true>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((k_expert_tile<FW, WT, false>), grid, block, 0, s, a);
@@ -413,17 +426,17 @@ void run_wgrad(const ExpertGradArgs& a, bool f32, hipStream_t s) {
   else hipLaunchKernelGGL((k_expert_wgrad<FT, FW, false>), dim3(kCus), dim3(kThreads), 0, s, a);
 }
 
+}  // namespace
+
 // Columns of a tile: 256, unless 192 or 128 fill the last one so much better that more
 // tiles cost less (a step of 64 of 256 columns takes 1.70 us, of 192 1.45, of 128 1.2).
-int fragments(int cols) {
+int tile_fragments(int cols) {
   const int64_t t8 = 170 * ceil_div(cols, 256), t6 = 145 * ceil_div(cols, 192), t4 = 120 * ceil_div(cols, 128);
   return t8 <= t6 && t8 <= t4 ? 8 : t6 <= t4 ? 6 : 4;
 }
 
-}  // namespace
-
 void launch_expert_tiles(const ExpertArgs& a, bool w_trans, bool f32, hipStream_t s) {
-  const int fw = fragments(a.O);
+  const int fw = tile_fragments(a.O);
   if (w_trans) {
     if (fw == 8) run_tiles<8, true>(a, f32, s);
     else if (fw == 6) run_tiles<6, true>(a, f32, s);
@@ -436,7 +449,7 @@ void launch_expert_tiles(const ExpertArgs& a, bool w_trans, bool f32, hipStream_
 }
 
 void launch_expert_wgrad(const ExpertGradArgs& a, bool f32, hipStream_t s) {
-  const int ft = fragments(a.N), fw = fragments(a.C);
+  const int ft = tile_fragments(a.N), fw = tile_fragments(a.C);
   if (ft == 8) {
     if (fw == 8) run_wgrad<8, 8>(a, f32, s);
     else if (fw == 6) run_wgrad<8, 6>(a, f32, s);

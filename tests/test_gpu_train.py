@@ -289,6 +289,21 @@ def test_products_of_many_tiles(dev, sizes, N, C):
     check_products(dev, sizes, N, C, seed=N)
 
 
+# few tiles: the contraction of the product, of dx (over N), of dw (over the rows) in parts
+@pytest.mark.parametrize("sizes,N,C,split", [
+    ([300], 256, 7168, "y"), ([150, 0, 200, 160, 3], 256, 7168, "y"), ([700], 7168, 128, "dx"), ([90, 300, 0, 257], 4096, 256, "dx"),
+    ([3000], 128, 128, "dw"), ([5000, 0, 130, 700], 128, 256, "dw"), ([20000, 1], 256, 128, "dw"), ([64 * 40 + 1], 384, 128, "dw")])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_products_in_parts(dev, sizes, N, C, split, dtype):
+    P, E = sum(sizes) + 5, len(sizes)
+    d = moe.ExpertDims(P, N, C, E, 0)
+    if split == "y":
+        assert moe.lib().moe_expert_linear_workspace_bytes(d) > 8 * P * N
+    else:
+        assert moe.lib().moe_expert_linear_grad_workspace_bytes(d) > 8 * (P * C if split == "dx" else E * N * C)
+    check_products(dev, sizes, N, C, behind=5, dtype=dtype, seed=N + C)
+
+
 def test_products_with_most_experts(dev):
     for sizes in ([(7 * i) % 41 for i in range(4096)], [i % 2 for i in range(4096)]):
         check_products(dev, sizes, 128, 128, behind=11)
