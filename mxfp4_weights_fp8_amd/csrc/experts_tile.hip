@@ -33,7 +33,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kXcds = 8;
 constexpr int kCus = 256;
-constexpr int kGroup = 8;   // row tiles that share a pass over the column tiles
+constexpr int kGroup = 4;   // row tiles that share a pass over the column tiles
 constexpr int kAStages = 2, kBStages = 3;
 
 // acc += A B, or acc = A B (FIRST, which saves writing zeros: 5 % of a tile of three
