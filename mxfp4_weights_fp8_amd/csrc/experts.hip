@@ -163,11 +163,13 @@ __global__ __launch_bounds__(kListThreads) void k_expert_list(const int32_t* off
   if (list) {
     // Each thread's kPer experts: tall tiles, and a last one of middle or small size.
     RowRange r[kPer];
-    int tall[kPer], n[3] = {0, 0, 0};
+    int tall[kPer], n[3] = {0, 0, 0}, disorder = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = tid * kPer + i;
-      r[i] = e < E ? rows_of(off[e], off[e + 1], P) : RowRange{0, 0};
+      const int lo = e < E ? off[e] : 0, hi = e < E ? off[e + 1] : 0;
+      disorder |= lo < 0 || hi < lo || hi > P;
+      r[i] = RowRange{lo, hi};
       const int rows = r[i].hi - r[i].lo, last = rows % kTileRows;
       const bool apart = last <= 128 && !(together && rows >= kTileRows);
       tall[i] = rows / kTileRows + (last > 0 && !apart);
@@ -182,7 +184,8 @@ __global__ __launch_bounds__(kListThreads) void k_expert_list(const int32_t* off
       if (lane == 63) waves[k][wave] = at[k];
       at[k] -= n[k];
     }
-    __syncthreads();
+    // Offsets that no plan gives: no tiles (what is counted here may then overflow).
+    const bool sound = !__syncthreads_or(disorder);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       total[k] = 0;
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(kListThreads) void k_expert_list(const int32_t* off
     at[2] += total[0] + total[1];
     auto write = [&](int t, int e, const RowRange& x, int k) {   // tile k of expert e at place t
       const int row0 = x.lo + k * kTileRows;
-      if (t < cap) list[1 + t] = make_int4(e, row0, min(kTileRows, x.hi - row0), 0);
+      if (sound && t < cap) list[1 + t] = make_int4(e, row0, min(kTileRows, x.hi - row0), 0);
     };
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -206,15 +209,15 @@ __global__ __launch_bounds__(kListThreads) void k_expert_list(const int32_t* off
       if (last > 0) write(last > 64 ? at[1]++ : at[2]++, tid * kPer + i, r[i], tall[i]);
     }
     __syncthreads();
-    if (tid == 0) list[0] = make_int4(min(total[0] + total[1] + total[2], cap), 0, 0, 0);
-    for (int t = tid; t < min(total[0], cap); t += kListThreads) {
+    if (tid == 0) list[0] = make_int4(sound ? min(total[0] + total[1] + total[2], cap) : 0, 0, 0, 0);
+    for (int t = tid; sound && t < min(total[0], cap); t += kListThreads) {
       int lo = 0, hi = E - 1;   // the first expert whose end is past t
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
         if (ends[mid] > t) hi = mid;
         else lo = mid + 1;
       }
-      write(t, lo, rows_of(off[lo], off[lo + 1], P), t - (lo ? ends[lo - 1] : 0));
+      write(t, lo, RowRange{off[lo], off[lo + 1]}, t - (lo ? ends[lo - 1] : 0));
     }
   }
   if (!order) return;

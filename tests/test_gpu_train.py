@@ -276,7 +276,7 @@ def test_products_of_few_rows(dev, sizes, N, C, dtype):
     ([100], 128, 128), ([64, 65, 127, 128, 129], 256, 128), ([255, 256, 257, 0, 1], 128, 256), ([0, 513, 0, 40], 384, 384),
     ([63, 0, 1025, 2], 640, 256), ([300, 700], 256, 1152), ([17] * 40, 384, 640), ([1, 900, 3], 896, 512),
     ([33, 190, 191, 192, 193], 768, 768), ([20] * 130, 128, 640), ([2100, 5], 256, 2304), ([130] * 20, 1280, 256),
-    ([400], 128, 3200)])
+    ([400], 128, 3200), ([300, 90, 0, 513, 33, 700], 2176, 128)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_products_in_tiles(dev, sizes, N, C, dtype):
     check_products(dev, with_filler(sizes, N, C), N, C, behind=37, dtype=dtype, seed=N + C)
