@@ -6,7 +6,9 @@
 //   return_grad  d_rows[r] = w[t, j] dy[t],  d_w[t, j] = <rows[r], dy[t]>
 // All three walk tokens, so that what a token has once is read once, whatever its K rows
 // are; every row has one pair, so each is written (read) once and nothing is added by
-// atomics. HBM-bound: all of a 32K chunk's traffic is whole rows.
+// atomics. HBM-bound, all of the traffic whole rows: 32768 tokens x 7168, top-8, by expert
+// 777 us (5.4 TB/s; from codes 366 us for half as many), back 716-750 us (5.7 TB/s), the
+// gradient of 8191 tokens 388 us (5.1 TB/s). 7 tokens 3.7 us, bound by the launch.
 #include "device_common.h"
 #include "host_internal.h"
 #include "lane_reduce.h"
@@ -149,7 +151,9 @@ struct ReturnGradArgs {
   int T, H, K;
 };
 
-// A wave per pick: its row's dot product with the token's gradient in lane sums.
+// A wave per pick: its row's dot product with the token's gradient in lane sums. The K waves
+// of a token read its gradient K times, from the caches: 1.16 GB come from HBM for 8191
+// tokens, 1.04 GB are rows and gradients read once.
 template <bool F32, bool NT>
 __global__ __launch_bounds__(kRowThreads) void k_return_rows_grad(ReturnGradArgs a) {
   const int lane = threadIdx.x & 63;
