@@ -151,22 +151,27 @@ struct ReturnGradArgs {
   int T, H, K;
 };
 
-// A wave per pick: its row's dot product with the token's gradient in lane sums. The K waves
-// of a token read its gradient K times, from the caches: 1.16 GB come from HBM for 8191
-// tokens, 1.04 GB are rows and gradients read once.
-template <bool F32, bool NT>
+// LANES lanes per pick, a wave or 16 (rows of up to kNarrow columns): its row's dot product
+// with the token's gradient in lane sums. A token's gradient is read K times, from the
+// caches: 1.16 GB come from HBM for 8191 tokens, 1.04 GB are rows and gradients read once.
+// A wave and 16 lanes per pick, top-4: 65317 x 72 86 and 32 us, 32768 x 256 49 and 29, x 512
+// 56 and 54.
+constexpr int kNarrow = 512;
+template <int LANES, bool F32, bool NT>
 __global__ __launch_bounds__(kRowThreads) void k_return_rows_grad(ReturnGradArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t pair = block_id() * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x % LANES;
+  int sub = threadIdx.x / LANES;
+  if constexpr (LANES == 64) sub = __builtin_amdgcn_readfirstlane(sub);
+  const int64_t pair = block_id() * (kRowThreads / LANES) + sub;
   if (pair >= a.P) return;
-  const int64_t t = pair / a.K;
+  const int64_t t = (uint32_t)pair / (uint32_t)a.K;   // P is below 2^28
   const uint32_t r = (uint32_t)a.pair_rows[pair];
   const bool ok = r < a.P;
   float dot = 0.f;
   if (ok) {
     const float w = a.w ? a.w[pair] : 1.f;
     const int64_t row = (int64_t)r * a.H;
-    for (int c = 8 * lane; c < a.H; c += 512) {
+    for (int c = 8 * lane; c < a.H; c += 8 * LANES) {
       float dy[8];
       load8<F32>(a.dy, t * a.H + c, dy);
       if (a.d_w) {
@@ -183,7 +188,7 @@ __global__ __launch_bounds__(kRowThreads) void k_return_rows_grad(ReturnGradArgs
     }
   }
   if (a.d_w) {
-    dot = row_sum<64>(dot);
+    dot = row_sum<LANES>(dot);
     if (lane == 0) a.d_w[pair] = dot;
   }
 }
@@ -228,9 +233,14 @@ hipError_t launch_return_rows_grad(int T, int H, int K, const void* dy, bool f32
                                    const int32_t* pair_rows, const float* w, uint16_t* d_rows, float* d_w,
                                    hipStream_t s) {
   const ReturnGradArgs a{dy, rows, pair_rows, w, d_rows, d_w, (int64_t)T * K, T, H, K};
-  const dim3 grid = grid_of_blocks(ceil_div(a.P, kRowThreads / 64)), block(kRowThreads);
+  const dim3 block(kRowThreads);
   by_kind(f32, a.P * H > kCachedRows, [&](auto f, auto nt) {
-    hipLaunchKernelGGL((k_return_rows_grad<decltype(f)::value, decltype(nt)::value>), grid, block, 0, s, a);
+    constexpr bool F = decltype(f)::value, N = decltype(nt)::value;
+    auto go = [&](auto kernel, int lanes) {
+      hipLaunchKernelGGL(kernel, grid_of_blocks(ceil_div(a.P, kRowThreads / lanes)), block, 0, s, a);
+    };
+    if (H <= kNarrow) go(k_return_rows_grad<16, F, N>, 16);
+    else go(k_return_rows_grad<64, F, N>, 64);
   });
   return hipGetLastError();
 }

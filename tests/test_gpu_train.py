@@ -78,7 +78,7 @@ def marked(dev, *shape, dtype=BF16):
 # ------------------------------------------------------------------- rows and back
 
 ROWS = [(1, 1, 8, 1), (1, 8, 7168, 4), (7, 8, 7168, 384), (3, 64, 128, 70), (33, 5, 1000, 9), (2, 2, 16384, 3),
-        (300, 4, 264, 8), (5, 9, 520, 4096), (129, 3, 1032, 2), (4100, 2, 136, 17)]
+        (300, 4, 264, 8), (5, 9, 520, 4096), (129, 3, 1032, 2), (4100, 2, 136, 17), (61, 7, 512, 12)]
 
 
 @pytest.mark.parametrize("T,K,H,E", ROWS)
@@ -148,8 +148,8 @@ def test_return_rows_and_its_gradient(dev, T, K, H, E, dtype):
         want[r] = v
     within(d_rows, want, want.abs() * (BF + 2 * U), "d_rows")
     assert bool((d_rows.cpu()[live:] == MARK).all())
-    # a lane adds H / 64 products one after another, then six levels of a tree
-    within(d_w, rdw, mag * (H / 64 + 16) * U, "d_weights")
+    # a lane of 64 (16 up to 512 columns) adds H / 64 (H / 16) products, then levels of a tree
+    within(d_w, rdw, mag * (H / (16 if H <= 512 else 64) + 16) * U, "d_weights")
     assert bool((d_w.cpu()[pr[:T * K].view(T, K) < 0] == 0).all())
     alone, none = moe.return_rows_grad(dy.to(dev), None, p, wd, need=(True, False))
     assert none is None and torch.equal(alone[:live], d_rows[:live])
