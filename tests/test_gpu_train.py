@@ -459,6 +459,67 @@ def test_glu_leaves_rows_of_no_expert(dev):
         moe.glu(zd[:live].contiguous(), p=p)
 
 
+def test_glu_past_32_bits(dev):
+    """More than 2^31 elements of h, 2^32 of z and dz: the first and the last rows."""
+    R, I = 131200, 16384
+    z = torch.zeros(R, 2 * I, dtype=BF16, device=dev)
+    dh = torch.zeros(R, I, dtype=BF16, device=dev)
+    at = [0, 1, 65535, 65536, R - 1]
+    assert R * I > 2 ** 31
+    some, d = randn(len(at), 2 * I, seed=1, scale=2.0, dtype=BF16), randn(len(at), I, seed=2, dtype=BF16)
+    z[at], dh[at] = some.to(dev), d.to(dev)
+    h, q, s = moe.glu(z)
+    rh = ot.glu_ref(some, "silu")
+    within(h[at], rh, glu_tol(some.to(F64), rh), "h")
+    check_saved(some, q[at], s[at], "glu")
+    assert int((h != 0).any(1).sum()) == len(at)
+    dz, h2 = moe.glu_grad(dh, q, scales=s, out=(z, None))
+    check_glu_grad(dz[at], h2[at], d, ot.restored_ref(q[at].cpu(), s[at].cpu()), "silu", "gradient")
+    assert int((dz != 0).any(1).sum()) == len(at)
+
+
+def test_binding_refuses_what_the_kernels_cannot_take(dev):
+    T, K, E, H, N = 6, 2, 3, 256, 128
+    p, _, _ = routed(dev, T, K, E, seed=1, H=H)
+    x, rows = randn(T, H, seed=1, dtype=BF16).to(dev), randn(T * K, H, seed=2, dtype=BF16).to(dev)
+    w, z = randn(E, N, H, seed=3, dtype=BF16).to(dev), randn(T * K, 2 * N, seed=4, dtype=BF16).to(dev)
+    q, s = moe.quant_act(x)
+    off = torch.zeros(T * H + 4, dtype=BF16, device=dev)[4:].view(T, H)        # 8 bytes past an aligned address
+    wrong = [
+        lambda: moe.sort_rows(x.float(), p), lambda: moe.sort_rows(rows, p), lambda: moe.sort_rows(x[:, ::2], p),
+        lambda: moe.sort_rows(q, p), lambda: moe.sort_rows(x, p, scales=s), lambda: moe.sort_rows(q, p, scales=s[:, :1]),
+        lambda: moe.sort_rows(x, p, rows=rows[:4]), lambda: moe.restore_act(q, s.t()), lambda: moe.restore_act(x, s),
+        lambda: moe.return_rows(x, p), lambda: moe.return_rows(rows, p, weights=torch.ones(T, K, dtype=BF16, device=dev)),
+        lambda: moe.return_rows(rows, p, add=x.float()), lambda: moe.return_rows(rows, p, dtype=torch.float16),
+        lambda: moe.return_rows_grad(x[1:], rows, p), lambda: moe.return_rows_grad(x, x, p),
+        lambda: moe.return_rows_grad(x.half(), rows, p),
+        lambda: moe.expert_linear(rows, w[:2], p), lambda: moe.expert_linear(x, w, p),
+        lambda: moe.expert_linear(rows, w.transpose(1, 2), p), lambda: moe.expert_linear(rows, w.float(), p),
+        lambda: moe.expert_linear_grad(z, rows, w, p), lambda: moe.expert_linear_grad(rows[:, :N], rows, w, p),
+        lambda: moe.expert_linear_grad(z[:, :N].contiguous(), None, None, p, need=(False, True)),
+        lambda: moe.expert_linear_grad(z[:, :N].contiguous(), rows, None, p),
+        lambda: moe.glu(z, act="tanh"), lambda: moe.glu(z[:, :255].contiguous()), lambda: moe.glu(x, p=p),
+        lambda: moe.glu_grad(rows, z), lambda: moe.glu_grad(z[:, :N].contiguous(), z.to(U8)),
+    ]
+    for i, call in enumerate(wrong):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was taken")
+    refused = [
+        (lambda: moe.sort_rows(off, p), moe.MOE_EINVAL), (lambda: moe.return_rows_grad(x, None, p), moe.MOE_EINVAL),
+        (lambda: moe.return_rows_grad(x, rows, p, need=(False, False)), moe.MOE_EINVAL),
+        (lambda: moe.expert_linear_grad(z[:, :N].contiguous(), None, w, p), moe.MOE_EINVAL),
+        (lambda: moe.glu(z[:, :N].contiguous()), moe.MOE_EUNSUPPORTED),
+        (lambda: moe.expert_linear(rows, w[:, :100].contiguous(), p), moe.MOE_EUNSUPPORTED),
+        (lambda: moe.expert_linear_grad(z[:, :N].contiguous(), rows, w, p, ws=torch.empty(16, dtype=U8, device=dev)),
+         moe.MOE_EWORKSPACE),
+    ]
+    for i, (call, code) in enumerate(refused):
+        with pytest.raises(moe.MoEError) as e:
+            call()
+        assert e.value.code == code, i
+
+
 def test_glu_far_out(dev):
     """Gates far out on both sides, blocks of tiny and of huge values."""
     g = torch.cat([torch.linspace(-300, 300, 120), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 88.0, -88.0, 104.0, -104.0])])
