@@ -27,7 +27,7 @@
 // the full tiles alone 1.92 ms at 1.23 PFLOP/s, the others 0.98 ms at 5.1 TB/s of weights,
 // and the two hardly overlap: a CU holds two steps in LDS, too few to hide a loaded HBM.
 // MFMAs are busy 63 % of the time at the 1.75 GHz that the power leaves. dx of 64238 rows 1.08
-// ms (4.8 TB/s), dw 1.35 ms: bound by reading (writing) 4.2 GB of weights; three steps
+// ms (4.8 TB/s), dw 1.31 ms: bound by reading (writing) 4.2 GB of weights; three steps
 // of the contraction per tile of dw, then 128 KB of stores that the copies queue behind.
 #include "experts.h"
 #include "linear_stage.h"
@@ -347,14 +347,18 @@ __global__ __launch_bounds__(kThreads, 1) void k_expert_tile(ExpertArgs a) {
   wait_vmcnt<0>();   // no copy may be in flight when the workgroup's LDS is given away
 }
 
-// Every expert's tiles are split over the XCDs in runs of one column tile after another.
+// Every expert's tiles, in the same order (kGroup tiles of its N, column tile, tile of N),
+// are split over four XCDs in runs, over eight where there are fewer than eight experts:
+// enough for one expert of many rows, and a run still shares its operands' rows. Four and
+// eight, in us: 384 experts, 768 x 7168, of 704 rows each 3014 and 3149, of a 32K chunk's 47 to
+// 30133 rows 3613 and 3929 (two: 4107), 64 experts of up to 3418 rows, 1024 x 2048 293 and 300.
 template <int FT, int FW, bool F32>
 __global__ __launch_bounds__(kThreads, 1) void k_expert_wgrad(ExpertGradArgs a) {
   typedef Stream<FT, FW, true, true, F32> S;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kSmem];
   const int m_tiles = (a.N + 32 * FT - 1) / (32 * FT), n_tiles = (a.C + 32 * FW - 1) / (32 * FW);
   const int tiles = m_tiles * n_tiles, per = tiles * a.splits;   // of an expert
-  const int parts = min(kXcds, per), len = (per + parts - 1) / parts;
+  const int parts = min(a.E < kXcds ? kXcds : kXcds / 2, per), len = (per + parts - 1) / parts;
   const int xcd = blockIdx.x % kXcds, stride = gridDim.x / kXcds;
   const int end = len * ((a.E * parts - xcd + kXcds - 1) / kXcds);   // this XCD's parts
   const const_ints off = as_const(a.off), order = as_const(a.order);
@@ -368,11 +372,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_expert_wgrad(ExpertGradArgs a) 
     const int run = uniform_div(i, len), part = run * kXcds + xcd, at = uniform_div(part, parts);
     const int k = (part - at * parts) * len + i - run * len;
     if (i >= end || k >= per) return Tile{-1, 0, 0, 0, 0, 0, 0};
-    const int e = order[at], split = uniform_div(k, tiles), t = k - split * tiles, nt = uniform_div(t, m_tiles);
+    const int e = order[at], split = uniform_div(k, tiles), t = k - split * tiles;
+    const int group = uniform_div(t, kGroup * n_tiles), in = t - group * kGroup * n_tiles;
+    const int in_group = min(kGroup, m_tiles - group * kGroup), nt = uniform_div(in, in_group);
+    const int mt = group * kGroup + in - nt * in_group;
     const int lo = min(max(off[e], 0), a.P), hi = min(max(off[e + 1], lo), a.P);
     const int steps = (hi - lo + 63) / 64;
     const int s0 = uniform_div(steps * split, a.splits), s1 = uniform_div(steps * (split + 1), a.splits);
-    return Tile{e, (t - nt * m_tiles) * 32 * FT, nt * 32 * FW, lo + 64 * s0, min(hi, lo + 64 * s1), max(s1 - s0, 1),
+    return Tile{e, mt * 32 * FT, nt * 32 * FW, lo + 64 * s0, min(hi, lo + 64 * s1), max(s1 - s0, 1),
                 split};
   };
   int id = blockIdx.x / kXcds;
