@@ -16,6 +16,8 @@
 #include "rows.h"
 #include "linear.h"
 
+#include <float.h>
+
 namespace moe {
 namespace {
 
@@ -90,9 +92,16 @@ __global__ __launch_bounds__(kGluThreads) void k_glu_grad(GluArgs a) {
     unpack8(load16_nt(a.z + gate), g);
     unpack8(load16_nt(a.z + up), u);
   }
-  float dg[8], du[8];
+  float dg[8], du[8], most = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dg[i] = d[i] * u[i] * activate_slope(g[i], a.act);
+  for (int i = 0; i < 8; ++i) {
+    dg[i] = d[i] * u[i];
+    most = fmaxf(most, fabsf(dg[i]));
+    dg[i] *= activate_slope(g[i], a.act);
+  }
+  // dh u leaves fp32 where a gate's tail may take it back (relu: to zero): the slope first
+  if (most > FLT_MAX)
+    for (int i = 0; i < 8; ++i) dg[i] = fabsf(d[i] * u[i]) > FLT_MAX ? d[i] * activate_slope(g[i], a.act) * u[i] : dg[i];
   activate(g, a.act);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
