@@ -532,6 +532,8 @@ int moe_glu(const moe_glu_dims* dims, const uint16_t* z, const int32_t* expert_o
 
 /* Its gradient, at the values that the codes stand for, or at z itself:
  *   dz = (dh u act'(g), dh act(g))
+ * What fp32 cannot hold on the way (dh u, a code's 2^128) does not make a result infinite or
+ * NaN that bf16 can hold.
  *   dh        [R, I] bf16
  *   z         [R, 2I] bf16, or NULL with z_q and z_s from moe_glu (one of the two)
  *   dz        [R, 2I] bf16 out; may be z

@@ -85,9 +85,12 @@ __global__ __launch_bounds__(kGluThreads) void k_glu_grad(GluArgs a) {
   const int64_t gate = p.row * 2 * a.I + p.col, up = gate + a.I, at = p.row * a.I + p.col;
   float g[8], u[8], d[8];
   unpack8(load16_nt(a.dh + at), d);
+  int scale = 0;
   if constexpr (CODES) {
-    decode8(*reinterpret_cast<const uint2*>(a.z_q + gate), (int)a.z_s[gate / 128] - 127, g);
-    decode8(*reinterpret_cast<const uint2*>(a.z_q + up), (int)a.z_s[up / 128] - 127, u);
+    const int eg = a.z_s[gate / 128], eu = a.z_s[up / 128];
+    decode8(*reinterpret_cast<const uint2*>(a.z_q + gate), eg - 127, g);
+    decode8(*reinterpret_cast<const uint2*>(a.z_q + up), eu - 127, u);
+    scale = max(eg, eu);
   } else {
     unpack8(load16_nt(a.z + gate), g);
     unpack8(load16_nt(a.z + up), u);
@@ -99,9 +102,18 @@ __global__ __launch_bounds__(kGluThreads) void k_glu_grad(GluArgs a) {
     most = fmaxf(most, fabsf(dg[i]));
     dg[i] *= activate_slope(g[i], a.act);
   }
-  // dh u leaves fp32 where a gate's tail may take it back (relu: to zero): the slope first
-  if (most > FLT_MAX)
-    for (int i = 0; i < 8; ++i) dg[i] = fabsf(d[i] * u[i]) > FLT_MAX ? d[i] * activate_slope(g[i], a.act) * u[i] : dg[i];
+  // What leaves fp32 on the way: dh u, where a gate's tail may take it back (relu: to zero), so
+  // that the slope comes first; and 2^128, the code 256 under the largest scale of a finite
+  // block, 2^120 (bf16 values from 1.9375 2^127 on), for which fp32's largest value stands.
+  if (most > FLT_MAX || scale >= 120 + 127)
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (CODES) {   // an infinity of z itself stays one
+        g[i] = fabsf(g[i]) > FLT_MAX ? copysignf(FLT_MAX, g[i]) : g[i];
+        u[i] = fabsf(u[i]) > FLT_MAX ? copysignf(FLT_MAX, u[i]) : u[i];
+      }
+      const float p = d[i] * u[i], slope = activate_slope(g[i], a.act);
+      dg[i] = fabsf(p) > FLT_MAX ? d[i] * slope * u[i] : p * slope;
+    }
   activate(g, a.act);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

@@ -1,5 +1,6 @@
 """GPU tests of the operators that train the experts at their edges: gradients of the gated
-activation where the product of two factors leaves fp32 and the third brings it back."""
+activation where the product of two factors leaves fp32 and the third brings it back, and
+where codes stand for more than fp32 holds."""
 
 import pytest
 import torch
@@ -7,7 +8,7 @@ import torch
 import mxfp4_weights_fp8_amd as moe
 from gpu_helpers import say
 from oracle import train as ot
-from test_gpu_train import BF, BF16, F64, U, dev, on  # noqa: F401
+from test_gpu_train import ACTS, BF, BF16, F64, U, check_saved, dev, on  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,32 @@ def test_glu_grad_where_dh_times_u_leaves_fp32(dev, act, R, I):
         assert bool((dz == dz[:1]).all()), what          # the rows are alike, and no NaN
         off = (dz[:1, :I].cpu().to(F64) - want).abs()
         assert bool((off <= tol).all()), what
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("R,I", [(2, 128), (700, 12288)])
+def test_glu_grad_of_codes_at_the_top(dev, act, R, I):
+    """Values from 1.9375 2^127 on are finite in bf16, and their codes stand for 2^128: the
+    gradient at 2^128, where it is a number, is that number."""
+    top = 2.0 ** 127
+    z, dh = torch.zeros(R, 2 * I), torch.zeros(R, I)
+    z[0, :128] = top * torch.tensor([1.9921875, -1.9921875, 1.9375, -1.9375, 1.90625, -1.875, 1.0, 0.0]).repeat(16)
+    z[0, I:I + 128] = 2.0 ** -100
+    z[1, :128] = torch.tensor([-64.0, 0.0, -8.0, -10.0]).repeat(32)
+    z[1, I:I + 128] = top * torch.tensor([1.9921875, -1.9375, 1.25, -1.9921875, 1.9375]).repeat(26)[:128]
+    dh[:, :128] = 2.0 ** -20 * torch.tensor([1.0, 1.5, -1.0, 1.0, -1.75]).repeat(26)[:128]
+    z, dh = z.to(BF16), dh.to(BF16)
+    assert bool(torch.isfinite(z).all())
+    zd, dhd = on(dev, z, dh)
+    _, q, s = moe.glu(zd, act=act)
+    check_saved(z[:2], q[:2], s[:2], "top")
+    val = ot.restored_ref(q[:2].cpu(), s[:2].cpu())
+    assert float(val.max()) == 2.0 ** 128 and float(val.min()) == -2.0 ** 128
+    say(f"[glu_grad of codes at the top {R}x{I} {act}]")
+    dz, h = moe.glu_grad(dhd, q, scales=s, act=act)
+    for got, want in zip((dz, h), ot.glu_grad_ref(dh[:2], val, act)):
+        got = got[:2].cpu().to(F64)
+        past = want.abs() >= 2.0 ** 128
+        assert torch.equal(got[past], torch.copysign(torch.full_like(want, float("inf")), want)[past])
+        # as above; 2^128 itself is taken as fp32's largest value, off by U
+        assert bool(((got - want).abs() <= want.abs() * (BF + 2 ** 9 * U) + 1e-37)[~past].all())
