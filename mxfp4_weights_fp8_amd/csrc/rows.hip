@@ -95,7 +95,11 @@ struct ReturnArgs {
   int T, H, K;
 };
 
-constexpr int kPicks = 8;   // rows on their way at once
+// Rows on their way at once. Only rows that there are are read, each under its own condition
+// where a wave lacks one (which all the time costs 1 % of top-8). That, and row 0 in place of a
+// missing one: 10595 x 11816 fp32, top-1 153 and 236 us, 22216 x 576, top-1 16 and 28, 32768 x 7168,
+// top-2 248 and 342, 16384 x 7168, top-9 393 and 448; 32768 x 7168, top-8 720 and 719.
+constexpr int kPicks = 8;
 
 template <bool F32, bool NT>
 __global__ __launch_bounds__(kRowThreads) void k_return_rows(ReturnArgs a) {
@@ -106,15 +110,25 @@ __global__ __launch_bounds__(kRowThreads) void k_return_rows(ReturnArgs a) {
   float acc[8] = {};
   for (int j0 = 0; j0 < a.K; j0 += kPicks) {
     v4i v[kPicks];
+    uint32_t r[kPicks];
     float w[kPicks];
-    bool ok[kPicks];
+    bool ok[kPicks], whole = true;
 #pragma unroll
     for (int u = 0; u < kPicks; ++u) {
       const int64_t pair = p.t * a.K + min(j0 + u, a.K - 1);
-      const uint32_t r = (uint32_t)a.pair_rows[pair];
-      ok[u] = j0 + u < a.K && r < a.P;
+      r[u] = (uint32_t)a.pair_rows[pair];
       w[u] = a.w ? a.w[pair] : 1.f;
-      v[u] = load16_nt(a.rows + (int64_t)(ok[u] ? r : 0) * a.H + 8 * p.c8);   // row 0 is there: T K > 0
+      ok[u] = j0 + u < a.K && r[u] < a.P;
+    }
+#pragma unroll
+    for (int u = 0; u < kPicks; ++u) whole &= ok[u];
+    if (__all(whole)) {
+#pragma unroll
+      for (int u = 0; u < kPicks; ++u) v[u] = load16_nt(a.rows + (int64_t)r[u] * a.H + 8 * p.c8);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kPicks; ++u)
+        if (ok[u]) v[u] = load16_nt(a.rows + (int64_t)r[u] * a.H + 8 * p.c8);
     }
 #pragma unroll
     for (int u = 0; u < kPicks; ++u)

@@ -1,6 +1,6 @@
-"""GPU tests of the operators that train the experts at their edges: gradients of the gated
-activation where the product of two factors leaves fp32 and the third brings it back, and
-where codes stand for more than fp32 holds."""
+"""GPU tests of the operators that train the experts at their edges: rows of every number of
+picks, gradients of the gated activation where the product of two factors leaves fp32 and
+the third brings it back, and where codes stand for more than fp32 holds."""
 
 import pytest
 import torch
@@ -8,9 +8,40 @@ import torch
 import mxfp4_weights_fp8_amd as moe
 from gpu_helpers import say
 from oracle import train as ot
-from test_gpu_train import ACTS, BF, BF16, F64, U, check_saved, dev, on  # noqa: F401
+from test_gpu_train import ACTS, BF, BF16, F32, F64, U, check_saved, dev, on, randn, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("K", list(range(1, 18)) + [63, 64])
+@pytest.mark.parametrize("H", [72, 1032])      # waves of several tokens, and of one
+def test_return_rows_of_every_number_of_picks(dev, K, H):
+    """Tokens with all, some and none of their picks; rows of nobody, and a first row that is
+    somebody else's NaN, stay out of them."""
+    T, E = 37, 5
+    g = torch.Generator().manual_seed(K)
+    ids = torch.randint(0, E, (T, K), generator=g, dtype=torch.int32)
+    ids[torch.rand(T, K, generator=g) < 0.3] = -1
+    ids[4:9], ids[20], ids[36] = -1, 1, 2
+    ids[11] = -1
+    ids[11, K - 1] = 0
+    p = moe.plan(ids.to(dev), E, 128, 128)
+    pr, live = p.pair_rows.cpu(), int(p.expert_offsets[-1])
+    rows, w = randn(T * K, H, seed=1, dtype=BF16), randn(T, K, seed=2)
+    rows[live:] = float("nan")
+    first = int((pr[:T * K] == 0).nonzero()) // K         # the token that has row 0
+    w[(ids < 0)] = float("nan")                           # weights of dropped picks
+    say(f"[return_rows {T}x{K}, {H}]")
+    for dtype, out in ((BF16, BF), (F32, U)):
+        add = randn(T, H, seed=3, dtype=dtype)
+        want, mag = ot.return_rows_ref(rows, pr, T, K, w, add)
+        y = moe.return_rows(rows.to(dev), p, weights=w.to(dev), add=add.to(dev), dtype=dtype)
+        within(y, want, want.abs() * out + mag * (K + 2) * U, "y")
+        bad = rows.clone()
+        bad[0] = float("nan")
+        y2 = moe.return_rows(bad.to(dev), p, weights=w.to(dev), add=add.to(dev), dtype=dtype)
+        rest = torch.arange(T) != first
+        assert torch.equal(y2.cpu()[rest], y.cpu()[rest]) and bool(torch.isnan(y2[first]).all())
 
 
 # Gates whose slope takes 2^134 back into range; each a value that its E4M3 code holds exactly.
