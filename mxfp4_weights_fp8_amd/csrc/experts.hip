@@ -68,10 +68,10 @@ __device__ __forceinline__ Unit find_unit(const int32_t* off, int E, int P, int 
 // of the contraction straight from memory into registers, kDepth steps' loads at a time,
 // and add their sums through LDS in wave order. FT: 16-row fragments.
 //
-// 56 rows of 30 experts, 768 x 7168 (330 MB of weights) 74 us, 4.5 TB/s. Eight workgroups of
-// four waves share a CU, so that one looks up its rows or adds its sums while others load:
-// with eight waves each 78 us, with sixteen 88 us. A row's 128 bytes come by two loads of 64;
-// with the nontemporal hint, which lets go of the line between them, 101 us.
+// 56 rows of 30 experts, 768 x 7168 (330 MB of weights) 74 us, 4.5 TB/s. The registers (94 per
+// lane) leave room for five waves per SIMD: five workgroups of four waves share a CU, two of
+// eight (78 us) or one of sixteen (88 us). A row's 128 bytes come by two loads of 64; with the
+// nontemporal hint, which lets go of the line between them, 101 us.
 constexpr int kFewWaves = 4;
 
 template <int FT, bool F32>
@@ -147,7 +147,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_expert_few(ExpertArgs a) {
 // against 2734).
 // order: the experts by their number of rows, the most first (in classes of a quarter of
 // an octave; within one by index).
-constexpr int kListPer = 4;     // experts per thread: 256 threads up to 1024 experts (2.4 us, 1024 threads 3.9)
+// With 256 and 1024 threads, in us: 384 experts of one tile each right behind a product of theirs
+// 3.4 and 4.3, behind other work 4.8 and 4.8, with the order 5.3 and 7.4; of three tiles each
+// 6.7-7.3 and 5.7-6.3, with the order 8.7 and 8.8. (1024 threads for 4096 experts: 7, with the order 11.5.)
+constexpr int kListPer = 4;     // experts per thread: 256 threads up to 1024 experts
 constexpr int kClasses = 128;
 constexpr int kTogether = 8;    // column tiles
 

@@ -8,8 +8,8 @@
 // Everything between load and store is fp32, each output is rounded once. HBM-bound: 16
 // lanes own 128 gate columns and the 128 up columns of the same h, 8 each per lane, so a
 // block's amax is a 16-lane butterfly. 262144 x 384: 147 us (5.5 TB/s), the gradient from
-// codes 200 us (4.9 TB/s); 128 x 512 3.3 us, bound by the launch. Rows from *live on (the
-// plan's last offset) are neither read nor written.
+// codes 200 us (4.9 TB/s); with gelu 189 and 312 us, bound by erfcf; 128 x 512 3.3 us, bound by
+// the launch. Rows from *live on (the plan's last offset) are neither read nor written.
 #include "device_common.h"
 #include "host_internal.h"
 #include "lane_reduce.h"
