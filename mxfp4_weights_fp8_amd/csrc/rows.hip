@@ -95,10 +95,11 @@ struct ReturnArgs {
   int T, H, K;
 };
 
-// Rows on their way at once. Only rows that there are are read, each under its own condition
-// where a wave lacks one (which all the time costs 1 % of top-8). That, and row 0 in place of a
-// missing one: 10595 x 11816 fp32, top-1 153 and 236 us, 22216 x 576, top-1 16 and 28, 32768 x 7168,
-// top-2 248 and 342, 16384 x 7168, top-9 393 and 448; 32768 x 7168, top-8 720 and 719.
+// Rows on their way at once. A missing row is not read: in a wave that lacks one every load
+// has its own condition (in all waves, that costs top-8 1 %). Conditions, and row 0 read in
+// place of a missing one, in us: 10595 x 11816 fp32, top-1 153 and 236; 22216 x 576, top-1 16 and
+// 28; 32768 x 7168, top-2 248 and 342; 16384 x 7168, top-9 393 and 448; 32768 x 7168, top-8 720
+// and 719.
 constexpr int kPicks = 8;
 
 template <bool F32, bool NT>
